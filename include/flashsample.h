@@ -331,6 +331,129 @@ FS_API fs_status fs_sample_noalloc(const void* h, const void* W, int64_t B, int6
                                    const float* temp, uint64_t seed, uint64_t step,
                                    int64_t* out_ids, float* out_max, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Learning from sampled tokens: their log-probabilities through the LM head
+ * with gradients, the clipped policy loss, and clipping by the global
+ * gradient norm.  Same conventions as above (shapes, alignment, streams,
+ * errors).  These calls take their workspace from the caller (16-byte
+ * aligned device memory whose contents need not survive the call), apart
+ * from a fixed 64 KB block per (device, stream) that the library allocates on
+ * the first call; that block is part of fs_workspace_reserve(), which makes
+ * them capturable.
+ *
+ * A row t takes part ("is scored") when 0 <= ids[t] < V and its temperature
+ * is valid.  T > 0 divides the logits; T == 0 scores under softmax(logits),
+ * the logits being what greedy sampling compares; T < 0 or NaN: the row is
+ * not scored.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Log-probabilities of given tokens, fused into the LM-head matmul: with
+ *   x[t, v] = (sum_k h[t, k] W[v, k] + bias[t, v]) / T[t]
+ *   lse[t]  = log sum_v exp x[t, v],   logp[t] = x[t, ids[t]] - lse[t].
+ *   h [n, d] bf16, W [V, d] bf16, ids [n] int64, temp [n] fp32, bias as in
+ *   fs_sample_ex; logp [n], lse [n] fp32: outputs.
+ * A row that is not scored gets logp 0 (its lse is still written; -inf where
+ * the temperature is invalid).  A row whose every x is -inf has lse -inf; a
+ * token at x = -inf has logp -inf.  A logit that is NaN or +inf gives NaN for
+ * its row, and for no other.
+ *   kept (nullable): fp32 [fs_logprob_buffer_elems(n, V)] where the call
+ *     leaves the logits for fs_token_logprobs_backward, 16-byte aligned.
+ *     Without it the n x V logits never reach device memory.
+ *   workspace: fs_token_logprobs_workspace_bytes(n, d, V) bytes.
+ */
+FS_API fs_status fs_token_logprobs(const void* h, const void* W, int64_t n, int64_t d, int64_t V,
+                                   const int64_t* ids, const float* temp, const float* bias,
+                                   int64_t bias_row_stride, float* logp, float* lse, float* kept,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
+FS_API size_t fs_token_logprobs_workspace_bytes(int64_t n, int64_t d, int64_t V);
+
+/* Elements of the `kept` buffer for n rows and V vocabulary rows (rows are
+ * padded to a multiple of 64 elements). */
+FS_API int64_t fs_logprob_buffer_elems(int64_t n, int64_t V);
+
+/*
+ * Backward pass of fs_token_logprobs: given g[t] = dL/dlogp[t] (fp32 [n]),
+ *   ds[t, v] = g[t] / T[t] (1[v = ids[t]] - exp(x[t, v] - lse[t]))
+ *   grad_h = ds W  (bf16 [n, d]),   grad_W = ds^T h  (bf16 [V, d]);
+ * either output may be NULL.  logp and lse are the forward call's; kept is
+ * its buffer, or NULL to form the logits again from h, W and bias.
+ * Rows that are not scored, have g == 0, lse == -inf or logp == -inf carry no
+ * gradient: their grad_h is zero and their h may hold anything.
+ * Products take ds rounded to bf16 and accumulate in fp32.
+ *   workspace: fs_token_logprobs_backward_workspace_bytes(n, d, V) bytes.
+ */
+FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, int64_t d, int64_t V,
+                                            const int64_t* ids, const float* temp, const float* bias,
+                                            int64_t bias_row_stride, const float* logp, const float* lse,
+                                            const float* grad_logp, const float* kept, void* grad_h, void* grad_W,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+FS_API size_t fs_token_logprobs_backward_workspace_bytes(int64_t n, int64_t d, int64_t V);
+
+/* How fs_policy_loss weighs tokens (those that the mask leaves). */
+#define FS_MEAN_TOKEN 0       /* the mean over all tokens */
+#define FS_MEAN_SEQUENCE 1    /* the mean over sequences of each one's mean; sequences without tokens do not count */
+#define FS_MEAN_NONE 2        /* the sum over all tokens */
+
+/*
+ * Clipped policy loss with a KL penalty, and its gradient, in one call.  For
+ * each token i of advantage A, with r = exp(logp - old_logp), q = ref_logp -
+ * logp and weight w (from `mean`):
+ *   loss = sum w (-min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (e^q - 1 - q))
+ *   grad[i] = dloss/dlogp[i] = w (-r A [not clipped] + kl_coef (1 - e^q)).
+ * A token is clipped when A > 0 and logp - old_logp > log(1 + clip_high), or
+ * A < 0 and logp - old_logp < log(1 - clip_low), compared exactly.
+ *   logp, old_logp, ref_logp (nullable: no KL term) fp32 [N].
+ *   Sequences: seq_starts (device int64 [n_seqs + 1], non-decreasing from 0
+ *     to N; empty sequences allowed) for packed tokens, or NULL for n_seqs
+ *     rows of N / n_seqs tokens.
+ *   advantages: fp32 [N], or [n_seqs] when adv_per_seq is 1.
+ *   mask (nullable): one byte per token, 0 = takes no part: its inputs may
+ *     hold anything and its gradient is 0.
+ *   stats [4] fp32: loss, its policy term, its KL term (before kl_coef) and
+ *     the weighted share of clipped tokens; grad [N] fp32.  All zero when no
+ *     token takes part.
+ *   0 <= clip_low < 1, clip_high >= 0, kl_coef finite (0 without ref_logp).
+ *   workspace: fs_policy_loss_workspace_bytes(n_seqs) bytes.
+ * Sums are held in fp64; the results do not depend on the run.
+ */
+FS_API fs_status fs_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,
+                                const float* advantages, int adv_per_seq, const uint8_t* mask,
+                                const int64_t* seq_starts, int64_t n_seqs, int64_t N, double clip_low,
+                                double clip_high, double kl_coef, int mean, float* stats, float* grad,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+FS_API size_t fs_policy_loss_workspace_bytes(int64_t n_seqs);
+
+/* Element types of fs_clip_grad_norm's tensors, and its norms. */
+#define FS_TYPE_F32 0
+#define FS_TYPE_BF16 1
+#define FS_TYPE_F16 2
+#define FS_NORM_L2 0
+#define FS_NORM_MAX 1
+
+/*
+ * The norm of n_tensors gradients taken as one vector, and their scaling by
+ * min(1, max_norm / (norm + 1e-6)).
+ *   grads, sizes, types: host arrays [n_tensors] of device pointers, element
+ *     counts and FS_TYPE_*; types may differ, sizes may be 0.
+ *   outs: host array of device pointers for the scaled gradients (each its
+ *     gradient's own pointer, or memory that overlaps no gradient), or NULL
+ *     for the norm alone.
+ *   max_norm >= 0; +inf never scales.  norm (device fp32 [1]): the norm
+ *     before scaling.
+ * The scaled values are formed in fp32 and rounded once.  A norm that is not
+ * finite (a NaN or an infinity among the gradients, or a square above the
+ * fp32 range) is reported and scales nothing.  Squares are summed in fp32
+ * over 64 elements, then in fp64, in an order that does not depend on the
+ * run.
+ */
+FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes,
+                                   const int* types, int n_tensors, double max_norm, int norm_type, float* norm,
+                                   void* stream);
+
 /* Workspace bytes one call with (B, V) needs on the current device. */
 FS_API size_t fs_workspace_bytes(int64_t B, int64_t V);
 

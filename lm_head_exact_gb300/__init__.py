@@ -8,6 +8,7 @@ is no CPU fallback.
 """
 
 __all__ = ["sample", "sample_ex", "sample_chunked", "sample_unfused", "sample_host",
+           "token_logprobs", "token_logprobs_backward", "logprob_buffer", "policy_loss", "clip_grad_norm",
            "FlashSampleError", "library"]
 
 

@@ -20,6 +20,9 @@ FS_CHUNK_LAST = 2
 FS_CHUNK_SERIAL = 4
 FS_PATH_AUTO, FS_PATH_SIMT, FS_PATH_TC_VOCAB, FS_PATH_TC_BATCH, FS_PATH_TC_PAIR = 0, 1, 2, 3, 4
 FS_FAULT_NONE, FS_FAULT_ALLOC, FS_FAULT_LAUNCH = 0, 1, 2
+FS_MEAN_TOKEN, FS_MEAN_SEQUENCE, FS_MEAN_NONE = 0, 1, 2
+FS_TYPE_F32, FS_TYPE_BF16, FS_TYPE_F16 = 0, 1, 2
+FS_NORM_L2, FS_NORM_MAX = 0, 1
 
 _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -66,6 +69,20 @@ SIGNATURES = {
     "fs_debug_set_fault": (_int, [_int]),
     "fs_status_string": (ctypes.c_char_p, [_int]),
     "fs_last_error": (ctypes.c_char_p, []),
+    "fs_token_logprobs": (_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _i64,
+                                 _c_void_p, _c_void_p, _c_void_p, _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "fs_token_logprobs_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "fs_logprob_buffer_elems": (_i64, [_i64, _i64]),
+    "fs_token_logprobs_backward": (_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
+                                          _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                          _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "fs_token_logprobs_backward_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "fs_policy_loss": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _c_void_p, _i64, _i64,
+                              ctypes.c_double, ctypes.c_double, ctypes.c_double, _int, _c_void_p, _c_void_p,
+                              _c_void_p, ctypes.c_size_t, _c_void_p]),
+    "fs_policy_loss_workspace_bytes": (ctypes.c_size_t, [_i64]),
+    "fs_clip_grad_norm": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _int, ctypes.c_double, _int, _c_void_p,
+                                 _c_void_p]),
     "fs_debug_noise": (_int, [_u64, _u64, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p]),
     "fs_debug_fused_logits": (_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _i64,
                                      _u64, _u64, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
@@ -400,6 +417,192 @@ def sample_host(h_host, W, temp_host, seed, step, bias=None, out_ids=None, out_m
                                    seed, step, host_ptr(out_ids, "out_ids"),
                                    host_ptr(out_max, "out_max"), _stream_ptr(stream)))
     return out_ids, out_max
+
+
+# ---------------------------------------------------------------- learning from sampled tokens
+def _arg(t, name, dtype=None, shape=None):
+    """Address of a contiguous CUDA tensor of this type and shape."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be a CUDA tensor (no CPU fallback)")
+    if dtype is not None and t.dtype != dtype:
+        raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _head_args(h, W, ids, temp, bias):
+    torch = _torch()
+    if getattr(h, "ndim", 0) != 2 or getattr(W, "ndim", 0) != 2 or h.shape[1] != W.shape[1]:
+        raise FlashSampleError("FS_ERR_INVALID_ARG", "h must be [n, d] and W [V, d]")
+    n, d = h.shape
+    V = W.shape[0]
+    if bias is not None and tuple(bias.shape) not in ((n, V), (V,)):
+        raise FlashSampleError("FS_ERR_INVALID_ARG", f"bias must be [n, V] or [V], got {tuple(bias.shape)}")
+    bptr, bstride = _bias_args(bias, n, V) if bias is not None else (None, 0)
+    return (_arg(h, "h", torch.bfloat16), _arg(W, "W", torch.bfloat16), n, d, V,
+            _arg(ids, "ids", torch.int64, (n,)), _arg(temp, "temp", torch.float32, (n,)), bptr, bstride)
+
+
+def _workspace(nbytes, device, stream):
+    """Device memory for one call, allocated on the stream that the call runs
+    on: it may be handed out again as soon as this returns to the caller, but
+    only to work that follows on that stream."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def logprob_buffer(n, V, device="cuda"):
+    """The fp32 buffer in which ``token_logprobs`` leaves the logits of n rows
+    for ``token_logprobs_backward``."""
+    return _torch().empty(library().fs_logprob_buffer_elems(n, V), dtype=_torch().float32, device=device)
+
+
+def _kept_arg(kept, n, V):
+    torch = _torch()
+    if kept is None:
+        return None
+    if kept.numel() != library().fs_logprob_buffer_elems(n, V):
+        raise FlashSampleError("FS_ERR_INVALID_ARG", "kept must be logprob_buffer(n, V)")
+    return _arg(kept, "kept", torch.float32)
+
+
+def token_logprobs(h, W, ids, temp, bias=None, kept=None, out=None, stream=None):
+    """Log-probabilities of the tokens ``ids`` under softmax((h Wᵀ + bias) /
+    temp), fused into the LM-head matmul.
+
+    h: bf16 [n, d], W: bf16 [V, d], ids: int64 [n] (outside [0, V): the row is
+    not scored, e.g. -1 for padding), temp: fp32 [n], bias: optional fp32
+    [n, V] or [V].  ``kept`` (``logprob_buffer``) keeps the logits for the
+    backward pass; without it they never reach device memory.  Returns
+    (logp fp32 [n], lse fp32 [n])."""
+    torch = _torch()
+    args = _head_args(h, W, ids, temp, bias)
+    n, d, V = args[2:5]
+    if out is None:
+        out = (torch.empty(n, dtype=torch.float32, device=h.device), torch.empty(n, dtype=torch.float32, device=h.device))
+    logp, lse = out
+    lib = library()
+    work = _workspace(lib.fs_token_logprobs_workspace_bytes(n, d, V), h.device, stream)
+    check(lib.fs_token_logprobs(*args, _arg(logp, "logp", torch.float32, (n,)), _arg(lse, "lse", torch.float32, (n,)),
+                                _kept_arg(kept, n, V), work.data_ptr(), work.numel(), _stream_ptr(stream)))
+    return logp, lse
+
+
+def token_logprobs_backward(h, W, ids, temp, logp, lse, grad_logp, bias=None, kept=None, need_h=True, need_W=True,
+                            out=None, stream=None):
+    """Gradients of ``token_logprobs``: from ``grad_logp`` (dL/dlogp, fp32
+    [n]) to (grad_h bf16 [n, d], grad_W bf16 [V, d]); one that is not needed is
+    None.  ``logp``, ``lse`` and ``kept`` are the forward call's (without
+    ``kept`` the logits are formed again).  ``out``: the two tensors to
+    write, where given."""
+    torch = _torch()
+    args = _head_args(h, W, ids, temp, bias)
+    n, d, V = args[2:5]
+    grad_h, grad_W = out if out is not None else (None, None)
+    if need_h and grad_h is None:
+        grad_h = torch.empty_like(h)
+    if need_W and grad_W is None:
+        grad_W = torch.empty_like(W)
+    lib = library()
+    work = _workspace(lib.fs_token_logprobs_backward_workspace_bytes(n, d, V), h.device, stream)
+    check(lib.fs_token_logprobs_backward(
+        *args, _arg(logp, "logp", torch.float32, (n,)), _arg(lse, "lse", torch.float32, (n,)),
+        _arg(grad_logp, "grad_logp", torch.float32, (n,)), _kept_arg(kept, n, V),
+        _arg(grad_h, "grad_h", torch.bfloat16, (n, d)) if need_h else None,
+        _arg(grad_W, "grad_W", torch.bfloat16, (V, d)) if need_W else None,
+        work.data_ptr(), work.numel(), _stream_ptr(stream)))
+    return grad_h if need_h else None, grad_W if need_W else None
+
+
+_MEANS = {"token": FS_MEAN_TOKEN, "sequence": FS_MEAN_SEQUENCE, "none": FS_MEAN_NONE}
+
+
+def policy_loss(logp, old_logp, advantages, seq_starts=None, mask=None, ref_logp=None, clip_low=0.2, clip_high=0.2,
+                kl_coef=0.0, mean="token", adv_per_seq=None, out=None, stream=None):
+    """Clipped policy loss with a KL penalty against ``ref_logp``, and its
+    gradient, in one call.
+
+    ``logp``, ``old_logp`` and ``ref_logp``: fp32, either packed [N] with
+    ``seq_starts`` (int64 [S + 1] on the device, from 0 to N) or padded
+    [S, L]; [N] without ``seq_starts`` is one sequence.  ``advantages``: fp32
+    [S], or one per token in logp's shape (``adv_per_seq`` says which where S
+    = N packed tokens leave it open).  ``mask``: bool in logp's shape,
+    False where a token takes no part.  ``mean``: "token", "sequence" or
+    "none" (the sum).  Returns (stats fp32 [4]: loss, policy term, KL term,
+    share of clipped tokens; grad fp32 in logp's shape = dloss/dlogp)."""
+    torch = _torch()
+    f32 = torch.float32
+    ptr = _arg(logp, "logp", f32)
+    shape = logp.shape
+    if len(shape) not in (1, 2) or (len(shape) == 2 and seq_starts is not None):
+        raise FlashSampleError("FS_ERR_INVALID_ARG", "logp must be [N], with or without seq_starts, or [S, L]")
+    if mean not in _MEANS:
+        raise FlashSampleError("FS_ERR_INVALID_ARG", f"mean must be one of {sorted(_MEANS)}, got {mean!r}")
+    starts = None
+    if seq_starts is not None:
+        starts = _arg(seq_starts, "seq_starts", torch.int64)
+        S = seq_starts.numel() - 1
+        if seq_starts.dim() != 1 or S < 0:
+            raise FlashSampleError("FS_ERR_INVALID_ARG", "seq_starts must be [S + 1]")
+    else:
+        S = shape[0] if len(shape) == 2 else 1
+    N = logp.numel()
+    if adv_per_seq is None:
+        if seq_starts is not None and S == N and advantages.shape == shape:
+            raise FlashSampleError("FS_ERR_INVALID_ARG", "as many sequences as tokens: say adv_per_seq")
+        adv_per_seq = advantages.shape != shape
+    adv = _arg(advantages, "advantages", f32, (S,) if adv_per_seq else shape)
+    if out is None:
+        out = torch.empty(4, dtype=f32, device=logp.device), torch.empty_like(logp)
+    stats, grad = out
+    lib = library()
+    work = _workspace(lib.fs_policy_loss_workspace_bytes(S), logp.device, stream)
+    check(lib.fs_policy_loss(
+        ptr, _arg(old_logp, "old_logp", f32, shape), None if ref_logp is None else _arg(ref_logp, "ref_logp", f32, shape),
+        adv, 1 if adv_per_seq else 0, None if mask is None else _arg(mask, "mask", torch.bool, shape), starts, S, N,
+        clip_low, clip_high, kl_coef, _MEANS[mean], _arg(stats, "stats", f32, (4,)), _arg(grad, "grad", f32, shape),
+        work.data_ptr(), work.numel(), _stream_ptr(stream)))
+    return stats, grad
+
+
+def clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, stream=None):
+    """The norm of ``grads`` taken as one vector (fp32 scalar tensor, before
+    scaling), and their scaling by min(1, max_norm / (norm + 1e-6)): in place,
+    or into the tensors ``out``.  fp32, bf16 and fp16 tensors may be mixed;
+    ``norm_type`` 2 or inf.  A norm that is not finite scales nothing; an
+    infinite ``max_norm`` measures only.  Nothing is synchronized."""
+    torch = _torch()
+    types = {torch.float32: FS_TYPE_F32, torch.bfloat16: FS_TYPE_BF16, torch.float16: FS_TYPE_F16}
+    if norm_type not in (2, float("inf")):
+        raise FlashSampleError("FS_ERR_INVALID_ARG", f"norm_type must be 2 or inf, got {norm_type}")
+    grads = list(grads)
+    n = len(grads)
+    for g in grads:
+        if g.dtype not in types or not g.is_cuda or not g.is_contiguous():
+            raise FlashSampleError("FS_ERR_INVALID_ARG", "gradients must be contiguous fp32, bf16 or fp16 CUDA "
+                                   "tensors (no CPU fallback)")
+    pointers = (_c_void_p * n)(*[g.data_ptr() for g in grads])
+    outs = pointers
+    if out is not None:
+        if len(out) != n:
+            raise FlashSampleError("FS_ERR_INVALID_ARG", f"out must hold {n} tensors, got {len(out)}")
+        for g, o in zip(grads, out):
+            if o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous():
+                raise FlashSampleError("FS_ERR_INVALID_ARG", "an output must be a contiguous CUDA tensor of its "
+                                       "gradient's type and shape")
+        outs = (_c_void_p * n)(*[o.data_ptr() for o in out])
+    norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
+    check(library().fs_clip_grad_norm(pointers, outs, (_i64 * n)(*[g.numel() for g in grads]),
+                                      (_int * n)(*[types[g.dtype] for g in grads]), n, max_norm,
+                                      FS_NORM_L2 if norm_type == 2 else FS_NORM_MAX, norm.data_ptr(),
+                                      _stream_ptr(stream)))
+    return norm
 
 
 def debug_noise(seed, step, row0, n_rows, v0, n_vocab, stream=None):

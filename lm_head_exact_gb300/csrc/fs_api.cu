@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "flashsample.h"
+#include "fs_api_util.h"
 #include "fs_internal.h"
 
 namespace fs {
@@ -87,6 +88,8 @@ struct Workspace {
   size_t host_out_bytes = 0;
   void* topk = nullptr;         // per-(row, CTA group) candidate lists of fs_sample_topk
   size_t topk_bytes = 0;
+  void* train = nullptr;        // tickets and block sums of the training operators (fixed size)
+  size_t train_bytes = 0;
 };
 
 std::mutex g_ws_mutex;
@@ -501,6 +504,55 @@ fs_status sample_chunk(const void* h, const void* W_chunk, int64_t B, int64_t d,
 
 void record_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
 
+// ---------------------------------------------------------------- fs_api_util.h
+void api_begin() { g_last_error[0] = '\0'; }
+
+fs_status api_fail(fs_status s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
+  va_end(ap);
+  return s;
+}
+
+fs_status api_launched(cudaError_t e, const char* what) { return e == cudaSuccess ? FS_OK : cuda_fail(e, what); }
+
+fs_status api_check_array(const void* p, size_t align, const char* name) {
+  FS_TRY(check_device_ptr(p, name));
+  return check_aligned(p, align, name);
+}
+
+fs_status api_check_shapes(int64_t B, int64_t d, int64_t V) { return check_shapes(B, d, V); }
+
+fs_status api_check_launch() {
+  if (injected_fault() == FS_FAULT_LAUNCH)
+    return fail(FS_ERR_CUDA, "training kernel launch failed: injected (FS_FAULT=launch)");
+  return FS_OK;
+}
+
+fs_status api_error_word(int** out, cudaStream_t stream) { return error_word(out, stream); }
+
+fs_status api_train_scratch(cudaStream_t stream, TrainScratch** out) {
+  int dev;
+  FS_TRY(current_device(&dev));
+  std::lock_guard<std::mutex> lock(g_ws_mutex);
+  Workspace& ws = g_workspaces[{dev, stream}];
+  if (ws.train == nullptr) {
+    FS_TRY(grow(&ws.train, &ws.train_bytes, sizeof(TrainScratch), stream));
+    // on the call's stream, which the kernels that use it follow on
+    cudaError_t e = cudaMemsetAsync(ws.train, 0, sizeof(TrainScratch), stream);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      cudaFree(ws.train);
+      ws.train = nullptr;
+      ws.train_bytes = 0;
+      return fail(FS_ERR_WORKSPACE, "zeroing the workspace failed: %s", cudaGetErrorString(e));
+    }
+  }
+  *out = static_cast<TrainScratch*>(ws.train);
+  return FS_OK;
+}
+
 }  // namespace fs
 
 using namespace fs;
@@ -911,6 +963,8 @@ fs_status fs_workspace_reserve(int64_t B, int64_t V, void* stream) {
   if (B < 0 || V < 0) return fail(FS_ERR_INVALID_ARG, "need B >= 0 and V >= 0");
   int* err = nullptr;
   FS_TRY(error_word(&err, static_cast<cudaStream_t>(stream)));   // once per device, never during capture
+  TrainScratch* scratch = nullptr;
+  FS_TRY(api_train_scratch(static_cast<cudaStream_t>(stream), &scratch));
   Finish f{};
   return get_finish(static_cast<cudaStream_t>(stream), B, &f);
 }
@@ -927,6 +981,7 @@ fs_status fs_workspace_release(void) {
       if (it->second.host_out) cudaFreeHost(it->second.host_out);
       if (it->second.staging) cudaFree(it->second.staging);
       if (it->second.topk) cudaFree(it->second.topk);
+      if (it->second.train) cudaFree(it->second.train);
       it = g_workspaces.erase(it);
     } else {
       ++it;

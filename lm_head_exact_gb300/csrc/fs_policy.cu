@@ -1,0 +1,303 @@
+// Clipped policy loss with a KL penalty: the loss, its terms and its gradient
+// with respect to the log-probabilities, in one pass over the tokens.
+//
+//   r = exp(logp - old), q = ref - logp, weight w of the token
+//   loss += w (-min(r A, clip(r) A) + kl (e^q - 1 - q)),
+//   grad  = w (-r A [not clipped] + kl (1 - e^q)).
+//
+// Each token is read once and its gradient written once (12 to 17 bytes in, 4
+// out).  The weights need the number of tokens that take part: with a mask or
+// a mean over sequences a counting launch goes first, which reads the mask
+// only (one byte a token).
+#include <algorithm>
+
+#include "fs_train.h"
+
+namespace fs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCountThreads = 512;
+
+__device__ __forceinline__ int bytes_set(uint32_t w) {
+  return __popc(__vcmpne4(w, 0u) & 0x01010101u);
+}
+
+// Bytes that are not zero in mask[lo, hi), over the block's threads (each
+// returns its own share).
+__device__ long long count_range(const uint8_t* mask, int64_t lo, int64_t hi, int tid, int threads) {
+  long long c = 0;
+  const int64_t a = min(hi, lo + static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(mask + lo) & 15)) & 15));
+  const int64_t b = a + (hi - a) / 16 * 16;
+  for (int64_t i = lo + tid; i < a; i += threads) c += mask[i] != 0;
+  for (int64_t i = a + static_cast<int64_t>(tid) * 16; i < b; i += static_cast<int64_t>(threads) * 16) {
+    const uint4 w = *reinterpret_cast<const uint4*>(mask + i);
+    c += bytes_set(w.x) + bytes_set(w.y) + bytes_set(w.z) + bytes_set(w.w);
+  }
+  for (int64_t i = b + tid; i < hi; i += threads) c += mask[i] != 0;
+  return c;
+}
+
+template <int kBlock>
+__device__ long long block_sum(long long v) {
+  __shared__ long long part[kBlock / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+  for (int i = 0; i < kBlock / 32; ++i) v += part[i];
+  __syncthreads();
+  return v;
+}
+
+// Tokens that take part: of each sequence (a block each) and the number of
+// sequences that have any, or of the whole batch.  Whole numbers, so the order
+// of the atomic additions does not matter.
+__global__ void __launch_bounds__(kCountThreads) policy_count_kernel(const PolicyProblem p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  if (p.mean == FS_MEAN_SEQUENCE) {
+    for (int64_t s = blockIdx.x; s < p.n_seqs; s += gridDim.x) {
+      int64_t lo = p.starts != nullptr ? p.starts[s] : s * p.row_len;
+      int64_t hi = p.starts != nullptr ? p.starts[s + 1] : lo + p.row_len;
+      lo = max(static_cast<int64_t>(0), min(lo, p.N));        // no read outside whatever the offsets hold
+      hi = max(lo, min(hi, p.N));
+      const long long c = p.mask == nullptr
+                              ? hi - lo
+                              : block_sum<kCountThreads>(count_range(p.mask, lo, hi, threadIdx.x, kCountThreads));
+      if (threadIdx.x == 0) {
+        p.counts[s] = static_cast<int>(min(c, static_cast<long long>(0x7fffffff)));
+        if (c > 0) atomicAdd(&p.scratch->count, 1ull);
+      }
+    }
+  } else {
+    const int64_t per = ((p.N + gridDim.x - 1) / gridDim.x + 15) / 16 * 16;
+    const int64_t lo = min(p.N, static_cast<int64_t>(blockIdx.x) * per), hi = min(p.N, lo + per);
+    const long long c = block_sum<kCountThreads>(count_range(p.mask, lo, hi, threadIdx.x, kCountThreads));
+    if (threadIdx.x == 0 && c > 0) atomicAdd(&p.scratch->count, static_cast<unsigned long long>(c));
+  }
+}
+
+// e^q - 1 - q.  For small q the difference loses what it is made of (q =
+// 0.01: 5e-5 of two terms near 0.01), so it is summed from its Taylor series
+// there: the first term left out, q^10 / 10!, is below 2^-27 of q^2 / 2 for
+// |q| <= 1/2.
+__device__ __forceinline__ float kl_estimate(float q, float em1) {
+  if (fabsf(q) > 0.5f) return em1 - q;
+  float s = 1.0f / 362880.0f;
+  s = fmaf(s, q, 1.0f / 40320.0f);
+  s = fmaf(s, q, 1.0f / 5040.0f);
+  s = fmaf(s, q, 1.0f / 720.0f);
+  s = fmaf(s, q, 1.0f / 120.0f);
+  s = fmaf(s, q, 1.0f / 24.0f);
+  s = fmaf(s, q, 1.0f / 6.0f);
+  s = fmaf(s, q, 0.5f);
+  return s * q * q;
+}
+
+// Whether logp - old lies above (or, with kBelow, below) a border, decided as
+// in fp64: the fp32 difference decides unless it is so near the border that
+// its own rounding, at most 2^-24 of it, matters.
+template <bool kBelow>
+__device__ __forceinline__ bool beyond(float d32, float logp, float old, double border) {
+  const float b = static_cast<float>(border);
+  if (fabsf(d32 - b) > 1e-6f * fmaxf(1.0f, fabsf(b))) return kBelow ? d32 < b : d32 > b;
+  const double d = static_cast<double>(logp) - static_cast<double>(old);
+  return kBelow ? d < border : d > border;
+}
+
+struct Sums {
+  double policy, kl, clipped;
+};
+
+struct Weights {
+  float token;                  // FS_MEAN_TOKEN / FS_MEAN_NONE: the same for every token
+  float seqs;                   // FS_MEAN_SEQUENCE: sequences that have tokens
+};
+
+// The sequence that token i belongs to: the last one that starts at or before
+// it.  Always in [0, n_seqs), whatever the offsets hold.
+__device__ __forceinline__ int64_t sequence_of(const PolicyProblem& p, int64_t i) {
+  if (p.starts == nullptr) return i / p.row_len;
+  int64_t lo = 0, hi = p.n_seqs;                // starts[lo] <= i < starts[hi]
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (p.starts[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Tokens [i, i + kVec) of one thread.
+template <int kVec>
+__device__ __forceinline__ void tokens(const PolicyProblem& p, const Weights& w, int64_t i, Sums& sums) {
+  float lp[kVec], old[kVec], ref[kVec], adv[kVec], g[kVec];
+  bool on[kVec];
+  if constexpr (kVec == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p.logp + i);
+    const float4 b = *reinterpret_cast<const float4*>(p.old_logp + i);
+    lp[0] = a.x; lp[1] = a.y; lp[2] = a.z; lp[3] = a.w;
+    old[0] = b.x; old[1] = b.y; old[2] = b.z; old[3] = b.w;
+    if (p.ref_logp != nullptr) {
+      const float4 c = *reinterpret_cast<const float4*>(p.ref_logp + i);
+      ref[0] = c.x; ref[1] = c.y; ref[2] = c.z; ref[3] = c.w;
+    }
+    if (!p.adv_per_seq) {
+      const float4 c = *reinterpret_cast<const float4*>(p.adv + i);
+      adv[0] = c.x; adv[1] = c.y; adv[2] = c.z; adv[3] = c.w;
+    }
+    uchar4 m = make_uchar4(1, 1, 1, 1);
+    if (p.mask != nullptr) m = *reinterpret_cast<const uchar4*>(p.mask + i);
+    on[0] = m.x != 0; on[1] = m.y != 0; on[2] = m.z != 0; on[3] = m.w != 0;
+  } else {
+    lp[0] = p.logp[i];
+    old[0] = p.old_logp[i];
+    if (p.ref_logp != nullptr) ref[0] = p.ref_logp[i];
+    if (!p.adv_per_seq) adv[0] = p.adv[i];
+    on[0] = p.mask == nullptr || p.mask[i] != 0;
+  }
+  const bool by_seq = p.adv_per_seq || p.mean == FS_MEAN_SEQUENCE;
+  int64_t s = by_seq ? sequence_of(p, i) : 0;
+  int64_t end = 0;
+  if (by_seq) end = p.starts != nullptr ? p.starts[s + 1] : (s + 1) * p.row_len;
+  float seq_adv = 0.0f, weight = w.token;
+  auto enter = [&]() {
+    if (p.adv_per_seq) seq_adv = p.adv[s];
+    if (p.mean == FS_MEAN_SEQUENCE) weight = 1.0f / (static_cast<float>(p.counts[s]) * w.seqs);
+  };
+  if (by_seq) enter();
+  float policy = 0.0f, kl = 0.0f, clipped = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) {
+    while (by_seq && i + j >= end && s + 1 < p.n_seqs) {       // into the next sequence that has tokens
+      ++s;
+      end = p.starts != nullptr ? p.starts[s + 1] : end + p.row_len;
+      if (i + j < end) enter();
+    }
+    g[j] = 0.0f;
+    if (!on[j]) continue;
+    const float A = p.adv_per_seq ? seq_adv : adv[j];
+    const float d = lp[j] - old[j];
+    const bool cut = A > 0.0f ? beyond<false>(d, lp[j], old[j], p.log_hi)
+                              : A < 0.0f && beyond<true>(d, lp[j], old[j], p.log_lo);
+    const float rA = expf(d) * A;
+    const float term = cut ? (A > 0.0f ? p.hi : p.lo) * A : rA;
+    policy = fmaf(-term, weight, policy);
+    float grad = cut ? 0.0f : -rA;
+    if (cut) clipped += weight;
+    if (p.ref_logp != nullptr) {
+      const float q = ref[j] - lp[j];
+      const float em1 = expm1f(q);
+      kl = fmaf(kl_estimate(q, em1), weight, kl);
+      grad = fmaf(-p.kl_coef, em1, grad);
+    }
+    g[j] = grad * weight;
+  }
+  sums.policy += policy;
+  sums.kl += kl;
+  sums.clipped += clipped;
+  if constexpr (kVec == 4)
+    *reinterpret_cast<float4*>(p.grad + i) = make_float4(g[0], g[1], g[2], g[3]);
+  else
+    p.grad[i] = g[0];
+}
+
+__device__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sums of three values over the block, in a fixed order; valid in thread 0.
+__device__ void block_sums(double (&v)[3]) {
+  __shared__ double part[kThreads / 32][3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    v[k] = warp_sum(v[k]);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][k] = v[k];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      v[k] = 0.0;
+      for (int i = 0; i < kThreads / 32; ++i) v[k] += part[i][k];
+    }
+  }
+  __syncthreads();
+}
+
+template <bool kAligned>
+__global__ void __launch_bounds__(kThreads) policy_loss_kernel(const PolicyProblem p, const bool counted) {
+  __shared__ bool last;
+  pdl_wait();                                   // the counts, and whatever wrote the inputs
+  Weights w{1.0f, 1.0f};
+  const unsigned long long count = counted ? *reinterpret_cast<volatile unsigned long long*>(&p.scratch->count) : 0ull;
+  if (p.mean == FS_MEAN_TOKEN) w.token = 1.0f / static_cast<float>(counted ? max(count, 1ull) : p.N);
+  if (p.mean == FS_MEAN_SEQUENCE) w.seqs = static_cast<float>(count);
+  Sums sums{0.0, 0.0, 0.0};
+  const int64_t tid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  if constexpr (kAligned) {
+    const int64_t quads = p.N / 4;
+    for (int64_t k = tid; k < quads; k += stride) tokens<4>(p, w, k * 4, sums);
+    if (tid < p.N - quads * 4) tokens<1>(p, w, quads * 4 + tid, sums);
+  } else {
+    for (int64_t k = tid; k < p.N; k += stride) tokens<1>(p, w, k, sums);
+  }
+  double v[3] = {sums.policy, sums.kl, sums.clipped};
+  block_sums(v);
+  if (threadIdx.x == 0) {
+    double* mine = p.scratch->sums[blockIdx.x];
+    mine[0] = v[0];
+    mine[1] = v[1];
+    mine[2] = v[2];
+    __threadfence();
+    last = atomicAdd(&p.scratch->ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  // the block that finishes last adds the blocks' sums, in their order
+  __threadfence();
+  double t[3] = {0.0, 0.0, 0.0};
+  for (unsigned b = threadIdx.x; b < gridDim.x; b += kThreads) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) t[k] += __ldcg(&p.scratch->sums[b][k]);
+  }
+  block_sums(t);
+  if (threadIdx.x == 0) {
+    p.stats[0] = static_cast<float>(t[0] + static_cast<double>(p.kl_coef) * t[1]);
+    p.stats[1] = static_cast<float>(t[0]);
+    p.stats[2] = static_cast<float>(t[1]);
+    p.stats[3] = static_cast<float>(t[2]);
+    p.scratch->ticket = 0;
+    p.scratch->count = 0;
+  }
+}
+
+bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+
+cudaError_t launch_policy_loss(const PolicyProblem& p, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const bool counted = p.mean == FS_MEAN_SEQUENCE || (p.mean == FS_MEAN_TOKEN && p.mask != nullptr);
+  if (counted) {
+    const int64_t want = p.mean == FS_MEAN_SEQUENCE ? p.n_seqs : (p.N + kCountThreads * 16 - 1) / (kCountThreads * 16);
+    e = launch_kernel(policy_count_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(want, 4 * sms))),
+                      dim3(kCountThreads), 0, stream, false, p);
+    if (e != cudaSuccess) return e;
+  }
+  const bool vec = aligned_to(p.logp, 16) && aligned_to(p.old_logp, 16) && aligned_to(p.ref_logp, 16) &&
+                   (p.adv_per_seq || aligned_to(p.adv, 16)) && aligned_to(p.mask, 4) && aligned_to(p.grad, 16);
+  const int64_t items = vec ? (p.N + 3) / 4 : p.N;
+  const int64_t blocks = std::min<int64_t>({(items + kThreads - 1) / kThreads, 8 * sms, kTrainMaxBlocks});
+  return launch_kernel(vec ? policy_loss_kernel<true> : policy_loss_kernel<false>,
+                       dim3(static_cast<unsigned>(std::max<int64_t>(blocks, 1))), dim3(kThreads), 0, stream, counted,
+                       p, counted);
+}
+
+}  // namespace fs

@@ -8,81 +8,19 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
+#include "fs_head_tc.cuh"
 #include "fs_train.h"
 
 namespace fs {
 namespace {
-
-constexpr int kTile = 64;
-constexpr int kStep = 16;
 
 __device__ __forceinline__ LsePart lse_join(LsePart a, LsePart b) {
   if (b.s == 0.0f) return a;
   if (a.s == 0.0f) return b;
   const float m = fmaxf(a.m, b.m);
   return LsePart{m, a.s * expf(a.m - m) + b.s * expf(b.m - m)};
-}
-
-// acc[i][j] = sum_k A(m0 + ty + 16 i, k) B(n0 + tx + 16 j, k) over k in
-// [0, K), with element (r, k) of an operand at r * row + k * col.
-__device__ __forceinline__ void tile_product(const __nv_bfloat16* A, int64_t a_row, int64_t a_col, int64_t M,
-                                             const __nv_bfloat16* B, int64_t b_row, int64_t b_col, int64_t N,
-                                             int64_t k_begin, int64_t K, int64_t m0, int64_t n0, float (&acc)[4][4]) {
-  __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-  for (int64_t k0 = k_begin; k0 < K; k0 += kStep) {
-    for (int e = threadIdx.x; e < kTile * kStep; e += 256) {
-      int r = e / kStep, k = e % kStep;
-      if (a_col != 1) { r = e % kTile; k = e / kTile; }
-      sa[k][r] = m0 + r < M && k0 + k < K ? __bfloat162float(A[(m0 + r) * a_row + (k0 + k) * a_col]) : 0.0f;
-      r = e / kStep, k = e % kStep;
-      if (b_col != 1) { r = e % kTile; k = e / kTile; }
-      sb[k][r] = n0 + r < N && k0 + k < K ? __bfloat162float(B[(n0 + r) * b_row + (k0 + k) * b_col]) : 0.0f;
-    }
-    __syncthreads();
-    for (int k = 0; k < kStep; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-}
-
-__device__ __forceinline__ float scaled(const HeadProblem& p, int64_t t, int64_t v, float dot, float inv_t) {
-  if (p.bias != nullptr) dot += p.bias[t * p.bias_stride + v];
-  return dot * inv_t;
-}
-
-__global__ void __launch_bounds__(256) head_parts_kernel(const HeadProblem p, LsePart* parts, int64_t n_parts,
-                                                         float* own_x, float* kept, int64_t pitch) {
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4];
-  tile_product(static_cast<const __nv_bfloat16*>(p.h), p.d, 1, p.n, static_cast<const __nv_bfloat16*>(p.W), p.d, 1, p.V,
-               0, p.d, m0, n0, acc);
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = m0 + ty + 16 * i;
-    const bool row = t < p.n;
-    const float inv_t = row ? row_temp(p.temp[t]).inv_t : 0.0f;
-    const int64_t id = row ? p.ids[t] : -1;
-    float x[4];
-    LsePart part{-INFINITY, 0.0f};
-    for (int j = 0; j < 4; ++j) {
-      const int64_t v = n0 + tx + 16 * j;
-      x[j] = -INFINITY;
-      if (!row || v >= p.V) continue;
-      x[j] = scaled(p, t, v, acc[i][j], inv_t);
-      if (kept != nullptr) kept[t * pitch + v] = x[j];
-      if (v == id) own_x[t] = x[j];
-      if (x[j] == -INFINITY) continue;
-      part = lse_join(part, LsePart{x[j], 1.0f});
-    }
-    for (int o = 8; o > 0; o >>= 1)
-      part = lse_join(part, LsePart{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o)});
-    if (tx == 0 && row) parts[t * n_parts + blockIdx.x] = part;
-  }
 }
 
 __global__ void __launch_bounds__(128) head_merge_kernel(const HeadProblem p, const LsePart* parts, int64_t n_parts,
@@ -99,7 +37,7 @@ __global__ void __launch_bounds__(128) head_merge_kernel(const HeadProblem p, co
   const bool valid = row_temp(p.temp[t]).mode != kRowInvalid;
   const int64_t id = p.ids[t];
   float z = !valid || part.s == 0.0f ? -INFINITY : part.m + logf(part.s);
-  if (valid && part.m == INFINITY) z = NAN;
+  if (valid && !(part.s < INFINITY)) z = NAN;
   lse[t] = z;
   float lp = 0.0f;
   if (valid && id >= 0 && id < p.V) {
@@ -123,88 +61,195 @@ __global__ void __launch_bounds__(256) head_rows_kernel(const HeadProblem p, con
   for (int64_t i = threadIdx.x; i < p.d / 8; i += 256) dst[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
 }
 
-__device__ __forceinline__ float ds_of(float x, float lse, float c, bool own) {
-  return c == 0.0f ? 0.0f : c * ((own ? 1.0f : 0.0f) - expf(x - lse));
-}
-
+// ds of vocabulary rows [v0, v0 + vc) from the kept logits: 4 bytes read and 2
+// written per element, 8 elements a thread.  The pitches are multiples of 64
+// elements and v0 of 256, so every group of 8 is aligned; columns in [vc,
+// pitch) hold what the padding of `kept` gives and are never read.
 __global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, const float* lse, const float* coef,
                                                            const float* kept, int64_t kept_pitch, int64_t v0,
-                                                           int64_t vc, __nv_bfloat16* ds, int64_t pitch) {
+                                                           __nv_bfloat16* ds, int64_t pitch) {
   const int64_t t = blockIdx.x;
   const float c = coef[t], z = lse[t];
   const int64_t id = p.ids[t] - v0;
-  for (int64_t v = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x; v < vc; v += static_cast<int64_t>(gridDim.y) * 256)
-    ds[t * pitch + v] = __float2bfloat16_rn(ds_of(kept[t * kept_pitch + v0 + v], z, c, v == id));
-}
-
-__global__ void __launch_bounds__(256) head_ds_kernel(const HeadProblem p, const float* lse, const float* coef,
-                                                      int64_t v0, int64_t vc, __nv_bfloat16* ds, int64_t pitch) {
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4];
-  tile_product(static_cast<const __nv_bfloat16*>(p.h), p.d, 1, p.n,
-               static_cast<const __nv_bfloat16*>(p.W) + v0 * p.d, p.d, 1, vc, 0, p.d, m0, n0, acc);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = m0 + ty + 16 * i, v = n0 + tx + 16 * j;
-      if (t >= p.n || v >= vc) continue;
-      const float x = scaled(p, t, v0 + v, acc[i][j], row_temp(p.temp[t]).inv_t);
-      ds[t * pitch + v] = __float2bfloat16_rn(ds_of(x, lse[t], coef[t], v0 + v == p.ids[t]));
+  const float* src = kept + t * kept_pitch + v0;
+  __nv_bfloat16* dst = ds + t * pitch;
+  const int64_t stride = static_cast<int64_t>(gridDim.y) * 256 * 8;
+  for (int64_t v = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * 8; v < pitch; v += stride) {
+    __align__(16) __nv_bfloat16 o[8];
+    if (c == 0.0f) {
+      *reinterpret_cast<uint4*>(o) = make_uint4(0, 0, 0, 0);
+    } else {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(src + v));
+      const float4 b = __ldcs(reinterpret_cast<const float4*>(src + v + 4));
+      const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float q = __expf(x[j] - z);
+        o[j] = __float2bfloat16_rn(v + j == id ? c * (1.0f - q) : -c * q);
+      }
     }
-}
-
-// partials[t, j] (+)= sum over [0, vc) of ds(t, v) W(v0 + v, j).
-__global__ void __launch_bounds__(256) head_dh_kernel(const HeadProblem p, const __nv_bfloat16* ds, int64_t pitch,
-                                                      int64_t v0, int64_t vc, bool add, float* partials) {
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4];
-  tile_product(ds, pitch, 1, p.n, static_cast<const __nv_bfloat16*>(p.W) + v0 * p.d, 1, p.d, p.d, 0, vc, m0, n0, acc);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = m0 + ty + 16 * i, k = n0 + tx + 16 * j;
-      if (t >= p.n || k >= p.d) continue;
-      float* at = partials + t * p.d + k;
-      *at = add ? *at + acc[i][j] : acc[i][j];
-    }
-}
-
-__global__ void __launch_bounds__(256) head_dw_kernel(const HeadProblem p, const __nv_bfloat16* ds, int64_t pitch,
-                                                      const __nv_bfloat16* h_live, int64_t v0, int64_t vc,
-                                                      __nv_bfloat16* grad_W) {
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, n0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4];
-  tile_product(ds, 1, pitch, vc, h_live, 1, p.d, p.d, 0, p.n, m0, n0, acc);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t v = m0 + ty + 16 * i, k = n0 + tx + 16 * j;
-      if (v < vc && k < p.d) grad_W[(v0 + v) * p.d + k] = __float2bfloat16_rn(acc[i][j]);
-    }
-}
-
-__global__ void __launch_bounds__(256) head_dh_sum_kernel(const HeadProblem p, const float* partials, int64_t splits,
-                                                          const float* coef, __nv_bfloat16* grad_h) {
-  const int64_t t = blockIdx.x;
-  const bool live = coef[t] != 0.0f;
-  for (int64_t k = threadIdx.x; k < p.d; k += 256) {
-    float s = 0.0f;
-    if (live)
-      for (int64_t i = 0; i < splits; ++i) s += partials[(i * p.n + t) * p.d + k];
-    grad_h[t * p.d + k] = __float2bfloat16_rn(s);
+    *reinterpret_cast<uint4*>(dst + v) = *reinterpret_cast<uint4*>(o);
   }
 }
 
-unsigned tiles(int64_t n) { return static_cast<unsigned>((n + kTile - 1) / kTile); }
+// grad_h: the splits' partials added in their order and rounded once.
+__global__ void __launch_bounds__(256) head_dh_sum_kernel(const HeadProblem p, const float* partials, int64_t splits,
+                                                          const float* coef, __nv_bfloat16* grad_h) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;     // d is a multiple of 8
+  if (i >= p.n * p.d) return;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (coef[i / p.d] != 0.0f) {
+#pragma unroll 4
+    for (int64_t k = 0; k < splits; ++k) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(partials + k * p.n * p.d + i));
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+  }
+  __align__(8) __nv_bfloat16 o[4] = {__float2bfloat16_rn(s.x), __float2bfloat16_rn(s.y), __float2bfloat16_rn(s.z),
+                                     __float2bfloat16_rn(s.w)};
+  *reinterpret_cast<uint2*>(grad_h + i) = *reinterpret_cast<uint2*>(o);
+}
+
+// ---------------------------------------------------------------- launch geometry
+using head::Args;
+using head::Kind;
+
+// Columns of a tile for n tokens: as few tiles as 256 columns allow, all of
+// one size.
+struct ColumnTiles {
+  int bn, count;
+};
+
+ColumnTiles column_tiles(int64_t n) {
+  ColumnTiles c;
+  const int64_t count = std::max<int64_t>(1, (n + head::kMaxN - 1) / head::kMaxN);
+  c.bn = static_cast<int>(((n + count - 1) / count + 15) / 16 * 16);
+  c.bn = std::max(c.bn, 16);
+  c.count = static_cast<int>((n + c.bn - 1) / c.bn);
+  return c;
+}
+
+int row_tiles(int64_t m) { return static_cast<int>((m + head::kTileM - 1) / head::kTileM); }
+int k_blocks(int64_t k) { return static_cast<int>((k + head::kBK - 1) / head::kBK); }
+
+template <Kind kKind>
+int stages_for(int bn) {
+  return std::min(head::kMaxStages,
+                  (head::kSmemLimit - 1024 - head::kBarBytes - head::epi_bytes(kKind)) / (head::kATile + bn * head::kBK));
+}
+
+template <Kind kKind>
+int smem_for(int bn) {
+  return stages_for<kKind>(bn) * (head::kATile + bn * head::kBK) + head::kBarBytes + head::epi_bytes(kKind) + 1024;
+}
+
+// Pairs that can be resident at once: a pair needs two SMs of one cluster
+// group, so this can be below SMs / 2.
+int resident_pairs() {
+  static std::atomic<int> cached[64];                    // zero-initialized (static storage)
+  int dev = -1, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 76;                                           // no device: sizes only
+  }
+  if (dev < 64 && cached[dev].load(std::memory_order_relaxed) > 0) return cached[dev].load(std::memory_order_relaxed);
+  constexpr auto kernel = head::gemm_kernel<head::kDw, false>;
+  int n = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (sms / 2)));
+  cfg.blockDim = dim3(head::kThreads);
+  cfg.dynamicSmemBytes = smem_for<head::kDw>(head::kMaxN);
+  if (raise_smem_limit<kernel>(dev, smem_for<head::kDw>(head::kMaxN)) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = sms / 2;
+  }
+  n = std::max(1, std::min(n, sms / 2));
+  if (dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// kLse / kDs: the column tiles of one launch (as many as there are pairs at
+// most; larger batches take several launches of about the same size) and the
+// groups of pairs that share the row tiles, as few as leave every group the
+// same number of them.
+struct Groups {
+  ColumnTiles cols;
+  int64_t slice;                // tokens of one launch
+  int groups;
+};
+
+Groups groups_for(int64_t n, int64_t V) {
+  const int pairs = resident_pairs();
+  Groups g;
+  const int64_t most = static_cast<int64_t>(pairs) * head::kMaxN;
+  const int64_t slices = (n + most - 1) / most;
+  g.slice = slices <= 1 ? n : std::min(most, ((n + slices - 1) / slices + 15) / 16 * 16);
+  g.cols = column_tiles(g.slice);
+  const int tiles = std::max(1, row_tiles(V));
+  const int can = std::max(1, std::min(tiles, pairs / g.cols.count));
+  const int per = (tiles + can - 1) / can;
+  g.groups = (tiles + per - 1) / per;
+  return g;
+}
+
+template <Kind kKind, bool kBias>
+cudaError_t launch(const Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const int smem = smem_for<kKind>(a.bn);
+  if (e == cudaSuccess) e = raise_smem_limit<head::gemm_kernel<kKind, kBias>>(dev, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(head::gemm_kernel<kKind, kBias>, dim3(static_cast<unsigned>(2 * a.n_pairs)),
+                       dim3(head::kThreads), smem, stream, false, ta, tb, a);
+}
+
+// The products x^T = W h^T over vocabulary rows [v0, v0 + vc), slice by slice.
+template <Kind kKind>
+cudaError_t launch_logits(Args a, int64_t v0, int64_t vc, const Groups& g, cudaStream_t stream) {
+  const HeadProblem& p = a.p;
+  CUtensorMap tw, th;
+  if (!encode_rows_bf16(&tw, static_cast<const uint16_t*>(p.W) + v0 * p.d, vc, p.d, p.d, 128)) return cudaErrorInvalidValue;
+  a.M = vc;
+  a.n_mt = row_tiles(vc);
+  a.n_kb = k_blocks(p.d);
+  a.splits = 1;
+  a.v0 = v0;
+  a.bn = g.cols.bn;
+  a.n_stages = stages_for<kKind>(a.bn);
+  for (int64_t t0 = 0; t0 < p.n; t0 += g.slice) {
+    a.t0 = t0;
+    a.N = std::min(g.slice, p.n - t0);
+    a.t_end = t0 + a.N;
+    a.n_nt = static_cast<int>((a.N + a.bn - 1) / a.bn);
+    a.n_pairs = g.groups * a.n_nt;
+    if (!encode_rows_bf16(&th, static_cast<const uint16_t*>(p.h) + t0 * p.d, a.N, p.d, p.d, a.bn / 2))
+      return cudaErrorInvalidValue;
+    const cudaError_t e = p.bias != nullptr ? launch<kKind, true>(a, tw, th, stream) : launch<kKind, false>(a, tw, th, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 }  // namespace
 
-int64_t head_parts(int64_t, int64_t V) { return std::max<int64_t>(1, tiles(V)); }
+int64_t head_parts(int64_t n, int64_t V) { return 8 * groups_for(n, V).groups; }
 
-cudaError_t launch_head_parts(const HeadProblem& p, LsePart* parts, float* own_x, float* kept, int*,
+cudaError_t launch_head_parts(const HeadProblem& p, LsePart* parts, float* own_x, float* kept, int* err,
                               cudaStream_t stream) {
-  return launch_kernel(head_parts_kernel, dim3(tiles(p.V), tiles(p.n)), dim3(256), 0, stream, false, p, parts,
-                       head_parts(p.n, p.V), own_x, kept, padded_cols(p.V));
+  const Groups g = groups_for(p.n, p.V);
+  Args a{};
+  a.p = p;
+  a.parts = parts;
+  a.n_parts = 8 * g.groups;
+  a.own_x = own_x;
+  a.kept = kept;
+  a.kept_pitch = padded_cols(p.V);
+  a.err = err;
+  return launch_logits<head::kLse>(a, 0, p.V, g, stream);
 }
 
 cudaError_t launch_head_merge(const HeadProblem& p, const LsePart* parts, int64_t n_parts, const float* own_x,
@@ -220,34 +265,98 @@ cudaError_t launch_head_rows(const HeadProblem& p, const float* logp, const floa
 }
 
 cudaError_t launch_head_ds(const HeadProblem& p, const float* lse, const float* coef, const float* kept, int64_t v0,
-                           int64_t vc, void* ds, int*, cudaStream_t stream) {
+                           int64_t vc, void* ds, int* err, cudaStream_t stream) {
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(ds);
-  if (kept != nullptr)
-    return launch_kernel(head_ds_kept_kernel, dim3(static_cast<unsigned>(p.n), 64), dim3(256), 0, stream, false, p,
-                         lse, coef, kept, padded_cols(p.V), v0, vc, out, padded_cols(vc));
-  return launch_kernel(head_ds_kernel, dim3(tiles(vc), tiles(p.n)), dim3(256), 0, stream, false, p, lse, coef, v0, vc,
-                       out, padded_cols(vc));
+  const int64_t pitch = padded_cols(vc);
+  if (kept != nullptr) {
+    const int64_t blocks = std::min<int64_t>((pitch + 2047) / 2048, 64);
+    return launch_kernel(head_ds_kept_kernel, dim3(static_cast<unsigned>(p.n), static_cast<unsigned>(blocks)),
+                         dim3(256), 0, stream, false, p, lse, coef, kept, padded_cols(p.V), v0, out, pitch);
+  }
+  Args a{};
+  a.p = p;
+  a.lse = lse;
+  a.coef = coef;
+  a.ds = out;
+  a.ds_pitch = pitch;
+  a.err = err;
+  return launch_logits<head::kDs>(a, v0, vc, groups_for(p.n, vc), stream);
 }
 
-int64_t head_dh_splits(int64_t, int64_t, int64_t) { return 1; }
+// Splits of grad_h's product along the vocabulary: its tiles alone (16 by the
+// number of column tiles for a width of 4096) seldom fill the pairs evenly.
+// Each count is rated by its rounds of pairs times the k blocks of a split
+// (bn clocks per k block and 128 rows at the tensor rate, twice that for the
+// pair's tile) plus the partials' way through memory and back.
+int64_t head_dh_splits(int64_t n, int64_t d, int64_t vc) {
+  const ColumnTiles c = column_tiles(n);
+  const int64_t tiles = static_cast<int64_t>(row_tiles(d)) * c.count;
+  const int64_t pairs = resident_pairs(), kb = k_blocks(vc);
+  int64_t best = 1;
+  double best_time = 1e300;
+  for (int64_t s = 1; s <= std::min<int64_t>(kb, 32); ++s) {
+    const double rounds = static_cast<double>((tiles * s + pairs - 1) / pairs);
+    const double time = rounds * (static_cast<double>((kb + s - 1) / s) * std::max(c.bn, 64) * 1.1e-9 + 1.0e-6) +
+                        static_cast<double>(s) * n * d * 8.0 / 6.0e12;
+    if (time < best_time * 0.995) {
+      best_time = time;
+      best = s;
+    }
+  }
+  return best;
+}
 
-cudaError_t launch_head_dh(const HeadProblem& p, const void* ds, int64_t v0, int64_t vc, int64_t, bool add,
-                           float* partials, int*, cudaStream_t stream) {
-  return launch_kernel(head_dh_kernel, dim3(tiles(p.d), tiles(p.n)), dim3(256), 0, stream, false, p,
-                       static_cast<const __nv_bfloat16*>(ds), padded_cols(vc), v0, vc, add, partials);
+cudaError_t launch_head_dh(const HeadProblem& p, const void* ds, int64_t v0, int64_t vc, int64_t splits, bool add,
+                           float* partials, int* err, cudaStream_t stream) {
+  const ColumnTiles c = column_tiles(p.n);
+  CUtensorMap tw, ts;
+  if (!encode_rows_bf16(&tw, static_cast<const uint16_t*>(p.W) + v0 * p.d, vc, p.d, p.d, head::kBK) ||
+      !encode_rows_bf16(&ts, ds, p.n, vc, padded_cols(vc), c.bn / 2))
+    return cudaErrorInvalidValue;
+  Args a{};
+  a.p = p;
+  a.M = p.d;
+  a.N = p.n;
+  a.bn = c.bn;
+  a.n_stages = stages_for<head::kDh>(c.bn);
+  a.n_nt = c.count;
+  a.n_mt = row_tiles(p.d);
+  a.n_kb = k_blocks(vc);
+  a.splits = static_cast<int>(std::min<int64_t>(splits, a.n_kb));
+  a.n_pairs = static_cast<int>(std::min<int64_t>(resident_pairs(), static_cast<int64_t>(a.n_mt) * a.n_nt * a.splits));
+  a.partials = partials;
+  a.add = add;
+  a.err = err;
+  return launch<head::kDh, false>(a, tw, ts, stream);
 }
 
 cudaError_t launch_head_dh_sum(const HeadProblem& p, const float* partials, int64_t splits, const float* coef,
                                void* grad_h, cudaStream_t stream) {
-  return launch_kernel(head_dh_sum_kernel, dim3(static_cast<unsigned>(p.n)), dim3(256), 0, stream, false, p, partials,
-                       splits, coef, static_cast<__nv_bfloat16*>(grad_h));
+  return launch_kernel(head_dh_sum_kernel, dim3(static_cast<unsigned>((p.n * p.d / 4 + 255) / 256)), dim3(256), 0,
+                       stream, false, p, partials, splits, coef, static_cast<__nv_bfloat16*>(grad_h));
 }
 
 cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_live, int64_t v0, int64_t vc,
-                           void* grad_W, int*, cudaStream_t stream) {
-  return launch_kernel(head_dw_kernel, dim3(tiles(p.d), tiles(vc)), dim3(256), 0, stream, false, p,
-                       static_cast<const __nv_bfloat16*>(ds), padded_cols(vc),
-                       static_cast<const __nv_bfloat16*>(h_live), v0, vc, static_cast<__nv_bfloat16*>(grad_W));
+                           void* grad_W, int* err, cudaStream_t stream) {
+  CUtensorMap th, ts;
+  if (!encode_rows_bf16(&th, h_live, p.n, p.d, p.d, head::kBK) ||
+      !encode_rows_bf16(&ts, ds, p.n, vc, padded_cols(vc), head::kBK))
+    return cudaErrorInvalidValue;
+  Args a{};
+  a.p = p;
+  a.M = p.d;
+  a.N = vc;
+  a.bn = head::kMaxN;
+  a.n_stages = stages_for<head::kDw>(a.bn);
+  a.n_nt = static_cast<int>((vc + a.bn - 1) / a.bn);
+  a.n_mt = row_tiles(p.d);
+  a.n_kb = k_blocks(p.n);
+  a.splits = 1;
+  a.n_pairs = static_cast<int>(std::min<int64_t>(resident_pairs(), static_cast<int64_t>(a.n_mt) * a.n_nt));
+  a.v0 = v0;
+  a.grad_W = static_cast<__nv_bfloat16*>(grad_W);
+  a.err = err;
+  return launch<head::kDw, false>(a, th, ts, stream);
 }
 
 }  // namespace fs

@@ -187,6 +187,21 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr));
 }
 
+// 32 TMEM lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr));
+}
+
+// 32 TMEM lanes x 1 32-bit column.
+__device__ __forceinline__ uint32_t tmem_ld_1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  return r;
+}
+
 __device__ __forceinline__ void tmem_ld_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -205,6 +220,25 @@ __device__ __forceinline__ uint64_t smem_desc_k128(uint32_t smem_addr) {
   d |= static_cast<uint64_t>(2u) << 61;                            // 128-byte swizzle
   return d;
 }
+
+// The same for an operand stored along its M or N axis (MN-major): boxes of 64
+// MN elements (128 bytes) by 64 k rows, 8192 bytes each, one after another
+// along MN.  Leading byte offset: from one 64-element block to the next;
+// stride byte offset: from 8 k rows to the next 8.  Stepping K by 16 rows
+// advances the start address by 2048 bytes.
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);          // start address
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;                    // leading byte offset
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;                    // stride byte offset
+  d |= static_cast<uint64_t>(1u) << 46;                            // descriptor version (sm_100)
+  d |= static_cast<uint64_t>(2u) << 61;                            // 128-byte swizzle
+  return d;
+}
+
+// Bits of the instruction descriptor that mark A or B as MN-major.
+constexpr uint32_t kIdescMnMajorA = 1u << 15;
+constexpr uint32_t kIdescMnMajorB = 1u << 16;
 
 // Instruction descriptor of kind::f16 with bf16 A/B, fp32 D, both K-major.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(uint32_t M, uint32_t N) {

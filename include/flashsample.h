@@ -416,7 +416,8 @@ FS_API size_t fs_token_logprobs_backward_workspace_bytes(int64_t n, int64_t d, i
  *     the weighted share of clipped tokens; grad [N] fp32.  All zero when no
  *     token takes part.
  *   0 <= clip_low < 1, clip_high >= 0, kl_coef finite (0 without ref_logp).
- *   workspace: fs_policy_loss_workspace_bytes(n_seqs) bytes.
+ *   workspace: fs_policy_loss_workspace_bytes(n_seqs) bytes, for
+ *     FS_MEAN_SEQUENCE only (NULL otherwise).
  * Sums are held in fp64; the results do not depend on the run.
  */
 FS_API fs_status fs_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,

@@ -8,6 +8,7 @@ there is no CPU fallback.
 
 import ctypes
 import os
+from array import array
 
 import numpy as np
 
@@ -420,17 +421,26 @@ def sample_host(h_host, W, temp_host, seed, step, bias=None, out_ids=None, out_m
 
 
 # ---------------------------------------------------------------- learning from sampled tokens
-def _arg(t, name, dtype=None, shape=None):
+def _arg(t, name, dtype, shape=None):
     """Address of a contiguous CUDA tensor of this type and shape."""
+    try:
+        if t.is_cuda and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be a CUDA tensor (no CPU fallback)")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be contiguous")
-    return t.data_ptr()
+    raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be contiguous")
+
+
+def _stream_of(t, stream):
+    """Handle of ``stream``, or of the current stream of t's device (the raw
+    handle: building a Stream object costs as much as the call itself)."""
+    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _head_args(h, W, ids, temp, bias):
@@ -485,12 +495,12 @@ def token_logprobs(h, W, ids, temp, bias=None, kept=None, out=None, stream=None)
     args = _head_args(h, W, ids, temp, bias)
     n, d, V = args[2:5]
     if out is None:
-        out = (torch.empty(n, dtype=torch.float32, device=h.device), torch.empty(n, dtype=torch.float32, device=h.device))
+        out = (torch.empty_like(temp), torch.empty_like(temp))
     logp, lse = out
     lib = library()
     work = _workspace(lib.fs_token_logprobs_workspace_bytes(n, d, V), h.device, stream)
     check(lib.fs_token_logprobs(*args, _arg(logp, "logp", torch.float32, (n,)), _arg(lse, "lse", torch.float32, (n,)),
-                                _kept_arg(kept, n, V), work.data_ptr(), work.numel(), _stream_ptr(stream)))
+                                _kept_arg(kept, n, V), work.data_ptr(), work.numel(), _stream_of(h, stream)))
     return logp, lse
 
 
@@ -516,7 +526,7 @@ def token_logprobs_backward(h, W, ids, temp, logp, lse, grad_logp, bias=None, ke
         _arg(grad_logp, "grad_logp", torch.float32, (n,)), _kept_arg(kept, n, V),
         _arg(grad_h, "grad_h", torch.bfloat16, (n, d)) if need_h else None,
         _arg(grad_W, "grad_W", torch.bfloat16, (V, d)) if need_W else None,
-        work.data_ptr(), work.numel(), _stream_ptr(stream)))
+        work.data_ptr(), work.numel(), _stream_of(h, stream)))
     return grad_h if need_h else None, grad_W if need_W else None
 
 
@@ -562,13 +572,19 @@ def policy_loss(logp, old_logp, advantages, seq_starts=None, mask=None, ref_logp
         out = torch.empty(4, dtype=f32, device=logp.device), torch.empty_like(logp)
     stats, grad = out
     lib = library()
-    work = _workspace(lib.fs_policy_loss_workspace_bytes(S), logp.device, stream)
+    work, nbytes = None, 0
+    if mean == "sequence":                    # one count for each sequence
+        nbytes = lib.fs_policy_loss_workspace_bytes(S)
+        work = _workspace(nbytes, logp.device, stream)
     check(lib.fs_policy_loss(
         ptr, _arg(old_logp, "old_logp", f32, shape), None if ref_logp is None else _arg(ref_logp, "ref_logp", f32, shape),
         adv, 1 if adv_per_seq else 0, None if mask is None else _arg(mask, "mask", torch.bool, shape), starts, S, N,
         clip_low, clip_high, kl_coef, _MEANS[mean], _arg(stats, "stats", f32, (4,)), _arg(grad, "grad", f32, shape),
-        work.data_ptr(), work.numel(), _stream_ptr(stream)))
+        None if work is None else work.data_ptr(), nbytes, _stream_of(logp, stream)))
     return stats, grad
+
+
+_CLIP_TYPES = {}
 
 
 def clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, stream=None):
@@ -578,30 +594,35 @@ def clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, stream=None):
     ``norm_type`` 2 or inf.  A norm that is not finite scales nothing; an
     infinite ``max_norm`` measures only.  Nothing is synchronized."""
     torch = _torch()
-    types = {torch.float32: FS_TYPE_F32, torch.bfloat16: FS_TYPE_BF16, torch.float16: FS_TYPE_F16}
     if norm_type not in (2, float("inf")):
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"norm_type must be 2 or inf, got {norm_type}")
+    if not _CLIP_TYPES:
+        _CLIP_TYPES.update({torch.float32: FS_TYPE_F32, torch.bfloat16: FS_TYPE_BF16, torch.float16: FS_TYPE_F16})
     grads = list(grads)
     n = len(grads)
+    types = array("i")
     for g in grads:
-        if g.dtype not in types or not g.is_cuda or not g.is_contiguous():
+        kind = _CLIP_TYPES.get(g.dtype)
+        if kind is None or not g.is_cuda or not g.is_contiguous():
             raise FlashSampleError("FS_ERR_INVALID_ARG", "gradients must be contiguous fp32, bf16 or fp16 CUDA "
                                    "tensors (no CPU fallback)")
-    pointers = (_c_void_p * n)(*[g.data_ptr() for g in grads])
+        types.append(kind)
+    pointers = array("Q", [g.data_ptr() for g in grads])
     outs = pointers
     if out is not None:
         if len(out) != n:
             raise FlashSampleError("FS_ERR_INVALID_ARG", f"out must hold {n} tensors, got {len(out)}")
         for g, o in zip(grads, out):
-            if o.dtype != g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous():
+            if o.dtype is not g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous():
                 raise FlashSampleError("FS_ERR_INVALID_ARG", "an output must be a contiguous CUDA tensor of its "
                                        "gradient's type and shape")
-        outs = (_c_void_p * n)(*[o.data_ptr() for o in out])
+        outs = array("Q", [o.data_ptr() for o in out])
+    sizes = array("q", [g.numel() for g in grads])
     norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
-    check(library().fs_clip_grad_norm(pointers, outs, (_i64 * n)(*[g.numel() for g in grads]),
-                                      (_int * n)(*[types[g.dtype] for g in grads]), n, max_norm,
+    check(library().fs_clip_grad_norm(pointers.buffer_info()[0], outs.buffer_info()[0], sizes.buffer_info()[0],
+                                      types.buffer_info()[0], n, max_norm,
                                       FS_NORM_L2 if norm_type == 2 else FS_NORM_MAX, norm.data_ptr(),
-                                      _stream_ptr(stream)))
+                                      _stream_of(norm, stream)))
     return norm
 
 

@@ -16,35 +16,49 @@
 namespace fs {
 namespace {
 
-__device__ __forceinline__ LsePart lse_join(LsePart a, LsePart b) {
-  if (b.s == 0.0f) return a;
-  if (a.s == 0.0f) return b;
-  const float m = fmaxf(a.m, b.m);
-  return LsePart{m, a.s * expf(a.m - m) + b.s * expf(b.m - m)};
-}
+using head::lse_join;
 
-__global__ void __launch_bounds__(128) head_merge_kernel(const HeadProblem p, const LsePart* parts, int64_t n_parts,
-                                                         const float* own_x, float* logp, float* lse) {
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (t >= p.n) return;
-  LsePart part{-INFINITY, 0.0f};
-  for (int64_t i = lane; i < n_parts; i += 32) part = lse_join(part, parts[t * n_parts + i]);
+// Merge of the parts [n_parts, n] of kMergeRows tokens a block: every thread
+// joins every 128th part of one token, then the block's threads are joined.
+constexpr int kMergeRows = 8;
+constexpr int kMergeThreads = 1024;
+
+__global__ void __launch_bounds__(kMergeThreads) head_merge_kernel(const HeadProblem p, const LsePart* parts,
+                                                                   int64_t n_parts, const float* own_x, float* logp,
+                                                                   float* lse) {
+  __shared__ LsePart warps[kMergeThreads / 32][kMergeRows];
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x & (kMergeRows - 1));
+  LsePart part{head::kLowest, 0.0f};
+  if (t < p.n) {
+#pragma unroll 4
+    for (int64_t i = threadIdx.x / kMergeRows; i < n_parts; i += kMergeThreads / kMergeRows)
+      part = lse_join(part, parts[i * p.n + t]);
+  }
+#pragma unroll
+  for (int o = 16; o >= kMergeRows; o >>= 1)
+    part = lse_join(part, LsePart{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o)});
+  if ((threadIdx.x & 31) < kMergeRows) warps[threadIdx.x >> 5][threadIdx.x & (kMergeRows - 1)] = part;
+  __syncthreads();
+  if (threadIdx.x >= 32 * kMergeRows) return;
+  // one warp a token
+  const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kMergeRows + row;
+  part = warps[lane][row];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     part = lse_join(part, LsePart{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o)});
-  if (lane != 0) return;
-  const bool valid = row_temp(p.temp[t]).mode != kRowInvalid;
-  const int64_t id = p.ids[t];
+  if (lane != 0 || mine >= p.n) return;
+  const bool valid = row_temp(p.temp[mine]).mode != kRowInvalid;
+  const int64_t id = p.ids[mine];
   float z = !valid || part.s == 0.0f ? -INFINITY : part.m + logf(part.s);
-  if (valid && !(part.s < INFINITY)) z = NAN;
-  lse[t] = z;
+  if (valid && !(part.s < INFINITY)) z = NAN;           // a NaN or infinite logit
+  lse[mine] = z;
   float lp = 0.0f;
   if (valid && id >= 0 && id < p.V) {
-    const float x = own_x[t];
+    const float x = own_x[mine];
     lp = x == -INFINITY ? -INFINITY : x - z;
   }
-  logp[t] = lp;
+  logp[mine] = lp;
 }
 
 __global__ void __launch_bounds__(256) head_rows_kernel(const HeadProblem p, const float* logp, const float* lse,
@@ -172,30 +186,6 @@ int resident_pairs() {
   return n;
 }
 
-// kLse / kDs: the column tiles of one launch (as many as there are pairs at
-// most; larger batches take several launches of about the same size) and the
-// groups of pairs that share the row tiles, as few as leave every group the
-// same number of them.
-struct Groups {
-  ColumnTiles cols;
-  int64_t slice;                // tokens of one launch
-  int groups;
-};
-
-Groups groups_for(int64_t n, int64_t V) {
-  const int pairs = resident_pairs();
-  Groups g;
-  const int64_t most = static_cast<int64_t>(pairs) * head::kMaxN;
-  const int64_t slices = (n + most - 1) / most;
-  g.slice = slices <= 1 ? n : std::min(most, ((n + slices - 1) / slices + 15) / 16 * 16);
-  g.cols = column_tiles(g.slice);
-  const int tiles = std::max(1, row_tiles(V));
-  const int can = std::max(1, std::min(tiles, pairs / g.cols.count));
-  const int per = (tiles + can - 1) / can;
-  g.groups = (tiles + per - 1) / per;
-  return g;
-}
-
 template <Kind kKind, bool kBias>
 cudaError_t launch(const Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t stream) {
   int dev = 0;
@@ -207,55 +197,55 @@ cudaError_t launch(const Args& a, const CUtensorMap& ta, const CUtensorMap& tb, 
                        dim3(head::kThreads), smem, stream, false, ta, tb, a);
 }
 
-// The products x^T = W h^T over vocabulary rows [v0, v0 + vc), slice by slice.
+int pairs_for(int64_t units) { return static_cast<int>(std::min<int64_t>(resident_pairs(), units)); }
+
+// The product x^T = W h^T over vocabulary rows [v0, v0 + vc).
 template <Kind kKind>
-cudaError_t launch_logits(Args a, int64_t v0, int64_t vc, const Groups& g, cudaStream_t stream) {
+cudaError_t launch_logits(Args a, int64_t v0, int64_t vc, cudaStream_t stream) {
   const HeadProblem& p = a.p;
+  const ColumnTiles c = column_tiles(p.n);
   CUtensorMap tw, th;
-  if (!encode_rows_bf16(&tw, static_cast<const uint16_t*>(p.W) + v0 * p.d, vc, p.d, p.d, 128)) return cudaErrorInvalidValue;
+  if (!encode_rows_bf16(&tw, static_cast<const uint16_t*>(p.W) + v0 * p.d, vc, p.d, p.d, 128) ||
+      !encode_rows_bf16(&th, p.h, p.n, p.d, p.d, c.bn / 2))
+    return cudaErrorInvalidValue;
   a.M = vc;
+  a.N = p.n;
+  a.bn = c.bn;
+  a.n_stages = stages_for<kKind>(c.bn);
+  a.n_nt = c.count;
   a.n_mt = row_tiles(vc);
   a.n_kb = k_blocks(p.d);
   a.splits = 1;
+  a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
   a.v0 = v0;
-  a.bn = g.cols.bn;
-  a.n_stages = stages_for<kKind>(a.bn);
-  for (int64_t t0 = 0; t0 < p.n; t0 += g.slice) {
-    a.t0 = t0;
-    a.N = std::min(g.slice, p.n - t0);
-    a.t_end = t0 + a.N;
-    a.n_nt = static_cast<int>((a.N + a.bn - 1) / a.bn);
-    a.n_pairs = g.groups * a.n_nt;
-    if (!encode_rows_bf16(&th, static_cast<const uint16_t*>(p.h) + t0 * p.d, a.N, p.d, p.d, a.bn / 2))
-      return cudaErrorInvalidValue;
-    const cudaError_t e = p.bias != nullptr ? launch<kKind, true>(a, tw, th, stream) : launch<kKind, false>(a, tw, th, stream);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return p.bias != nullptr ? launch<kKind, true>(a, tw, th, stream) : launch<kKind, false>(a, tw, th, stream);
 }
 
 }  // namespace
 
-int64_t head_parts(int64_t n, int64_t V) { return 8 * groups_for(n, V).groups; }
+// Eight parts (2 CTAs x 4 lane quarters) for each row tile, or, where one
+// column tile takes all tokens, for each pair.
+int64_t head_parts(int64_t n, int64_t V) {
+  const int tiles = std::max(1, row_tiles(V));
+  return 8 * static_cast<int64_t>(column_tiles(n).count > 1 ? tiles : pairs_for(tiles));
+}
 
 cudaError_t launch_head_parts(const HeadProblem& p, LsePart* parts, float* own_x, float* kept, int* err,
                               cudaStream_t stream) {
-  const Groups g = groups_for(p.n, p.V);
   Args a{};
   a.p = p;
   a.parts = parts;
-  a.n_parts = 8 * g.groups;
   a.own_x = own_x;
   a.kept = kept;
   a.kept_pitch = padded_cols(p.V);
   a.err = err;
-  return launch_logits<head::kLse>(a, 0, p.V, g, stream);
+  return launch_logits<head::kLse>(a, 0, p.V, stream);
 }
 
 cudaError_t launch_head_merge(const HeadProblem& p, const LsePart* parts, int64_t n_parts, const float* own_x,
                               float* logp, float* lse, cudaStream_t stream) {
-  return launch_kernel(head_merge_kernel, dim3(static_cast<unsigned>((p.n + 3) / 4)), dim3(128), 0, stream, false, p,
-                       parts, n_parts, own_x, logp, lse);
+  return launch_kernel(head_merge_kernel, dim3(static_cast<unsigned>((p.n + kMergeRows - 1) / kMergeRows)),
+                       dim3(kMergeThreads), 0, stream, false, p, parts, n_parts, own_x, logp, lse);
 }
 
 cudaError_t launch_head_rows(const HeadProblem& p, const float* logp, const float* lse, const float* g, float* coef,
@@ -280,7 +270,7 @@ cudaError_t launch_head_ds(const HeadProblem& p, const float* lse, const float* 
   a.ds = out;
   a.ds_pitch = pitch;
   a.err = err;
-  return launch_logits<head::kDs>(a, v0, vc, groups_for(p.n, vc), stream);
+  return launch_logits<head::kDs>(a, v0, vc, stream);
 }
 
 // Splits of grad_h's product along the vocabulary: its tiles alone (16 by the
@@ -323,7 +313,7 @@ cudaError_t launch_head_dh(const HeadProblem& p, const void* ds, int64_t v0, int
   a.n_mt = row_tiles(p.d);
   a.n_kb = k_blocks(vc);
   a.splits = static_cast<int>(std::min<int64_t>(splits, a.n_kb));
-  a.n_pairs = static_cast<int>(std::min<int64_t>(resident_pairs(), static_cast<int64_t>(a.n_mt) * a.n_nt * a.splits));
+  a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt * a.splits);
   a.partials = partials;
   a.add = add;
   a.err = err;
@@ -352,7 +342,7 @@ cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_l
   a.n_mt = row_tiles(p.d);
   a.n_kb = k_blocks(p.n);
   a.splits = 1;
-  a.n_pairs = static_cast<int>(std::min<int64_t>(resident_pairs(), static_cast<int64_t>(a.n_mt) * a.n_nt));
+  a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
   a.v0 = v0;
   a.grad_W = static_cast<__nv_bfloat16*>(grad_W);
   a.err = err;

@@ -48,9 +48,17 @@ constexpr bool b_mn_major(Kind k) { return k == kDw; }
 
 // Shared memory behind the stages: barriers, then the epilogue's arrays.
 constexpr int kBarBytes = (2 * kMaxStages + 5) * 8 + 24;
-constexpr int epi_bytes(Kind k) {
-  return k == kLse ? (kMaxN + kEpiWarps * kPartCols) * 4 : k == kDs ? 3 * kMaxN * 4 : 0;
-}
+constexpr int epi_arrays(Kind k) { return k == kLse ? 2 : k == kDs ? 3 : 0; }    // of kPartCols floats a warp
+constexpr int epi_bytes(Kind k) { return epi_arrays(k) * kEpiWarps * kPartCols * 4; }
+// The tensor cores add to an accumulator in TMEM by cutting, not rounding: each
+// of the d / 16 additions of a logit loses half a step of the running sum on
+// average, always toward zero, which for d = 4096 shrinks x by 5e-6 and moves
+// lse by 1e-6 of itself.  So logits are accumulated 16 k blocks (1024 products)
+// at a time and the pieces are added in registers, rounding to nearest: a
+// quarter of the error at d = 4096, and no more at larger d.  The gradients,
+// rounded to 8 bits in the end, take their whole sums.
+constexpr int kSubBlocks = 16;
+constexpr int sub_blocks(Kind k) { return k == kLse || k == kDs ? kSubBlocks : 0x7fffffff; }
 constexpr int kSmemLimit = 232448;
 
 struct Args {
@@ -63,10 +71,8 @@ struct Args {
   int n_kb;                  // k blocks of the whole product
   int splits;                // kDh
   int n_pairs;               // pairs of the grid
-  int64_t t0, t_end;         // kLse / kDs: the tokens of this launch
   // kLse
-  LsePart* parts;            // [n, n_parts]
-  int64_t n_parts;
+  LsePart* parts;            // [parts, n]
   float* own_x;              // [n]
   float* kept;               // nullable [n, kept_pitch]
   int64_t kept_pitch;
@@ -84,29 +90,27 @@ struct Args {
   int* err;
 };
 
-// The tiles of one pair, in order.  kLse and kDs: a fixed column tile and
-// every n_pairs / n_nt-th row tile, so that the pairs that share W rows run
-// side by side and W comes from HBM once.  kDh: one split after another, so
-// that all pairs work on the same vocabulary rows at a time.  kDw: the row
-// tiles (the model width) of one column tile after another.
+// The tiles of one pair: every n_pairs-th of an order in which the tiles that
+// run side by side share what is read from HBM.  kLse and kDs: the column tiles
+// (tokens) of one row tile after another, so that W is read once.  kDh: one
+// split after another, so that all pairs work on the same vocabulary rows at a
+// time.  kDw: the row tiles (the model width) of one column tile after another.
 struct Unit {
   int mt, nt, k0, k1, split;
 };
 
 template <Kind kKind>
 __device__ __forceinline__ bool unit_at(const Args& a, int pair, int i, Unit& u) {
+  const int64_t tiles = static_cast<int64_t>(a.n_mt) * a.n_nt;
+  const int64_t at = pair + static_cast<int64_t>(i) * a.n_pairs;
+  if (at >= tiles * a.splits) return false;
   u.k0 = 0;
   u.k1 = a.n_kb;
   u.split = 0;
   if constexpr (kKind == kLse || kKind == kDs) {
-    const int groups = a.n_pairs / a.n_nt;
-    u.nt = pair % a.n_nt;
-    u.mt = pair / a.n_nt + i * groups;
-    return u.mt < a.n_mt;
+    u.mt = static_cast<int>(at / a.n_nt);
+    u.nt = static_cast<int>(at % a.n_nt);
   } else {
-    const int64_t tiles = static_cast<int64_t>(a.n_mt) * a.n_nt;
-    const int64_t at = pair + static_cast<int64_t>(i) * a.n_pairs;
-    if (at >= tiles * a.splits) return false;
     u.split = static_cast<int>(at / tiles);
     const int64_t tile = at % tiles;
     u.mt = static_cast<int>(tile % a.n_mt);
@@ -115,82 +119,38 @@ __device__ __forceinline__ bool unit_at(const Args& a, int pair, int i, Unit& u)
       u.k0 = static_cast<int>(static_cast<int64_t>(a.n_kb) * u.split / a.splits);
       u.k1 = static_cast<int>(static_cast<int64_t>(a.n_kb) * (u.split + 1) / a.splits);
     }
-    return true;
   }
+  return true;
 }
 
-// ---------------------------------------------------------------- kLse epilogue
-// Each thread holds one vocabulary row of the tile and sums exp(x - ref) of
-// its rows for each of its part's columns (tokens) in a register, over all
-// tiles of the pair; lanes are added once, at the end.  ref, one per (warp,
-// column), is the warp's largest x of the first tile that had any, and moves
-// only when an x exceeds it by kSlack: the sums then stay within fp32's range
-// (2^24 terms of e^20 at most) and a term is lost only where the term at ref
-// outweighs it by far more than fp32 resolves.  So the common case is one
-// fused multiply-add, one comparison, one exponential and one addition per
-// logit, without a running maximum.
-constexpr float kSlack = 20.0f;
-constexpr float kUnset = -3.402823466e38f;   // the lowest finite value: an x of that value (a mask) counts as it should
+// ---------------------------------------------------------------- logit epilogues
+constexpr float kLowest = -3.402823466e38f;  // the lowest finite value
 
-struct LseState {
-  float s[kPartCols];
-};
-
-// x of column c + j before the scaling.
-template <bool kBias>
-__device__ __forceinline__ float biased(const Args& a, uint32_t acc, int64_t t, int64_t v, bool row_ok) {
-  float x = __uint_as_float(acc);
-  if constexpr (kBias) {
-    if (row_ok && t < a.t_end) x += __ldg(a.p.bias + t * a.p.bias_stride + v);
+// v[i] of 32 values per lane joined over the warp's lanes: lane l returns value
+// l.  31 shuffles instead of the 160 of 32 separate reductions: each step
+// sends the half of the values that the other lane keeps.
+template <typename Join, typename Value>
+__device__ __forceinline__ float join_columns(int lane, Join join, Value value) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const bool up = (lane & 16) != 0;
+    const float lo = value(i), hi = value(i + 16);
+    v[i] = join(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16));
   }
-  return x;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i)
+      v[i] = join(up ? v[i + o] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + o], o));
+  }
+  return v[0];
 }
 
-template <bool kBias>
-__device__ __forceinline__ void lse_tile(const Args& a, LseState& st, const float* inv_t, float* ref, uint32_t taddr,
-                                         int cols, int64_t t_first, int64_t v) {
-  const bool row_ok = v < a.p.V;
-#pragma unroll
-  for (int c = 0; c < kPartCols; c += 8) {
-    if (c >= cols) break;
-    float d[8];
-    float over = -INFINITY;
-    {
-      uint32_t r[8];
-      tmem_ld_8(taddr + c, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t t = t_first + c + j;
-        const float x = biased<kBias>(a, r[j], t, v, row_ok);
-        if (a.kept != nullptr && row_ok && t < a.t_end) a.kept[t * a.kept_pitch + v] = x * inv_t[c + j];
-        d[j] = row_ok ? fmaf(x, inv_t[c + j], -ref[c + j]) : -INFINITY;
-        over = fmaxf(over, d[j]);
-      }
-    }
-    if (__any_sync(0xffffffffu, over > kSlack)) {       // seldom: some ref moves
-      uint32_t r[8];
-      tmem_ld_8(taddr + c, r);
-      tmem_ld_wait();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (!__any_sync(0xffffffffu, d[j] > kSlack)) continue;
-        const float old = ref[c + j];
-        const float x = row_ok ? biased<kBias>(a, r[j], t_first + c + j, v, row_ok) * inv_t[c + j] : -INFINITY;
-        float top = x;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        top = fminf(top, 3.402823466e38f);
-        st.s[c + j] *= __expf(old - top);               // 0 from an unset ref
-        d[j] = x - top;
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0) ref[c + j] = top;
-      }
-      __syncwarp();
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) st.s[c + j] += __expf(d[j]);
-  }
+__device__ __forceinline__ LsePart lse_join(LsePart a, LsePart b) {
+  const float m = fmaxf(a.m, b.m);
+  return LsePart{m, a.s * __expf(a.m - m) + b.s * __expf(b.m - m)};
 }
 
 template <Kind kKind, bool kBias>
@@ -293,26 +253,30 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       uint32_t phase = 0;
       bool ok = true;
       Unit u;
+      int use = 0;                                       // accumulators taken so far, in turn
       for (int i = 0; ok && unit_at<kKind>(a, pair, i, u); ++i) {
-        const int acc = i & 1;
-        if (!mbar_wait(&tempty_bar[acc], ((i >> 1) & 1) ^ 1, a.err, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * kMaxN;
-        for (int kb = u.k0; kb < u.k1; ++kb) {
-          if (!mbar_wait(&full_bar[stage], phase, a.err, abort_flag)) { ok = false; break; }
+        for (int kb0 = u.k0; ok && kb0 < u.k1; kb0 += min(sub_blocks(kKind), u.k1 - kb0), ++use) {
+          const int acc = use & 1;
+          if (!mbar_wait(&tempty_bar[acc], ((use >> 1) & 1) ^ 1, a.err, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + stage * stage_bytes);
-          const uint32_t b_addr = a_addr + kATile;
+          const uint32_t d_tmem = tmem_base + acc * kMaxN;
+          const int kb1 = kb0 + min(sub_blocks(kKind), u.k1 - kb0);
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(&full_bar[stage], phase, a.err, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a_addr = smem_u32(smem + stage * stage_bytes);
+            const uint32_t b_addr = a_addr + kATile;
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            mma_bf16_pair(d_tmem,
-                          a_mn_major(kKind) ? smem_desc_mn128(a_addr + k * 2048) : smem_desc_k128(a_addr + k * 32),
-                          b_mn_major(kKind) ? smem_desc_mn128(b_addr + k * 2048) : smem_desc_k128(b_addr + k * 32),
-                          idesc, kb > u.k0 || k > 0);
-          mma_commit_pair_multicast(&empty_bar[stage], kPairMask);       // frees the stage in both CTAs
-          if (++stage == a.n_stages) { stage = 0; phase ^= 1; }
+            for (int k = 0; k < kBK / 16; ++k)
+              mma_bf16_pair(d_tmem,
+                            a_mn_major(kKind) ? smem_desc_mn128(a_addr + k * 2048) : smem_desc_k128(a_addr + k * 32),
+                            b_mn_major(kKind) ? smem_desc_mn128(b_addr + k * 2048) : smem_desc_k128(b_addr + k * 32),
+                            idesc, kb > kb0 || k > 0);
+            mma_commit_pair_multicast(&empty_bar[stage], kPairMask);     // frees the stage in both CTAs
+            if (++stage == a.n_stages) { stage = 0; phase ^= 1; }
+          }
+          if (ok) mma_commit_pair_multicast(&tfull_bar[acc], kPairMask);
         }
-        if (ok) mma_commit_pair_multicast(&tfull_bar[acc], kPairMask);
       }
       if (!ok) {
         mma_commit_pair_multicast(drain_bar, 0x1);
@@ -329,100 +293,161 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
     const int cols = max(0, min(part_cols, a.bn - col0));
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + col0;
     pdl_wait();
-    // kLse / kDs: the columns' constants, the same for all tiles of the pair
-    const int64_t tile_t = a.t0 + static_cast<int64_t>(pair % a.n_nt) * a.bn;
-    const int64_t t_first = tile_t + col0;
-    float* ref = epi + kMaxN + warp * kPartCols;
-    int64_t id[2] = {-1, -1};
-    LseState st;
-    if constexpr (kKind == kLse || kKind == kDs) {
-      for (int c = threadIdx.x; c < a.bn; c += kEpiWarps * 32) {
-        const int64_t t = tile_t + c;
-        epi[c] = t < a.t_end ? row_temp(a.p.temp[t]).inv_t : 0.0f;
-        if constexpr (kKind == kDs) {
-          epi[kMaxN + c] = t < a.t_end ? a.lse[t] : 0.0f;
-          epi[2 * kMaxN + c] = t < a.t_end ? a.coef[t] : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int c = k * 32 + lane;
-        if (c < cols && t_first + c < a.t_end) id[k] = a.p.ids[t_first + c];
-        if constexpr (kKind == kDs) {
-          if (id[k] >= 0) id[k] -= a.v0;
-        }
-      }
-      if constexpr (kKind == kLse) {
-#pragma unroll
-        for (int c = 0; c < kPartCols; ++c) st.s[c] = 0.0f;
-        for (int c = lane; c < kPartCols; c += 32) ref[c] = kUnset;
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
-    }
+    auto release = [&](int acc) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
+    };
     Unit u;
-    for (int i = 0; unit_at<kKind>(a, pair, i, u); ++i) {
-      const int acc = i & 1;
-      if (!mbar_wait(&tfull_bar[acc], (i >> 1) & 1, a.err, abort_flag)) break;
-      tc_fence_after();
-      const uint32_t taddr = lane_addr + acc * kMaxN;
-      const int64_t m_warp = static_cast<int64_t>(u.mt) * kTileM + rank * 128 + quad * 32;
-      const int64_t m = m_warp + lane;
-      if constexpr (kKind == kLse || kKind == kDs) {
-        if constexpr (kKind == kLse) {
-          lse_tile<kBias>(a, st, epi + col0, ref, taddr, cols, t_first, m);
-        } else {
-          const bool row_ok = m < a.M;
-#pragma unroll 1
-          for (int c = 0; c < cols; c += 16) {
-            uint32_t r[16];
-            tmem_ld_16(taddr + c, r);
-            tmem_ld_wait();
+    if constexpr (kKind == kLse || kKind == kDs) {
+      // per warp: 1/T of its columns, then kLse: the columns' largest x,
+      // kDs: their lse and coefficients
+      float* inv_t = epi + warp * epi_arrays(kKind) * kPartCols;
+      float* second = inv_t + kPartCols;
+      float* third = inv_t + 2 * kPartCols;
+      LsePart part[2] = {{kLowest, 0.0f}, {kLowest, 0.0f}};      // of columns lane and 32 + lane
+      int64_t id[2] = {-1, -1};                                  // their tokens, as rows of this W
+      int nt = -1, use = 0;
+      bool ok = cols > 0;
+      for (int i = 0; unit_at<kKind>(a, pair, i, u); ++i) {
+        const int64_t t_first = static_cast<int64_t>(u.nt) * a.bn + col0;
+        const int64_t m_warp = static_cast<int64_t>(u.mt) * kTileM + rank * 128 + quad * 32;
+        const int64_t m = m_warp + lane;
+        const bool row_ok = m < a.M;
+        if (u.nt != nt) {                                        // other tokens than before
+          nt = u.nt;
+          __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int64_t t = t_first + c + j;
-              if (t >= a.t_end) break;
-              float x = __uint_as_float(r[j]);
-              if constexpr (kBias) {
-                if (row_ok) x += __ldg(a.p.bias + t * a.p.bias_stride + a.v0 + m);
-              }
-              const int col = col0 + c + j;
-              const float coef = epi[2 * kMaxN + col];
-              const float p = __expf(fmaf(x, epi[col], -epi[kMaxN + col]));
-              if (row_ok) a.ds[t * a.ds_pitch + m] = __float2bfloat16_rn(coef == 0.0f ? 0.0f : -coef * p);
+          for (int k = 0; k < 2; ++k) {
+            const int c = k * 32 + lane;
+            const int64_t t = t_first + c;
+            const bool real = c < cols && t < a.N;
+            inv_t[c] = real ? row_temp(a.p.temp[t]).inv_t : 0.0f;
+            id[k] = real ? a.p.ids[t] : -1;
+            if (id[k] >= 0) id[k] -= a.v0;
+            if constexpr (kKind == kDs) {
+              second[c] = real ? a.lse[t] : 0.0f;
+              third[c] = real ? a.coef[t] : 0.0f;
+            }
+          }
+          __syncwarp();
+        }
+        // the logits start from the bias, whose loads then overlap the products
+        float x[kPartCols];
+#pragma unroll
+        for (int c = 0; c < kPartCols; ++c) x[c] = 0.0f;
+        if constexpr (kBias) {
+          if (row_ok) {
+            const float* b = a.p.bias + a.v0 + m;
+            if (a.p.bias_stride == 0) {
+              const float shared = __ldg(b);
+#pragma unroll
+              for (int c = 0; c < kPartCols; ++c) x[c] = shared;
+            } else {
+              b += t_first * a.p.bias_stride;
+#pragma unroll
+              for (int c = 0; c < kPartCols; ++c)
+                if (c < cols && t_first + c < a.N) x[c] = __ldg(b + c * a.p.bias_stride);
             }
           }
         }
-        // a token's own logit: in few tiles, so looked for by ballots
+        for (int kb0 = u.k0; kb0 < u.k1; kb0 += min(kSubBlocks, u.k1 - kb0), ++use) {
+          const int acc = use & 1;
+          if (!mbar_wait(&tfull_bar[acc], (use >> 1) & 1, a.err, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kPartCols; c += 8) {
+            if (c >= cols) break;
+            uint32_t r[8];
+            tmem_ld_8(lane_addr + acc * kMaxN + c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[c + j] += __uint_as_float(r[j]);
+          }
+          release(acc);
+        }
+        if (!ok) {                                               // a wait gave up, or this warp has no columns
+          if (cols > 0) break;
+          continue;
+        }
+#pragma unroll
+        for (int c = 0; c < kPartCols; ++c) x[c] = row_ok ? x[c] * inv_t[c] : -INFINITY;
+        if constexpr (kKind == kLse) {
+          if (a.kept != nullptr && row_ok) {
+            float* dst = a.kept + t_first * a.kept_pitch + m;
+#pragma unroll
+            for (int c = 0; c < kPartCols; ++c)
+              if (c < cols && t_first + c < a.N) __stcs(dst + c * a.kept_pitch, x[c]);
+          }
+          // of each column the largest x, then the sum of exp(x - largest)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (k * 32 >= cols) break;
+            float top = join_columns(lane, [](float p, float q) { return fmaxf(p, q); },
+                                     [&](int c) { return x[k * 32 + c]; });
+            top = fminf(fmaxf(top, kLowest), -kLowest);
+            second[k * 32 + lane] = top;
+            __syncwarp();
+            const float sum = join_columns(lane, [](float p, float q) { return p + q; },
+                                           [&](int c) { return __expf(x[k * 32 + c] - second[k * 32 + c]); });
+            part[k] = lse_join(part[k], LsePart{top, sum});
+          }
+        } else {
+          __nv_bfloat16* dst = a.ds + t_first * a.ds_pitch + m;
+#pragma unroll
+          for (int c = 0; c < kPartCols; ++c) {
+            if (c < cols && t_first + c < a.N && row_ok) {
+              const float coef = third[c];
+              dst[c * a.ds_pitch] = __float2bfloat16_rn(coef == 0.0f ? 0.0f : -coef * __expf(x[c] - second[c]));
+            }
+          }
+        }
+        // a token's own logit lies in few tiles: looked for by ballots
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t hits = __ballot_sync(0xffffffffu, id[k] >= m_warp && id[k] < m_warp + 32 && id[k] < a.M);
           while (hits != 0) {
-            const int c = __ffs(hits) - 1;
+            const int c = k * 32 + __ffs(hits) - 1;
             hits &= hits - 1;
-            const int own = static_cast<int>(__shfl_sync(0xffffffffu, id[k], c) - m_warp);
-            float x = __uint_as_float(tmem_ld_1(taddr + k * 32 + c));
-            tmem_ld_wait();
-            const int64_t t = t_first + k * 32 + c;
-            const int col = col0 + k * 32 + c;
+            const int own = static_cast<int>(__shfl_sync(0xffffffffu, id[k], c & 31) - m_warp);
+            float mine = 0.0f;
+#pragma unroll
+            for (int j = k * 32; j < k * 32 + 32; ++j) mine = j == c ? x[j] : mine;
             if (lane == own) {
-              if constexpr (kBias) x += __ldg(a.p.bias + t * a.p.bias_stride + a.v0 + m);
               if constexpr (kKind == kLse) {
-                a.own_x[t] = x * epi[col];
-              } else {
-                const float coef = epi[2 * kMaxN + col];
-                const float p = __expf(fmaf(x, epi[col], -epi[kMaxN + col]));
-                if (coef != 0.0f) a.ds[t * a.ds_pitch + m] = __float2bfloat16_rn(coef * (1.0f - p));
+                a.own_x[t_first + c] = mine;
+              } else if (third[c] != 0.0f) {
+                a.ds[(t_first + c) * a.ds_pitch + m] = __float2bfloat16_rn(third[c] * (1.0f - __expf(mine - second[c])));
               }
             }
           }
         }
-      } else {
+        if constexpr (kKind == kLse) {
+          // with one column tile the pair's tiles share a part, else each has its own
+          Unit next;
+          if (a.n_nt > 1 || !unit_at<kKind>(a, pair, i + 1, next)) {
+            const int64_t which = (a.n_nt > 1 ? u.mt : pair) * 8 + rank * 4 + quad;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int c = k * 32 + lane;
+              if (c < cols && t_first + c < a.N) a.parts[which * a.N + t_first + c] = part[k];
+              part[k] = LsePart{kLowest, 0.0f};
+            }
+          }
+        }
+      }
+    } else {
+      for (int i = 0; unit_at<kKind>(a, pair, i, u); ++i) {
+        const int acc = i & 1;
+        if (!mbar_wait(&tfull_bar[acc], (i >> 1) & 1, a.err, abort_flag)) break;
+        tc_fence_after();
+        const int64_t m = static_cast<int64_t>(u.mt) * kTileM + rank * 128 + quad * 32 + lane;
         const int64_t n_first = static_cast<int64_t>(u.nt) * a.bn + col0;
         const bool row_ok = m < a.M;
 #pragma unroll 1
         for (int c = 0; c < cols; c += 16) {
           uint32_t r[16];
-          tmem_ld_16(taddr + c, r);
+          tmem_ld_16(lane_addr + acc * kMaxN + c, r);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -437,22 +462,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
             }
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
-    }
-    if constexpr (kKind == kLse) {
-      // the warp's lanes added: one part per (column, pair group, CTA, quarter)
-      const int64_t which = static_cast<int64_t>(pair / a.n_nt) * 8 + rank * 4 + quad;
-#pragma unroll
-      for (int c = 0; c < kPartCols; ++c) {
-        if (c >= cols) break;
-        float s = st.s[c];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const int64_t t = t_first + c;
-        if (lane == (c & 31) && t < a.t_end) a.parts[t * a.n_parts + which] = LsePart{ref[c], s};
+        release(acc);
       }
     }
   }

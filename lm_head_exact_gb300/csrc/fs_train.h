@@ -31,7 +31,7 @@ struct __align__(8) LsePart {
   float m, s;
 };
 
-// Forward: every row's parts [n, head_parts] and its own token's x (written
+// Forward: every row's parts [head_parts, n] and its own token's x (written
 // by whichever tile holds the token's id), kept logits on request; then the
 // merge of the parts.
 int64_t head_parts(int64_t n, int64_t V);
@@ -65,7 +65,7 @@ struct PolicyProblem {
   const uint8_t* mask;          // nullable
   const int64_t* starts;        // nullable: n_seqs rows of row_len tokens
   int64_t n_seqs, row_len, N;
-  double log_hi, log_lo;        // log(1 + clip_high), log(1 - clip_low)
+  float2 log_hi, log_lo;        // log(1 + clip_high), log(1 - clip_low), each as the sum of two fp32 numbers
   float hi, lo;                 // 1 + clip_high, 1 - clip_low
   float kl_coef;
   int mean;

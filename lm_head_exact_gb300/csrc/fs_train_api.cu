@@ -92,6 +92,11 @@ fs_status check_head(const HeadProblem& p) {
   return FS_OK;
 }
 
+float2 two_floats(double v) {
+  const float hi = static_cast<float>(v);
+  return make_float2(hi, static_cast<float>(v - hi));
+}
+
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const char* x = static_cast<const char*>(a);
   const char* y = static_cast<const char*>(b);
@@ -220,13 +225,14 @@ fs_status fs_policy_loss(const float* logp, const float* old_logp, const float* 
   if (mask != nullptr) FS_API_TRY(api_check_array(mask, 1, "mask"));
   if (seq_starts != nullptr) FS_API_TRY(api_check_array(seq_starts, 8, "seq_starts"));
   FS_API_TRY(api_check_array(grad, 4, "grad"));
-  FS_API_TRY(check_workspace(workspace, workspace_bytes, fs_policy_loss_workspace_bytes(n_seqs)));
+  if (mean == FS_MEAN_SEQUENCE)
+    FS_API_TRY(check_workspace(workspace, workspace_bytes, fs_policy_loss_workspace_bytes(n_seqs)));
   TrainScratch* scratch = nullptr;
   FS_API_TRY(api_train_scratch(stream, &scratch));
   FS_API_TRY(api_check_launch());
   PolicyProblem p{logp, old_logp, ref_logp, advantages, adv_per_seq == 1, mask, seq_starts, n_seqs, N / n_seqs, N};
-  p.log_hi = std::log1p(clip_high);
-  p.log_lo = std::log1p(-clip_low);
+  p.log_hi = two_floats(std::log1p(clip_high));
+  p.log_lo = two_floats(std::log1p(-clip_low));
   p.hi = static_cast<float>(1.0 + clip_high);
   p.lo = static_cast<float>(1.0 - clip_low);
   p.kl_coef = static_cast<float>(kl_coef);

@@ -205,50 +205,65 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
 
   if (warp == kProducerWarp) {
     // -------------------------------------------------------------- TMA producer (both CTAs)
-    if (lane == 0) {
-      pdl_wait();
-      const uint64_t pol_a = kKind == kDw ? policy_evict_last() : policy_evict_first();
-      const uint64_t pol_b = kKind == kDw ? policy_evict_first() : policy_evict_last();
-      int stage = 0;
-      uint32_t phase = 0;
-      int64_t n_issued = 0;
-      bool ok = true;
-      Unit u;
-      for (int i = 0; ok && unit_at<kKind>(a, pair, i, u); ++i) {
-        const int m0 = u.mt * kTileM + static_cast<int>(rank) * 128;
-        const int n0 = u.nt * a.bn + static_cast<int>(rank) * (a.bn / 2);
-        for (int kb = u.k0; kb < u.k1; ++kb) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1, a.err, abort_flag)) { ok = false; break; }
-          const uint32_t full = mapa_shared(smem_u32(&full_bar[stage]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * stage_bytes);
-          uint8_t* dst = smem + stage * stage_bytes;
-          if constexpr (a_mn_major(kKind)) {
-            tma_load_2d_pair(dst, &tmap_a, full, m0, kb * kBK, pol_a);
-            tma_load_2d_pair(dst + kATile / 2, &tmap_a, full, m0 + 64, kb * kBK, pol_a);
-          } else {
-            tma_load_2d_pair(dst, &tmap_a, full, kb * kBK, m0, pol_a);
-          }
-          if constexpr (b_mn_major(kKind)) {
-            tma_load_2d_pair(dst + kATile, &tmap_b, full, n0, kb * kBK, pol_b);
-            tma_load_2d_pair(dst + kATile + kATile / 2, &tmap_b, full, n0 + 64, kb * kBK, pol_b);
-          } else {
-            tma_load_2d_pair(dst + kATile, &tmap_b, full, kb * kBK, n0, pol_b);
-          }
-          ++n_issued;
-          if (++stage == a.n_stages) { stage = 0; phase ^= 1; }
+    // As the MMA warp's, its loop is run by the whole warp: with one lane
+    // running them, the two loops took 500 clocks for a k block, as long as a
+    // tile of 256 columns multiplies and twice as long as one of 128.
+    pdl_wait();
+    const uint32_t elected = elect_one();
+    const uint64_t pol_a = kKind == kDw ? policy_evict_last() : policy_evict_first();
+    const uint64_t pol_b = kKind == kDw ? policy_evict_first() : policy_evict_last();
+    const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
+    const uint32_t leader0 = mapa_shared(full0, 0);
+    const uint32_t smem0 = smem_u32(smem);
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t n_issued = 0;
+    bool ok = true;
+    Unit u;
+    for (int i = 0; ok && unit_at<kKind>(a, pair, i, u); ++i) {
+      const int m0 = u.mt * kTileM + static_cast<int>(rank) * 128;
+      const int n0 = u.nt * a.bn + static_cast<int>(rank) * (a.bn / 2);
+      for (int kb = u.k0; kb < u.k1; ++kb) {
+        ok = mbar_wait_warp(empty0 + stage * 8, phase ^ 1, a.err, abort_flag);
+        if (!ok) break;
+        const uint32_t full = leader0 + stage * 8;
+        const uint32_t dst = smem0 + stage * stage_bytes;
+        if (rank == 0) mbar_arrive_expect_tx_if(elected, full0 + stage * 8, 2 * stage_bytes);
+        if constexpr (a_mn_major(kKind)) {
+          tma_load_2d_pair_if(elected, dst, &tmap_a, full, m0, kb * kBK, pol_a);
+          tma_load_2d_pair_if(elected, dst + kATile / 2, &tmap_a, full, m0 + 64, kb * kBK, pol_a);
+        } else {
+          tma_load_2d_pair_if(elected, dst, &tmap_a, full, kb * kBK, m0, pol_a);
         }
+        if constexpr (b_mn_major(kKind)) {
+          tma_load_2d_pair_if(elected, dst + kATile, &tmap_b, full, n0, kb * kBK, pol_b);
+          tma_load_2d_pair_if(elected, dst + kATile + kATile / 2, &tmap_b, full, n0 + 64, kb * kBK, pol_b);
+        } else {
+          tma_load_2d_pair_if(elected, dst + kATile, &tmap_b, full, kb * kBK, n0, pol_b);
+        }
+        ++n_issued;
+        if (++stage == a.n_stages) { stage = 0; phase ^= 1; }
       }
-      if (!ok && rank == 0) {                            // leave only after the loads in flight have landed
-        volatile int no_abort = 0;
-        for (int64_t i = max(static_cast<int64_t>(0), n_issued - a.n_stages); i < n_issued; ++i)
-          mbar_wait(&full_bar[i % a.n_stages], static_cast<uint32_t>((i / a.n_stages) & 1), a.err, &no_abort);
-      }
+    }
+    if (!ok && rank == 0) {                              // leave only after the loads in flight have landed
+      volatile int no_abort = 0;
+      for (int64_t i = max(static_cast<int64_t>(0), n_issued - a.n_stages); i < n_issued; ++i)
+        mbar_wait_warp(full0 + static_cast<uint32_t>(i % a.n_stages) * 8, static_cast<uint32_t>((i / a.n_stages) & 1), a.err,
+                       &no_abort);
     }
   } else if (warp == kMmaWarp) {
     // -------------------------------------------------------------- MMA issuer (even CTA only)
-    if (lane == 0 && rank == 0) {
+    // The whole warp runs the loop and one elected lane issues.  A stage's
+    // descriptors are the first stage's plus a multiple of its size.
+    if (rank == 0) {
+      const uint32_t elected = elect_one();
       const uint32_t idesc = idesc_bf16_f32(kTileM, static_cast<uint32_t>(a.bn)) |
                              (a_mn_major(kKind) ? kIdescMnMajorA : 0u) | (b_mn_major(kKind) ? kIdescMnMajorB : 0u);
+      const uint32_t smem0 = smem_u32(smem);
+      const uint64_t a_desc0 = a_mn_major(kKind) ? smem_desc_mn128(smem0) : smem_desc_k128(smem0);
+      const uint64_t b_desc0 = b_mn_major(kKind) ? smem_desc_mn128(smem0 + kATile) : smem_desc_k128(smem0 + kATile);
+      const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
+      const uint32_t stage_step = static_cast<uint32_t>(stage_bytes) >> 4;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -257,31 +272,31 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       for (int i = 0; ok && unit_at<kKind>(a, pair, i, u); ++i) {
         for (int kb0 = u.k0; ok && kb0 < u.k1; kb0 += min(sub_blocks(kKind), u.k1 - kb0), ++use) {
           const int acc = use & 1;
-          if (!mbar_wait(&tempty_bar[acc], ((use >> 1) & 1) ^ 1, a.err, abort_flag)) { ok = false; break; }
+          ok = mbar_wait_warp(smem_u32(&tempty_bar[acc]), ((use >> 1) & 1) ^ 1, a.err, abort_flag);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * kMaxN;
-          const int kb1 = kb0 + min(sub_blocks(kKind), u.k1 - kb0);
-          for (int kb = kb0; kb < kb1; ++kb) {
-            if (!mbar_wait(&full_bar[stage], phase, a.err, abort_flag)) { ok = false; break; }
+          const int n_kb = min(sub_blocks(kKind), u.k1 - kb0);
+          for (int kb = 0; kb < n_kb; ++kb) {
+            ok = mbar_wait_warp(full0 + stage * 8, phase, a.err, abort_flag);
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t a_addr = smem_u32(smem + stage * stage_bytes);
-            const uint32_t b_addr = a_addr + kATile;
+            const uint64_t a_desc = a_desc0 + stage * stage_step;
+            const uint64_t b_desc = b_desc0 + stage * stage_step;
 #pragma unroll
             for (int k = 0; k < kBK / 16; ++k)
-              mma_bf16_pair(d_tmem,
-                            a_mn_major(kKind) ? smem_desc_mn128(a_addr + k * 2048) : smem_desc_k128(a_addr + k * 32),
-                            b_mn_major(kKind) ? smem_desc_mn128(b_addr + k * 2048) : smem_desc_k128(b_addr + k * 32),
-                            idesc, kb > kb0 || k > 0);
-            mma_commit_pair_multicast(&empty_bar[stage], kPairMask);     // frees the stage in both CTAs
+              mma_bf16_pair_if(elected, d_tmem, a_desc + k * (a_mn_major(kKind) ? 128 : 2),
+                               b_desc + k * (b_mn_major(kKind) ? 128 : 2), idesc, kb > 0 || k > 0);
+            mma_commit_pair_multicast_if(elected, empty0 + stage * 8, kPairMask);   // frees the stage in both CTAs
             if (++stage == a.n_stages) { stage = 0; phase ^= 1; }
           }
-          if (ok) mma_commit_pair_multicast(&tfull_bar[acc], kPairMask);
+          if (ok) mma_commit_pair_multicast_if(elected, smem_u32(&tfull_bar[acc]), kPairMask);
         }
       }
       if (!ok) {
-        mma_commit_pair_multicast(drain_bar, 0x1);
+        mma_commit_pair_multicast_if(elected, smem_u32(drain_bar), 0x1);
         volatile int no_abort = 0;
-        mbar_wait(drain_bar, 0, a.err, &no_abort);
+        mbar_wait_warp(smem_u32(drain_bar), 0, a.err, &no_abort);
       }
     }
   } else {

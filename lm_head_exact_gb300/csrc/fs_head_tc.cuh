@@ -53,11 +53,13 @@ constexpr int epi_bytes(Kind k) { return epi_arrays(k) * kEpiWarps * kPartCols *
 // The tensor cores add to an accumulator in TMEM by cutting, not rounding: each
 // of the d / 16 additions of a logit loses half a step of the running sum on
 // average, always toward zero, which for d = 4096 shrinks x by 5e-6 and moves
-// lse by 1e-6 of itself.  So logits are accumulated 16 k blocks (1024 products)
-// at a time and the pieces are added in registers, rounding to nearest: a
-// quarter of the error at d = 4096, and no more at larger d.  The gradients,
+// lse by 1e-6 of itself.  So logits are accumulated 32 k blocks (2048 products)
+// at a time and the pieces are added in registers, rounding to nearest: half
+// of that at d = 4096, and no more at larger d.  (16 k blocks halve it again,
+// but then the epilogue of a tile outlasts the two accumulators' products:
+// 405 instead of 345 us for 528 rows of a 4096 x 128256 head.)  The gradients,
 // rounded to 8 bits in the end, take their whole sums.
-constexpr int kSubBlocks = 16;
+constexpr int kSubBlocks = 32;
 constexpr int sub_blocks(Kind k) { return k == kLse || k == kDs ? kSubBlocks : 0x7fffffff; }
 constexpr int kSmemLimit = 232448;
 
@@ -95,33 +97,44 @@ struct Args {
 // (tokens) of one row tile after another, so that W is read once.  kDh: one
 // split after another, so that all pairs work on the same vocabulary rows at a
 // time.  kDw: the row tiles (the model width) of one column tile after another.
-struct Unit {
-  int mt, nt, k0, k1, split;
-};
-
+//
+// The order is a mixed-radix count (for kLse and kDs: column tile, row tile;
+// else: row tile, column tile, split); a pair's step through it is split into
+// digits once, so that moving on takes additions and carries.
 template <Kind kKind>
-__device__ __forceinline__ bool unit_at(const Args& a, int pair, int i, Unit& u) {
-  const int64_t tiles = static_cast<int64_t>(a.n_mt) * a.n_nt;
-  const int64_t at = pair + static_cast<int64_t>(i) * a.n_pairs;
-  if (at >= tiles * a.splits) return false;
-  u.k0 = 0;
-  u.k1 = a.n_kb;
-  u.split = 0;
-  if constexpr (kKind == kLse || kKind == kDs) {
-    u.mt = static_cast<int>(at / a.n_nt);
-    u.nt = static_cast<int>(at % a.n_nt);
-  } else {
-    u.split = static_cast<int>(at / tiles);
-    const int64_t tile = at % tiles;
-    u.mt = static_cast<int>(tile % a.n_mt);
-    u.nt = static_cast<int>(tile / a.n_mt);
-    if constexpr (kKind == kDh) {
-      u.k0 = static_cast<int>(static_cast<int64_t>(a.n_kb) * u.split / a.splits);
-      u.k1 = static_cast<int>(static_cast<int64_t>(a.n_kb) * (u.split + 1) / a.splits);
-    }
+struct Units {
+  static constexpr bool kLogits = kKind == kLse || kKind == kDs;
+  int lo, mid, hi;                             // the digits of the present tile
+  int step_lo, step_mid, step_hi, n_lo, n_mid, n_hi;
+  int n_kb, splits;
+
+  __device__ __forceinline__ Units(const Args& a, int pair)
+      : n_lo(kLogits ? a.n_nt : a.n_mt), n_mid(kLogits ? a.n_mt : a.n_nt), n_hi(a.splits), n_kb(a.n_kb), splits(a.splits) {
+    lo = pair % n_lo;
+    mid = pair / n_lo % n_mid;
+    hi = pair / n_lo / n_mid;
+    step_lo = a.n_pairs % n_lo;
+    step_mid = a.n_pairs / n_lo % n_mid;
+    step_hi = a.n_pairs / n_lo / n_mid;
   }
-  return true;
-}
+  __device__ __forceinline__ bool more() const { return hi < n_hi; }
+  __device__ __forceinline__ void next() {
+    lo += step_lo;
+    mid += step_mid;
+    hi += step_hi;
+    if (lo >= n_lo) { lo -= n_lo; ++mid; }
+    if (mid >= n_mid) { mid -= n_mid; ++hi; }
+  }
+  __device__ __forceinline__ int mt() const { return kLogits ? mid : lo; }
+  __device__ __forceinline__ int nt() const { return kLogits ? lo : mid; }
+  __device__ __forceinline__ int split() const { return hi; }
+  __device__ __forceinline__ int k0() const {
+    return kKind == kDh ? static_cast<int>(static_cast<int64_t>(n_kb) * hi / splits) : 0;
+  }
+  __device__ __forceinline__ int k1() const {
+    return kKind == kDh ? static_cast<int>(static_cast<int64_t>(n_kb) * (hi + 1) / splits) : n_kb;
+  }
+};
 
 // ---------------------------------------------------------------- logit epilogues
 constexpr float kLowest = -3.402823466e38f;  // the lowest finite value
@@ -151,6 +164,12 @@ __device__ __forceinline__ float join_columns(int lane, Join join, Value value) 
 __device__ __forceinline__ LsePart lse_join(LsePart a, LsePart b) {
   const float m = fmaxf(a.m, b.m);
   return LsePart{m, a.s * __expf(a.m - m) + b.s * __expf(b.m - m)};
+}
+
+// ds of a token that is not the row's own; rows without a gradient hold zeros
+// whatever their logits are.
+__device__ __forceinline__ __nv_bfloat16 ds_of(float x, float lse, float coef) {
+  return __float2bfloat16_rn(coef == 0.0f ? 0.0f : -coef * __expf(x - lse));
 }
 
 template <Kind kKind, bool kBias>
@@ -219,11 +238,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
     uint32_t phase = 0;
     int64_t n_issued = 0;
     bool ok = true;
-    Unit u;
-    for (int i = 0; ok && unit_at<kKind>(a, pair, i, u); ++i) {
-      const int m0 = u.mt * kTileM + static_cast<int>(rank) * 128;
-      const int n0 = u.nt * a.bn + static_cast<int>(rank) * (a.bn / 2);
-      for (int kb = u.k0; kb < u.k1; ++kb) {
+    for (Units<kKind> u(a, pair); ok && u.more(); u.next()) {
+      const int m0 = u.mt() * kTileM + static_cast<int>(rank) * 128;
+      const int n0 = u.nt() * a.bn + static_cast<int>(rank) * (a.bn / 2);
+      const int k1 = u.k1();
+      for (int kb = u.k0(); kb < k1; ++kb) {
         ok = mbar_wait_warp(empty0 + stage * 8, phase ^ 1, a.err, abort_flag);
         if (!ok) break;
         const uint32_t full = leader0 + stage * 8;
@@ -267,16 +286,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      Unit u;
       int use = 0;                                       // accumulators taken so far, in turn
-      for (int i = 0; ok && unit_at<kKind>(a, pair, i, u); ++i) {
-        for (int kb0 = u.k0; ok && kb0 < u.k1; kb0 += min(sub_blocks(kKind), u.k1 - kb0), ++use) {
+      for (Units<kKind> u(a, pair); ok && u.more(); u.next()) {
+        const int k1 = u.k1();
+        for (int kb0 = u.k0(), n_kb; ok && kb0 < k1; kb0 += n_kb, ++use) {
+          n_kb = min(sub_blocks(kKind), k1 - kb0);
           const int acc = use & 1;
           ok = mbar_wait_warp(smem_u32(&tempty_bar[acc]), ((use >> 1) & 1) ^ 1, a.err, abort_flag);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d_tmem = tmem_base + acc * kMaxN;
-          const int n_kb = min(sub_blocks(kKind), u.k1 - kb0);
           for (int kb = 0; kb < n_kb; ++kb) {
             ok = mbar_wait_warp(full0 + stage * 8, phase, a.err, abort_flag);
             if (!ok) break;
@@ -313,7 +332,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
     };
-    Unit u;
     if constexpr (kKind == kLse || kKind == kDs) {
       // per warp: 1/T of its columns, then kLse: the columns' largest x,
       // kDs: their lse and coefficients
@@ -324,19 +342,21 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       int64_t id[2] = {-1, -1};                                  // their tokens, as rows of this W
       int nt = -1, use = 0;
       bool ok = cols > 0;
-      for (int i = 0; unit_at<kKind>(a, pair, i, u); ++i) {
-        const int64_t t_first = static_cast<int64_t>(u.nt) * a.bn + col0;
-        const int64_t m_warp = static_cast<int64_t>(u.mt) * kTileM + rank * 128 + quad * 32;
+      for (Units<kKind> u(a, pair); u.more();) {
+        const int mt = u.mt();
+        const int64_t t_first = static_cast<int64_t>(u.nt()) * a.bn + col0;
+        const int n_cols = static_cast<int>(min(static_cast<int64_t>(cols), a.N - t_first));   // that are tokens
+        const int64_t m_warp = static_cast<int64_t>(mt) * kTileM + rank * 128 + quad * 32;
         const int64_t m = m_warp + lane;
         const bool row_ok = m < a.M;
-        if (u.nt != nt) {                                        // other tokens than before
-          nt = u.nt;
+        if (u.nt() != nt) {                                      // other tokens than before
+          nt = u.nt();
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int c = k * 32 + lane;
             const int64_t t = t_first + c;
-            const bool real = c < cols && t < a.N;
+            const bool real = c < n_cols;
             inv_t[c] = real ? row_temp(a.p.temp[t]).inv_t : 0.0f;
             id[k] = real ? a.p.ids[t] : -1;
             if (id[k] >= 0) id[k] -= a.v0;
@@ -361,12 +381,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
             } else {
               b += t_first * a.p.bias_stride;
 #pragma unroll
-              for (int c = 0; c < kPartCols; ++c)
-                if (c < cols && t_first + c < a.N) x[c] = __ldg(b + c * a.p.bias_stride);
+              for (int c = 0; c < kPartCols; ++c, b += a.p.bias_stride)
+                if (c < n_cols) x[c] = __ldg(b);
             }
           }
         }
-        for (int kb0 = u.k0; kb0 < u.k1; kb0 += min(kSubBlocks, u.k1 - kb0), ++use) {
+        for (int kb0 = 0; kb0 < a.n_kb; kb0 += kSubBlocks, ++use) {
           const int acc = use & 1;
           if (!mbar_wait(&tfull_bar[acc], (use >> 1) & 1, a.err, abort_flag)) { ok = false; break; }
           tc_fence_after();
@@ -381,18 +401,25 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
           }
           release(acc);
         }
+        u.next();
         if (!ok) {                                               // a wait gave up, or this warp has no columns
           if (cols > 0) break;
           continue;
         }
 #pragma unroll
-        for (int c = 0; c < kPartCols; ++c) x[c] = row_ok ? x[c] * inv_t[c] : -INFINITY;
+        for (int c = 0; c < kPartCols; c += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(inv_t + c);
+          x[c + 0] = row_ok ? x[c + 0] * f.x : -INFINITY;
+          x[c + 1] = row_ok ? x[c + 1] * f.y : -INFINITY;
+          x[c + 2] = row_ok ? x[c + 2] * f.z : -INFINITY;
+          x[c + 3] = row_ok ? x[c + 3] * f.w : -INFINITY;
+        }
         if constexpr (kKind == kLse) {
           if (a.kept != nullptr && row_ok) {
             float* dst = a.kept + t_first * a.kept_pitch + m;
 #pragma unroll
-            for (int c = 0; c < kPartCols; ++c)
-              if (c < cols && t_first + c < a.N) __stcs(dst + c * a.kept_pitch, x[c]);
+            for (int c = 0; c < kPartCols; ++c, dst += a.kept_pitch)
+              if (c < n_cols) __stcs(dst, x[c]);
           }
           // of each column the largest x, then the sum of exp(x - largest)
 #pragma unroll
@@ -407,14 +434,17 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
                                            [&](int c) { return __expf(x[k * 32 + c] - second[k * 32 + c]); });
             part[k] = lse_join(part[k], LsePart{top, sum});
           }
-        } else {
+        } else if (row_ok) {
           __nv_bfloat16* dst = a.ds + t_first * a.ds_pitch + m;
 #pragma unroll
-          for (int c = 0; c < kPartCols; ++c) {
-            if (c < cols && t_first + c < a.N && row_ok) {
-              const float coef = third[c];
-              dst[c * a.ds_pitch] = __float2bfloat16_rn(coef == 0.0f ? 0.0f : -coef * __expf(x[c] - second[c]));
-            }
+          for (int c = 0; c < kPartCols; c += 4) {
+            const float4 z = *reinterpret_cast<const float4*>(second + c);
+            const float4 f = *reinterpret_cast<const float4*>(third + c);
+            if (c + 0 < n_cols) dst[0] = ds_of(x[c + 0], z.x, f.x);
+            if (c + 1 < n_cols) dst[a.ds_pitch] = ds_of(x[c + 1], z.y, f.y);
+            if (c + 2 < n_cols) dst[2 * a.ds_pitch] = ds_of(x[c + 2], z.z, f.z);
+            if (c + 3 < n_cols) dst[3 * a.ds_pitch] = ds_of(x[c + 3], z.w, f.w);
+            dst += 4 * a.ds_pitch;
           }
         }
         // a token's own logit lies in few tiles: looked for by ballots
@@ -439,25 +469,25 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
         }
         if constexpr (kKind == kLse) {
           // with one column tile the pair's tiles share a part, else each has its own
-          Unit next;
-          if (a.n_nt > 1 || !unit_at<kKind>(a, pair, i + 1, next)) {
-            const int64_t which = (a.n_nt > 1 ? u.mt : pair) * 8 + rank * 4 + quad;
+          if (a.n_nt > 1 || !u.more()) {
+            const int64_t which = static_cast<int64_t>(a.n_nt > 1 ? mt : pair) * 8 + rank * 4 + quad;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int c = k * 32 + lane;
-              if (c < cols && t_first + c < a.N) a.parts[which * a.N + t_first + c] = part[k];
+              if (c < n_cols) a.parts[which * a.N + t_first + c] = part[k];
               part[k] = LsePart{kLowest, 0.0f};
             }
           }
         }
       }
     } else {
-      for (int i = 0; unit_at<kKind>(a, pair, i, u); ++i) {
-        const int acc = i & 1;
-        if (!mbar_wait(&tfull_bar[acc], (i >> 1) & 1, a.err, abort_flag)) break;
+      int use = 0;
+      for (Units<kKind> u(a, pair); u.more(); u.next(), ++use) {
+        const int acc = use & 1;
+        if (!mbar_wait(&tfull_bar[acc], (use >> 1) & 1, a.err, abort_flag)) break;
         tc_fence_after();
-        const int64_t m = static_cast<int64_t>(u.mt) * kTileM + rank * 128 + quad * 32 + lane;
-        const int64_t n_first = static_cast<int64_t>(u.nt) * a.bn + col0;
+        const int64_t m = static_cast<int64_t>(u.mt()) * kTileM + rank * 128 + quad * 32 + lane;
+        const int64_t n_first = static_cast<int64_t>(u.nt()) * a.bn + col0;
         const bool row_ok = m < a.M;
 #pragma unroll 1
         for (int c = 0; c < cols; c += 16) {
@@ -470,7 +500,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
             if (n >= a.N || !row_ok) continue;
             const float y = __uint_as_float(r[j]);
             if constexpr (kKind == kDh) {
-              float* at = a.partials + (static_cast<int64_t>(u.split) * a.N + n) * a.M + m;
+              float* at = a.partials + (static_cast<int64_t>(u.split()) * a.N + n) * a.M + m;
               *at = a.add ? *at + y : y;
             } else {
               a.grad_W[(a.v0 + n) * a.M + m] = __float2bfloat16_rn(y);

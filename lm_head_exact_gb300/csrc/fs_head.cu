@@ -18,52 +18,66 @@ namespace {
 
 using head::lse_join;
 
-// Merge of the parts [n_parts, n] of kMergeRows tokens a block: every thread
-// joins every 128th part of one token, then the block's threads are joined.
-constexpr int kMergeRows = 8;
-constexpr int kMergeThreads = 1024;
+// Merge of the parts [n_parts, n] of kMergeRows tokens a block.  Every thread
+// joins every 64th part of one token, 8 loads in flight and one rescaling for
+// each 8 (one at a time took three times as long: the loads waited for the
+// exponentials); then the block's threads are joined.
+constexpr int kMergeRows = 4;
+constexpr int kMergeThreads = 256;
 
 __global__ void __launch_bounds__(kMergeThreads) head_merge_kernel(const HeadProblem p, const LsePart* parts,
                                                                    int64_t n_parts, const float* own_x, float* logp,
                                                                    float* lse) {
   __shared__ LsePart warps[kMergeThreads / 32][kMergeRows];
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x & (kMergeRows - 1));
+  constexpr int kSlices = kMergeThreads / kMergeRows;
+  const int row = threadIdx.x & (kMergeRows - 1);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kMergeRows + row;
+  pdl_launch_dependents();
+  pdl_wait();
   LsePart part{head::kLowest, 0.0f};
   if (t < p.n) {
-#pragma unroll 4
-    for (int64_t i = threadIdx.x / kMergeRows; i < n_parts; i += kMergeThreads / kMergeRows)
-      part = lse_join(part, parts[i * p.n + t]);
+    for (int64_t i = threadIdx.x / kMergeRows; i < n_parts; i += 8 * kSlices) {
+      LsePart v[8];
+      float m = part.m;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = LsePart{head::kLowest, 0.0f};
+        if (i + k * kSlices < n_parts) v[k] = parts[(i + k * kSlices) * p.n + t];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, v[k].m);
+      part.s *= __expf(part.m - m);
+      part.m = m;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) part.s += v[k].s * __expf(v[k].m - m);
+    }
   }
 #pragma unroll
   for (int o = 16; o >= kMergeRows; o >>= 1)
     part = lse_join(part, LsePart{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o)});
-  if ((threadIdx.x & 31) < kMergeRows) warps[threadIdx.x >> 5][threadIdx.x & (kMergeRows - 1)] = part;
+  if ((threadIdx.x & 31) < kMergeRows) warps[threadIdx.x >> 5][row] = part;
   __syncthreads();
-  if (threadIdx.x >= 32 * kMergeRows) return;
-  // one warp a token
-  const int row = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kMergeRows + row;
-  part = warps[lane][row];
+  if (threadIdx.x >= kMergeRows || t >= p.n) return;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    part = lse_join(part, LsePart{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o)});
-  if (lane != 0 || mine >= p.n) return;
-  const bool valid = row_temp(p.temp[mine]).mode != kRowInvalid;
-  const int64_t id = p.ids[mine];
+  for (int w = 1; w < kMergeThreads / 32; ++w) part = lse_join(part, warps[w][row]);
+  const bool valid = row_temp(p.temp[t]).mode != kRowInvalid;
+  const int64_t id = p.ids[t];
   float z = !valid || part.s == 0.0f ? -INFINITY : part.m + logf(part.s);
   if (valid && !(part.s < INFINITY)) z = NAN;           // a NaN or infinite logit
-  lse[mine] = z;
+  lse[t] = z;
   float lp = 0.0f;
   if (valid && id >= 0 && id < p.V) {
-    const float x = own_x[mine];
+    const float x = own_x[t];
     lp = x == -INFINITY ? -INFINITY : x - z;
   }
-  logp[mine] = lp;
+  logp[t] = lp;
 }
 
 __global__ void __launch_bounds__(256) head_rows_kernel(const HeadProblem p, const float* logp, const float* lse,
                                                         const float* g, float* coef, __nv_bfloat16* h_live) {
   const int64_t t = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
   const RowTemp rt = row_temp(p.temp[t]);
   const int64_t id = p.ids[t];
   const bool live = rt.mode != kRowInvalid && id >= 0 && id < p.V && g[t] != 0.0f && lse[t] != -INFINITY &&
@@ -83,6 +97,8 @@ __global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, 
                                                            const float* kept, int64_t kept_pitch, int64_t v0,
                                                            __nv_bfloat16* ds, int64_t pitch) {
   const int64_t t = blockIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
   const float c = coef[t], z = lse[t];
   const int64_t id = p.ids[t] - v0;
   const float* src = kept + t * kept_pitch + v0;
@@ -110,6 +126,8 @@ __global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, 
 __global__ void __launch_bounds__(256) head_dh_sum_kernel(const HeadProblem p, const float* partials, int64_t splits,
                                                           const float* coef, __nv_bfloat16* grad_h) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;     // d is a multiple of 8
+  pdl_launch_dependents();
+  pdl_wait();
   if (i >= p.n * p.d) return;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (coef[i / p.d] != 0.0f) {
@@ -128,6 +146,12 @@ __global__ void __launch_bounds__(256) head_dh_sum_kernel(const HeadProblem p, c
 }
 
 // ---------------------------------------------------------------- launch geometry
+// The products, and the small kernels that follow a small kernel, are launched
+// as programmatic dependents: each waits for the one before it
+// (griddepcontrol.wait) before it reads or writes global memory, so only its
+// start-up overlaps.  The small kernels after a product are launched plainly:
+// as dependents they slowed the next product's start down by more than they
+// gained (scores of 257 rows, width 520: 37 and 43 us).
 using head::Args;
 using head::Kind;
 
@@ -194,7 +218,7 @@ cudaError_t launch(const Args& a, const CUtensorMap& ta, const CUtensorMap& tb, 
   if (e == cudaSuccess) e = raise_smem_limit<head::gemm_kernel<kKind, kBias>>(dev, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(head::gemm_kernel<kKind, kBias>, dim3(static_cast<unsigned>(2 * a.n_pairs)),
-                       dim3(head::kThreads), smem, stream, false, ta, tb, a);
+                       dim3(head::kThreads), smem, stream, true, ta, tb, a);
 }
 
 int pairs_for(int64_t units) { return static_cast<int>(std::min<int64_t>(resident_pairs(), units)); }
@@ -250,7 +274,7 @@ cudaError_t launch_head_merge(const HeadProblem& p, const LsePart* parts, int64_
 
 cudaError_t launch_head_rows(const HeadProblem& p, const float* logp, const float* lse, const float* g, float* coef,
                              void* h_live, cudaStream_t stream) {
-  return launch_kernel(head_rows_kernel, dim3(static_cast<unsigned>(p.n)), dim3(256), 0, stream, false, p, logp, lse,
+  return launch_kernel(head_rows_kernel, dim3(static_cast<unsigned>(p.n)), dim3(256), 0, stream, true, p, logp, lse,
                        g, coef, static_cast<__nv_bfloat16*>(h_live));
 }
 
@@ -261,7 +285,7 @@ cudaError_t launch_head_ds(const HeadProblem& p, const float* lse, const float* 
   if (kept != nullptr) {
     const int64_t blocks = std::min<int64_t>((pitch + 2047) / 2048, 64);
     return launch_kernel(head_ds_kept_kernel, dim3(static_cast<unsigned>(p.n), static_cast<unsigned>(blocks)),
-                         dim3(256), 0, stream, false, p, lse, coef, kept, padded_cols(p.V), v0, out, pitch);
+                         dim3(256), 0, stream, true, p, lse, coef, kept, padded_cols(p.V), v0, out, pitch);
   }
   Args a{};
   a.p = p;

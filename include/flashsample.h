@@ -335,17 +335,21 @@ FS_API fs_status fs_sample_noalloc(const void* h, const void* W, int64_t B, int6
  * Learning from sampled tokens: their log-probabilities through the LM head
  * with gradients, the clipped policy loss, and clipping by the global
  * gradient norm.  Same conventions as above (shapes, alignment, streams,
- * errors).  These calls take their workspace from the caller (16-byte
- * aligned device memory whose contents need not survive the call), apart
- * from a fixed 64 KB block per (device, stream) that the library allocates on
- * the first call; that block is part of fs_workspace_reserve(), which makes
- * them capturable.
+ * errors).  These calls take their workspace from the caller: 16-byte
+ * aligned device memory whose contents need not survive the call, or NULL
+ * where FS_SMALL_WORKSPACE bytes suffice.  Those, block sums and tickets lie in
+ * a fixed block (0.6 MB) per (device, stream) that the library allocates on
+ * the first call; it is part of fs_workspace_reserve(), which makes the calls
+ * capturable.  A captured graph uses the block of the stream it was captured
+ * on: keep its replays ordered with that stream's other calls.
  *
  * A row t takes part ("is scored") when 0 <= ids[t] < V and its temperature
  * is valid.  T > 0 divides the logits; T == 0 scores under softmax(logits),
  * the logits being what greedy sampling compares; T < 0 or NaN: the row is
  * not scored.
  * ------------------------------------------------------------------------ */
+
+#define FS_SMALL_WORKSPACE 524288
 
 /*
  * Log-probabilities of given tokens, fused into the LM-head matmul: with

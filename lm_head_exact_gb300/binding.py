@@ -9,6 +9,8 @@ there is no CPU fallback.
 import ctypes
 import os
 from array import array
+from functools import lru_cache
+from operator import attrgetter
 
 import numpy as np
 
@@ -24,6 +26,7 @@ FS_FAULT_NONE, FS_FAULT_ALLOC, FS_FAULT_LAUNCH = 0, 1, 2
 FS_MEAN_TOKEN, FS_MEAN_SEQUENCE, FS_MEAN_NONE = 0, 1, 2
 FS_TYPE_F32, FS_TYPE_BF16, FS_TYPE_F16 = 0, 1, 2
 FS_NORM_L2, FS_NORM_MAX = 0, 1
+FS_SMALL_WORKSPACE = 524288
 
 _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -445,39 +448,64 @@ def _stream_of(t, stream):
 
 def _head_args(h, W, ids, temp, bias):
     torch = _torch()
-    if getattr(h, "ndim", 0) != 2 or getattr(W, "ndim", 0) != 2 or h.shape[1] != W.shape[1]:
+    try:
+        (n, d), (V, d2) = h.shape, W.shape
+    except (AttributeError, ValueError):
+        d, d2 = 0, 1
+    if d != d2:
         raise FlashSampleError("FS_ERR_INVALID_ARG", "h must be [n, d] and W [V, d]")
-    n, d = h.shape
-    V = W.shape[0]
-    if bias is not None and tuple(bias.shape) not in ((n, V), (V,)):
-        raise FlashSampleError("FS_ERR_INVALID_ARG", f"bias must be [n, V] or [V], got {tuple(bias.shape)}")
-    bptr, bstride = _bias_args(bias, n, V) if bias is not None else (None, 0)
+    bptr, bstride = None, 0
+    if bias is not None:
+        if tuple(bias.shape) not in ((n, V), (V,)):
+            raise FlashSampleError("FS_ERR_INVALID_ARG", f"bias must be [n, V] or [V], got {tuple(bias.shape)}")
+        bptr, bstride = _bias_args(bias, n, V)
     return (_arg(h, "h", torch.bfloat16), _arg(W, "W", torch.bfloat16), n, d, V,
             _arg(ids, "ids", torch.int64, (n,)), _arg(temp, "temp", torch.float32, (n,)), bptr, bstride)
 
 
+# bytes of workspace by sizes alone
+@lru_cache(maxsize=256)
+def _forward_bytes(n, d, V):
+    return library().fs_token_logprobs_workspace_bytes(n, d, V)
+
+
+@lru_cache(maxsize=256)
+def _backward_bytes(n, d, V):
+    return library().fs_token_logprobs_backward_workspace_bytes(n, d, V)
+
+
+@lru_cache(maxsize=256)
+def _kept_elems(n, V):
+    return library().fs_logprob_buffer_elems(n, V)
+
+
 def _workspace(nbytes, device, stream):
-    """Device memory for one call, allocated on the stream that the call runs
-    on: it may be handed out again as soon as this returns to the caller, but
-    only to work that follows on that stream."""
+    """(tensor, address) of device memory for one call, allocated on the
+    stream that the call runs on: it may be handed out again as soon as the
+    call returns, but only to work that follows on that stream.  Small ones
+    come from the library's own block (NULL)."""
+    if nbytes <= FS_SMALL_WORKSPACE:
+        return None, None
     torch = _torch()
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t, t.data_ptr()
 
 
 def logprob_buffer(n, V, device="cuda"):
     """The fp32 buffer in which ``token_logprobs`` leaves the logits of n rows
     for ``token_logprobs_backward``."""
-    return _torch().empty(library().fs_logprob_buffer_elems(n, V), dtype=_torch().float32, device=device)
+    return _torch().empty(_kept_elems(n, V), dtype=_torch().float32, device=device)
 
 
 def _kept_arg(kept, n, V):
     torch = _torch()
     if kept is None:
         return None
-    if kept.numel() != library().fs_logprob_buffer_elems(n, V):
+    if kept.numel() != _kept_elems(n, V):
         raise FlashSampleError("FS_ERR_INVALID_ARG", "kept must be logprob_buffer(n, V)")
     return _arg(kept, "kept", torch.float32)
 
@@ -497,10 +525,11 @@ def token_logprobs(h, W, ids, temp, bias=None, kept=None, out=None, stream=None)
     if out is None:
         out = (torch.empty_like(temp), torch.empty_like(temp))
     logp, lse = out
-    lib = library()
-    work = _workspace(lib.fs_token_logprobs_workspace_bytes(n, d, V), h.device, stream)
-    check(lib.fs_token_logprobs(*args, _arg(logp, "logp", torch.float32, (n,)), _arg(lse, "lse", torch.float32, (n,)),
-                                _kept_arg(kept, n, V), work.data_ptr(), work.numel(), _stream_of(h, stream)))
+    nbytes = _forward_bytes(n, d, V)
+    work, where = _workspace(nbytes, h.device, stream)
+    check(library().fs_token_logprobs(
+        *args, _arg(logp, "logp", torch.float32, (n,)), _arg(lse, "lse", torch.float32, (n,)), _kept_arg(kept, n, V),
+        where, nbytes, _stream_of(h, stream)))
     return logp, lse
 
 
@@ -519,14 +548,14 @@ def token_logprobs_backward(h, W, ids, temp, logp, lse, grad_logp, bias=None, ke
         grad_h = torch.empty_like(h)
     if need_W and grad_W is None:
         grad_W = torch.empty_like(W)
-    lib = library()
-    work = _workspace(lib.fs_token_logprobs_backward_workspace_bytes(n, d, V), h.device, stream)
-    check(lib.fs_token_logprobs_backward(
+    nbytes = _backward_bytes(n, d, V)
+    work, where = _workspace(nbytes, h.device, stream)
+    check(library().fs_token_logprobs_backward(
         *args, _arg(logp, "logp", torch.float32, (n,)), _arg(lse, "lse", torch.float32, (n,)),
         _arg(grad_logp, "grad_logp", torch.float32, (n,)), _kept_arg(kept, n, V),
         _arg(grad_h, "grad_h", torch.bfloat16, (n, d)) if need_h else None,
         _arg(grad_W, "grad_W", torch.bfloat16, (V, d)) if need_W else None,
-        work.data_ptr(), work.numel(), _stream_of(h, stream)))
+        where, nbytes, _stream_of(h, stream)))
     return grad_h if need_h else None, grad_W if need_W else None
 
 
@@ -572,19 +601,20 @@ def policy_loss(logp, old_logp, advantages, seq_starts=None, mask=None, ref_logp
         out = torch.empty(4, dtype=f32, device=logp.device), torch.empty_like(logp)
     stats, grad = out
     lib = library()
-    work, nbytes = None, 0
+    work, where, nbytes = None, None, 0
     if mean == "sequence":                    # one count for each sequence
         nbytes = lib.fs_policy_loss_workspace_bytes(S)
-        work = _workspace(nbytes, logp.device, stream)
+        work, where = _workspace(nbytes, logp.device, stream)
     check(lib.fs_policy_loss(
         ptr, _arg(old_logp, "old_logp", f32, shape), None if ref_logp is None else _arg(ref_logp, "ref_logp", f32, shape),
         adv, 1 if adv_per_seq else 0, None if mask is None else _arg(mask, "mask", torch.bool, shape), starts, S, N,
         clip_low, clip_high, kl_coef, _MEANS[mean], _arg(stats, "stats", f32, (4,)), _arg(grad, "grad", f32, shape),
-        None if work is None else work.data_ptr(), nbytes, _stream_of(logp, stream)))
+        where, nbytes, _stream_of(logp, stream)))
     return stats, grad
 
 
 _CLIP_TYPES = {}
+_DTYPE = attrgetter("dtype")
 
 
 def clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, stream=None):
@@ -600,24 +630,27 @@ def clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, stream=None):
         _CLIP_TYPES.update({torch.float32: FS_TYPE_F32, torch.bfloat16: FS_TYPE_BF16, torch.float16: FS_TYPE_F16})
     grads = list(grads)
     n = len(grads)
-    types = array("i")
-    for g in grads:
-        kind = _CLIP_TYPES.get(g.dtype)
-        if kind is None or not g.is_cuda or not g.is_contiguous():
-            raise FlashSampleError("FS_ERR_INVALID_ARG", "gradients must be contiguous fp32, bf16 or fp16 CUDA "
-                                   "tensors (no CPU fallback)")
-        types.append(kind)
-    pointers = array("Q", [g.data_ptr() for g in grads])
-    outs = pointers
+    tensor = torch.Tensor
+    try:                                      # (maps: a dozen Python steps for each tensor cost more than the kernels)
+        dtypes = list(map(_DTYPE, grads))
+        types = array("i", map(_CLIP_TYPES.__getitem__, dtypes))
+        fine = all(map(tensor.is_contiguous, grads)) and (n == 0 or grads[0].is_cuda)   # (the library checks each)
+    except (AttributeError, KeyError, TypeError):
+        fine = False
+    if not fine:
+        raise FlashSampleError("FS_ERR_INVALID_ARG", "gradients must be contiguous fp32, bf16 or fp16 CUDA tensors "
+                               "(no CPU fallback)")
+    pointers = outs = array("Q", map(tensor.data_ptr, grads))
+    sizes = array("q", map(tensor.numel, grads))
     if out is not None:
+        out = list(out)
         if len(out) != n:
             raise FlashSampleError("FS_ERR_INVALID_ARG", f"out must hold {n} tensors, got {len(out)}")
-        for g, o in zip(grads, out):
-            if o.dtype is not g.dtype or o.shape != g.shape or not o.is_cuda or not o.is_contiguous():
-                raise FlashSampleError("FS_ERR_INVALID_ARG", "an output must be a contiguous CUDA tensor of its "
-                                       "gradient's type and shape")
-        outs = array("Q", [o.data_ptr() for o in out])
-    sizes = array("q", [g.numel() for g in grads])
+        if (list(map(_DTYPE, out)) != dtypes or array("q", map(tensor.numel, out)) != sizes
+                or not all(map(tensor.is_contiguous, out))):
+            raise FlashSampleError("FS_ERR_INVALID_ARG", "an output must be a contiguous CUDA tensor of its "
+                                   "gradient's type and shape")
+        outs = array("Q", map(tensor.data_ptr, out))
     norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
     check(library().fs_clip_grad_norm(pointers.buffer_info()[0], outs.buffer_info()[0], sizes.buffer_info()[0],
                                       types.buffer_info()[0], n, max_norm,

@@ -14,13 +14,14 @@ namespace fs {
 // that used them leaves them so.  Calls on one stream are ordered, so they
 // may share it.
 constexpr int kTrainMaxBlocks = 2048;
-struct TrainScratch {
+struct alignas(256) TrainScratch {
   unsigned int ticket;
   unsigned int pad;
   unsigned long long count;             // tokens (or sequences) that take part
   float coef;                           // clip_grad_norm: the factor of the scaling launch
   float pad2[3];
   double sums[kTrainMaxBlocks][4];      // one row per block
+  alignas(256) unsigned char small[FS_SMALL_WORKSPACE];   // workspace of calls that bring none
 };
 
 void api_begin();                       // clears fs_last_error()

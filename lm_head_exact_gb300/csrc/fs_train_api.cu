@@ -74,9 +74,17 @@ BackwardWorkspace backward_workspace(void* base, int64_t n, int64_t d, int64_t V
   return w;
 }
 
-fs_status check_workspace(const void* workspace, size_t have, size_t need) {
+// The memory that a call works in: the caller's, or the library's own block
+// where that suffices.
+fs_status find_workspace(void** workspace, size_t have, size_t need, cudaStream_t stream) {
+  if (*workspace == nullptr && need <= FS_SMALL_WORKSPACE) {
+    TrainScratch* scratch = nullptr;
+    FS_API_TRY(api_train_scratch(stream, &scratch));
+    *workspace = scratch->small;
+    return FS_OK;
+  }
   if (have < need) return api_fail(FS_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", have, need);
-  return api_check_array(workspace, 16, "workspace");
+  return api_check_array(*workspace, 16, "workspace");
 }
 
 fs_status check_head(const HeadProblem& p) {
@@ -127,9 +135,9 @@ fs_status fs_token_logprobs(const void* h, const void* W, int64_t n, int64_t d, 
   FS_API_TRY(api_check_array(logp, 4, "logp"));
   FS_API_TRY(api_check_array(lse, 4, "lse"));
   if (kept != nullptr) FS_API_TRY(api_check_array(kept, 16, "kept"));
-  const ForwardWorkspace w = forward_workspace(workspace, n, V);
-  FS_API_TRY(check_workspace(workspace, workspace_bytes, w.bytes));
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  FS_API_TRY(find_workspace(&workspace, workspace_bytes, forward_workspace(nullptr, n, V).bytes, stream));
+  const ForwardWorkspace w = forward_workspace(workspace, n, V);
   int* err = nullptr;
   FS_API_TRY(api_error_word(&err, stream));
   FS_API_TRY(api_check_launch());
@@ -170,9 +178,9 @@ fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, in
       (grad_W != nullptr && (overlaps(grad_W, vd, h, nd) || overlaps(grad_W, vd, W, vd))) ||
       (grad_h != nullptr && grad_W != nullptr && overlaps(grad_h, nd, grad_W, vd)))
     return api_fail(FS_ERR_INVALID_ARG, "grad_h and grad_W must not overlap each other, h or W");
-  const BackwardWorkspace w = backward_workspace(workspace, n, d, V);
-  FS_API_TRY(check_workspace(workspace, workspace_bytes, w.bytes));
   if (grad_h == nullptr && grad_W == nullptr) return FS_OK;
+  FS_API_TRY(find_workspace(&workspace, workspace_bytes, backward_workspace(nullptr, n, d, V).bytes, stream));
+  const BackwardWorkspace w = backward_workspace(workspace, n, d, V);
   int* err = nullptr;
   FS_API_TRY(api_error_word(&err, stream));
   FS_API_TRY(api_check_launch());
@@ -226,7 +234,7 @@ fs_status fs_policy_loss(const float* logp, const float* old_logp, const float* 
   if (seq_starts != nullptr) FS_API_TRY(api_check_array(seq_starts, 8, "seq_starts"));
   FS_API_TRY(api_check_array(grad, 4, "grad"));
   if (mean == FS_MEAN_SEQUENCE)
-    FS_API_TRY(check_workspace(workspace, workspace_bytes, fs_policy_loss_workspace_bytes(n_seqs)));
+    FS_API_TRY(find_workspace(&workspace, workspace_bytes, fs_policy_loss_workspace_bytes(n_seqs), stream));
   TrainScratch* scratch = nullptr;
   FS_API_TRY(api_train_scratch(stream, &scratch));
   FS_API_TRY(api_check_launch());

@@ -176,12 +176,14 @@ int k_blocks(int64_t k) { return static_cast<int>((k + head::kBK - 1) / head::kB
 template <Kind kKind>
 int stages_for(int bn) {
   return std::min(head::kMaxStages,
-                  (head::kSmemLimit - 1024 - head::kBarBytes - head::epi_bytes(kKind)) / (head::kATile + bn * head::kBK));
+                  (head::kSmemLimit - 1024 - head::kBarBytes - head::epi_bytes(kKind) - head::out_bytes(kKind)) /
+                      (head::kATile + bn * head::kBK));
 }
 
 template <Kind kKind>
 int smem_for(int bn) {
-  return stages_for<kKind>(bn) * (head::kATile + bn * head::kBK) + head::kBarBytes + head::epi_bytes(kKind) + 1024;
+  return stages_for<kKind>(bn) * (head::kATile + bn * head::kBK) + head::kBarBytes + head::epi_bytes(kKind) +
+         head::out_bytes(kKind) + 1024;
 }
 
 // Pairs that can be resident at once: a pair needs two SMs of one cluster
@@ -211,14 +213,15 @@ int resident_pairs() {
 }
 
 template <Kind kKind, bool kBias>
-cudaError_t launch(const Args& a, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t stream) {
+cudaError_t launch(const Args& a, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tout,
+                   cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   const int smem = smem_for<kKind>(a.bn);
   if (e == cudaSuccess) e = raise_smem_limit<head::gemm_kernel<kKind, kBias>>(dev, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(head::gemm_kernel<kKind, kBias>, dim3(static_cast<unsigned>(2 * a.n_pairs)),
-                       dim3(head::kThreads), smem, stream, true, ta, tb, a);
+                       dim3(head::kThreads), smem, stream, true, ta, tb, tout, a);
 }
 
 int pairs_for(int64_t units) { return static_cast<int>(std::min<int64_t>(resident_pairs(), units)); }
@@ -242,7 +245,7 @@ cudaError_t launch_logits(Args a, int64_t v0, int64_t vc, cudaStream_t stream) {
   a.splits = 1;
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
   a.v0 = v0;
-  return p.bias != nullptr ? launch<kKind, true>(a, tw, th, stream) : launch<kKind, false>(a, tw, th, stream);
+  return p.bias != nullptr ? launch<kKind, true>(a, tw, th, tw, stream) : launch<kKind, false>(a, tw, th, tw, stream);
 }
 
 }  // namespace
@@ -341,7 +344,7 @@ cudaError_t launch_head_dh(const HeadProblem& p, const void* ds, int64_t v0, int
   a.partials = partials;
   a.add = add;
   a.err = err;
-  return launch<head::kDh, false>(a, tw, ts, stream);
+  return launch<head::kDh, false>(a, tw, ts, tw, stream);
 }
 
 cudaError_t launch_head_dh_sum(const HeadProblem& p, const float* partials, int64_t splits, const float* coef,
@@ -352,25 +355,25 @@ cudaError_t launch_head_dh_sum(const HeadProblem& p, const float* partials, int6
 
 cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_live, int64_t v0, int64_t vc,
                            void* grad_W, int* err, cudaStream_t stream) {
-  CUtensorMap th, ts;
-  if (!encode_rows_bf16(&th, h_live, p.n, p.d, p.d, head::kBK) ||
-      !encode_rows_bf16(&ts, ds, p.n, vc, padded_cols(vc), head::kBK))
-    return cudaErrorInvalidValue;
   Args a{};
   a.p = p;
-  a.M = p.d;
-  a.N = vc;
-  a.bn = head::kMaxN;
+  a.M = vc;
+  a.N = p.d;
+  a.bn = p.d <= 128 ? 128 : head::kMaxN;
+  CUtensorMap th, ts, tg;
+  if (!encode_rows_bf16(&ts, ds, p.n, vc, padded_cols(vc), head::kBK) ||
+      !encode_rows_bf16(&th, h_live, p.n, p.d, p.d, head::kBK) ||
+      !encode_rows_bf16(&tg, static_cast<uint16_t*>(grad_W) + v0 * p.d, vc, p.d, p.d, 32))
+    return cudaErrorInvalidValue;
   a.n_stages = stages_for<head::kDw>(a.bn);
-  a.n_nt = static_cast<int>((vc + a.bn - 1) / a.bn);
-  a.n_mt = row_tiles(p.d);
+  a.n_nt = static_cast<int>((p.d + a.bn - 1) / a.bn);
+  a.n_mt = row_tiles(vc);
   a.n_kb = k_blocks(p.n);
   a.splits = 1;
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
   a.v0 = v0;
-  a.grad_W = static_cast<__nv_bfloat16*>(grad_W);
   a.err = err;
-  return launch<head::kDw, false>(a, th, ts, stream);
+  return launch<head::kDw, false>(a, ts, th, tg, stream);
 }
 
 }  // namespace fs

@@ -5,13 +5,14 @@
 //   kLse  x^T  = W h^T          each tile reduced to its columns' sums of exp
 //   kDs   ds^T from x^T         the same product, written as bf16 ds
 //   kDh   grad_h^T = W^T ds^T   split along the vocabulary, fp32 partials
-//   kDw   grad_W^T = h^T ds
+//   kDw   grad_W = ds^T h
 //
-// All are formed TRANSPOSED: the axis that is contiguous in memory (vocabulary
-// ids of x and ds, the model width of the gradients) lies on the MMA's M axis,
-// that is on the 32 lanes of a warp, so the epilogues load and store whole
-// lines; and the tokens lie on N, whose size is any multiple of 16, so a batch
-// of 517 tokens runs as 3 x 176 columns instead of 3 x 256 rows.
+// The axis that a tile's epilogue stores along lies on the MMA's M axis, that
+// is on the 32 lanes of a warp (vocabulary ids of x and ds, the model width of
+// grad_h), so it loads and stores whole lines; and the tokens lie on N, whose
+// size is any multiple of 16, so a batch of 517 tokens runs as 3 x 176 columns
+// instead of 3 x 256 rows.  grad_W has the model width on N: its rows go
+// through shared memory and leave by TMA.
 #pragma once
 
 #include <cuda.h>
@@ -61,6 +62,10 @@ constexpr int epi_bytes(Kind k) { return epi_arrays(k) * kEpiWarps * kPartCols *
 // rounded to 8 bits in the end, take their whole sums.
 constexpr int kSubBlocks = 32;
 constexpr int sub_blocks(Kind k) { return k == kLse || k == kDs ? kSubBlocks : 0x7fffffff; }
+// kDw: a box of 32 vocabulary rows x 64 columns of bf16 a warp, on its way out.
+constexpr int kBoxCols = 64;
+constexpr int kBoxBytes = 32 * kBoxCols * 2;
+constexpr int out_bytes(Kind k) { return k == kDw ? kEpiWarps * kBoxBytes : 0; }
 constexpr int kSmemLimit = 232448;
 
 struct Args {
@@ -87,8 +92,6 @@ struct Args {
   // kDh
   float* partials;
   bool add;
-  // kDw
-  __nv_bfloat16* grad_W;
   int* err;
 };
 
@@ -96,20 +99,21 @@ struct Args {
 // run side by side share what is read from HBM.  kLse and kDs: the column tiles
 // (tokens) of one row tile after another, so that W is read once.  kDh: one
 // split after another, so that all pairs work on the same vocabulary rows at a
-// time.  kDw: the row tiles (the model width) of one column tile after another.
+// time.  kDw: the column tiles (the model width) of one row tile after another,
+// so that ds is read once.
 //
-// The order is a mixed-radix count (for kLse and kDs: column tile, row tile;
-// else: row tile, column tile, split); a pair's step through it is split into
+// The order is a mixed-radix count (kDh: row tile, column tile, split; else
+// column tile, row tile); a pair's step through it is split into
 // digits once, so that moving on takes additions and carries.
 template <Kind kKind>
 struct Units {
-  static constexpr bool kLogits = kKind == kLse || kKind == kDs;
+  static constexpr bool kColsFirst = kKind != kDh;
   int lo, mid, hi;                             // the digits of the present tile
   int step_lo, step_mid, step_hi, n_lo, n_mid, n_hi;
   int n_kb, splits;
 
   __device__ __forceinline__ Units(const Args& a, int pair)
-      : n_lo(kLogits ? a.n_nt : a.n_mt), n_mid(kLogits ? a.n_mt : a.n_nt), n_hi(a.splits), n_kb(a.n_kb), splits(a.splits) {
+      : n_lo(kColsFirst ? a.n_nt : a.n_mt), n_mid(kColsFirst ? a.n_mt : a.n_nt), n_hi(a.splits), n_kb(a.n_kb), splits(a.splits) {
     lo = pair % n_lo;
     mid = pair / n_lo % n_mid;
     hi = pair / n_lo / n_mid;
@@ -125,8 +129,8 @@ struct Units {
     if (lo >= n_lo) { lo -= n_lo; ++mid; }
     if (mid >= n_mid) { mid -= n_mid; ++hi; }
   }
-  __device__ __forceinline__ int mt() const { return kLogits ? mid : lo; }
-  __device__ __forceinline__ int nt() const { return kLogits ? lo : mid; }
+  __device__ __forceinline__ int mt() const { return kColsFirst ? mid : lo; }
+  __device__ __forceinline__ int nt() const { return kColsFirst ? lo : mid; }
   __device__ __forceinline__ int split() const { return hi; }
   __device__ __forceinline__ int k0() const {
     return kKind == kDh ? static_cast<int>(static_cast<int64_t>(n_kb) * hi / splits) : 0;
@@ -182,12 +186,14 @@ __device__ __forceinline__ __nv_bfloat16 ds_of(float x, float lse, float coef) {
 
 template <Kind kKind, bool kBias>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b, const Args a) {
+gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+            const __grid_constant__ CUtensorMap tmap_out, const Args a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int b_tile = a.bn * kBK;                         // bytes: half of the columns, 2 bytes each
   const int stage_bytes = kATile + b_tile;
-  uint8_t* tail = smem + a.n_stages * stage_bytes;
+  uint8_t* out = smem + a.n_stages * stage_bytes;
+  uint8_t* tail = out + out_bytes(kKind);
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(tail);               // used in the even CTA
   uint64_t* empty_bar = full_bar + kMaxStages;                          // both CTAs
   uint64_t* tfull_bar = empty_bar + kMaxStages;                         // both CTAs
@@ -236,8 +242,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
     // tile of 256 columns multiplies and twice as long as one of 128.
     pdl_wait();
     const uint32_t elected = elect_one();
-    const uint64_t pol_a = kKind == kDw ? policy_evict_last() : policy_evict_first();
-    const uint64_t pol_b = kKind == kDw ? policy_evict_first() : policy_evict_last();
+    // A comes from HBM once and is read by every column tile: where there are
+    // several, what one of them loaded must outlast the output written in
+    // between (grad_W of 528 rows: 427 us with evict_first, 361 so).
+    const uint64_t pol_a = a.n_nt > 1 ? policy_evict_last() : policy_evict_first();
+    const uint64_t pol_b = policy_evict_last();
     const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
     const uint32_t leader0 = mapa_shared(full0, 0);
     const uint32_t smem0 = smem_u32(smem);
@@ -263,7 +272,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
         }
         if constexpr (b_mn_major(kKind)) {
           tma_load_2d_pair_if(elected, dst + kATile, &tmap_b, full, n0, kb * kBK, pol_b);
-          tma_load_2d_pair_if(elected, dst + kATile + kATile / 2, &tmap_b, full, n0 + 64, kb * kBK, pol_b);
+          if (a.bn == kMaxN)
+            tma_load_2d_pair_if(elected, dst + kATile + kATile / 2, &tmap_b, full, n0 + 64, kb * kBK, pol_b);
         } else {
           tma_load_2d_pair_if(elected, dst + kATile, &tmap_b, full, kb * kBK, n0, pol_b);
         }
@@ -329,7 +339,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
     // -------------------------------------------------------------- epilogue (both CTAs)
     const int quad = warp & 3;
     const int part = warp >> 2;
-    const int part_cols = (a.bn / kParts + 15) / 16 * 16;  // columns of a part, whole loads of 16
+    const int part_cols = kKind == kDw ? kBoxCols : (a.bn / kParts + 15) / 16 * 16;  // columns of a part
     const int col0 = part * part_cols;
     const int cols = max(0, min(part_cols, a.bn - col0));
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + col0;
@@ -495,28 +505,62 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
         const int acc = use & 1;
         if (!mbar_wait(&tfull_bar[acc], (use >> 1) & 1, a.err, abort_flag)) break;
         tc_fence_after();
-        const int64_t m = static_cast<int64_t>(u.mt()) * kTileM + rank * 128 + quad * 32 + lane;
+        const int m_warp = u.mt() * kTileM + static_cast<int>(rank) * 128 + quad * 32;
         const int64_t n_first = static_cast<int64_t>(u.nt()) * a.bn + col0;
-        const bool row_ok = m < a.M;
+        if constexpr (kKind == kDh) {
+          const int64_t m = m_warp + lane;
+          const bool row_ok = m < a.M;
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 16) {
-          uint32_t r[16];
-          tmem_ld_16(lane_addr + acc * kMaxN + c, r);
-          tmem_ld_wait();
+          for (int c = 0; c < cols; c += 16) {
+            uint32_t r[16];
+            tmem_ld_16(lane_addr + acc * kMaxN + c, r);
+            tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int64_t n = n_first + c + j;
-            if (n >= a.N || !row_ok) continue;
-            const float y = __uint_as_float(r[j]);
-            if constexpr (kKind == kDh) {
+            for (int j = 0; j < 16; ++j) {
+              const int64_t n = n_first + c + j;
+              if (n >= a.N || !row_ok) continue;
+              const float y = __uint_as_float(r[j]);
               float* at = a.partials + (static_cast<int64_t>(u.split()) * a.N + n) * a.M + m;
               *at = a.add ? *at + y : y;
-            } else {
-              a.grad_W[(a.v0 + n) * a.M + m] = __float2bfloat16_rn(y);
             }
           }
+          release(acc);
+        } else {
+          // 32 rows x 64 columns to the warp's box, its 16-byte pieces swizzled
+          // as the tensor map says (no bank conflicts), then out by TMA
+          uint8_t* box = out + warp * kBoxBytes;
+          if (lane == 0) bulk_wait_read();                // the box's last store has been read
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < kBoxCols; c += 16) {
+            if (c >= cols) break;
+            uint32_t r[16];
+            tmem_ld_16(lane_addr + acc * kMaxN + c, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint4 v;
+              uint32_t* w = &v.x;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(r[q * 8 + 2 * j]),
+                                                                 __uint_as_float(r[q * 8 + 2 * j + 1]));
+                w[j] = *reinterpret_cast<const uint32_t*>(&two);
+              }
+              *reinterpret_cast<uint4*>(box + lane * 128 + (((c / 8 + q) ^ (lane & 7)) * 16)) = v;
+            }
+          }
+          release(acc);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0 && cols > 0 && m_warp < a.M && n_first < a.N) {
+            tma_store_2d(&tmap_out, box, static_cast<int32_t>(n_first), m_warp);
+            bulk_commit();
+          }
         }
-        release(acc);
+      }
+      if constexpr (kKind == kDw) {
+        if (lane == 0) bulk_wait();
       }
     }
   }

@@ -143,26 +143,27 @@ struct Units {
 // ---------------------------------------------------------------- logit epilogues
 constexpr float kLowest = -3.402823466e38f;  // the lowest finite value
 
-// v[i] of 32 values per lane joined over the warp's lanes: lane l returns value
-// l.  31 shuffles instead of the 160 of 32 separate reductions: each step
-// sends the half of the values that the other lane keeps.
+// value(i) of 16 columns joined over the warp's lanes: lanes 2 i and 2 i + 1
+// return column i.  16 shuffles instead of the 80 of 16 separate reductions:
+// each step but the last sends the half of the values that the other lane
+// keeps.
 template <typename Join, typename Value>
 __device__ __forceinline__ float join_columns(int lane, Join join, Value value) {
-  float v[16];
+  float v[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const bool up = (lane & 16) != 0;
-    const float lo = value(i), hi = value(i + 16);
+    const float lo = value(i), hi = value(i + 8);
     v[i] = join(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, 16));
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    const bool up = (lane & o) != 0;
+  for (int o = 4; o > 0; o >>= 1) {
+    const bool up = (lane & (2 * o)) != 0;
 #pragma unroll
     for (int i = 0; i < o; ++i)
-      v[i] = join(up ? v[i + o] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + o], o));
+      v[i] = join(up ? v[i + o] : v[i], __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + o], 2 * o));
   }
-  return v[0];
+  return join(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 // The largest value of a warp, in every lane; NaNs do not count.  One
@@ -339,7 +340,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
     // -------------------------------------------------------------- epilogue (both CTAs)
     const int quad = warp & 3;
     const int part = warp >> 2;
-    const int part_cols = kKind == kDw ? kBoxCols : (a.bn / kParts + 15) / 16 * 16;  // columns of a part
+    const int part_cols = kKind == kDw ? kBoxCols : kKind == kDh ? (a.bn / kParts + 15) / 16 * 16 : (a.bn / kParts + 7) / 8 * 8;
     const int col0 = part * part_cols;
     const int cols = max(0, min(part_cols, a.bn - col0));
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + col0;
@@ -354,8 +355,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       float* inv_t = epi + warp * epi_arrays(kKind) * kPartCols;
       float* second = inv_t + kPartCols;
       float* third = inv_t + 2 * kPartCols;
-      LsePart part[2] = {{kLowest, 0.0f}, {kLowest, 0.0f}};      // of columns lane and 32 + lane
-      int64_t id[2] = {-1, -1};                                  // their tokens, as rows of this W
+      constexpr int kGroups = kPartCols / 16;
+      LsePart part[kGroups];                                     // of columns 16 k + lane / 2
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) part[k] = LsePart{kLowest, 0.0f};
+      int id[2] = {-1, -1};                                      // tokens of columns lane and 32 + lane, as rows of A
       int nt = -1, use = 0;
       bool ok = cols > 0;
       for (Units<kKind> u(a, pair); u.more();) {
@@ -374,8 +378,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
             const int64_t t = t_first + c;
             const bool real = c < n_cols;
             inv_t[c] = real ? row_temp(a.p.temp[t]).inv_t : 0.0f;
-            id[k] = real ? a.p.ids[t] : -1;
-            if (id[k] >= 0) id[k] -= a.v0;
+            const int64_t own = real ? a.p.ids[t] - a.v0 : -1;
+            id[k] = own >= 0 && own < a.M ? static_cast<int>(own) : -1;
             if constexpr (kKind == kDs) {
               second[c] = real ? a.lse[t] : 0.0f;
               third[c] = real ? a.coef[t] : 0.0f;
@@ -443,13 +447,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
           }
           // of each column the largest x, then the sum of exp(x - largest)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (k * 32 >= cols) break;
-            float mine = kLowest;                                // the largest x of column lane
+          for (int k = 0; k < kGroups; ++k) {
+            if (k * 16 >= n_cols) break;
+            float mine = kLowest;                                // the largest x of this lane's column
             const float sum = join_columns(lane, [](float p, float q) { return p + q; }, [&](int c) {
-              const float top = fmaxf(warp_max(x[k * 32 + c]), kLowest);
-              if (lane == c) mine = top;
-              return __expf(x[k * 32 + c] - top);
+              const float top = fmaxf(warp_max(x[k * 16 + c]), kLowest);
+              if (lane >> 1 == c) mine = top;
+              return __expf(x[k * 16 + c] - top);
             });
             part[k] = lse_join(part[k], LsePart{mine, sum});
           }
@@ -469,11 +473,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
         // a token's own logit lies in few tiles: looked for by ballots
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t hits = __ballot_sync(0xffffffffu, id[k] >= m_warp && id[k] < m_warp + 32 && id[k] < a.M);
+          uint32_t hits = __ballot_sync(0xffffffffu, static_cast<unsigned>(id[k] - static_cast<int>(m_warp)) < 32u);
           while (hits != 0) {
             const int c = k * 32 + __ffs(hits) - 1;
             hits &= hits - 1;
-            const int own = static_cast<int>(__shfl_sync(0xffffffffu, id[k], c & 31) - m_warp);
+            const int own = __shfl_sync(0xffffffffu, id[k], c & 31) - static_cast<int>(m_warp);
             float mine = 0.0f;
 #pragma unroll
             for (int j = k * 32; j < k * 32 + 32; ++j) mine = j == c ? x[j] : mine;
@@ -491,9 +495,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
           if (a.n_nt > 1 || !u.more()) {
             const int64_t which = static_cast<int64_t>(a.n_nt > 1 ? mt : pair) * 8 + rank * 4 + quad;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const int c = k * 32 + lane;
-              if (c < n_cols) a.parts[which * a.N + t_first + c] = part[k];
+            for (int k = 0; k < kGroups; ++k) {
+              const int c = k * 16 + (lane >> 1);
+              if (c < n_cols && (lane & 1) == 0) a.parts[which * a.N + t_first + c] = part[k];
               part[k] = LsePart{kLowest, 0.0f};
             }
           }

@@ -19,7 +19,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kCountThreads = 512;
 constexpr int kFlush = 16;                      // rounds of 4 tokens a thread that stay in fp32
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 3;
 
 __device__ __forceinline__ int bytes_set(uint32_t w) {
   return __popc(__vcmpne4(w, 0u) & 0x01010101u);
@@ -81,12 +81,12 @@ __global__ void __launch_bounds__(kCountThreads) policy_count_kernel(const Polic
   }
 }
 
-// e^q - 1 - q.  For small q the difference loses what it is made of (q =
-// 0.01: 5e-5 of two terms near 0.01), so it is summed from its Taylor series
-// there: the first term left out, q^10 / 10!, is below 2^-27 of q^2 / 2 for
-// |q| <= 1/2.
-__device__ __forceinline__ float kl_estimate(float q, float em1) {
-  if (fabsf(q) > 0.5f) return em1 - q;
+// e^q - 1 - q (kl) and e^q - 1 (em1).  For small q the differences lose what
+// they are made of (q = 0.01: 5e-5 of two terms near 0.01), so kl is summed from
+// its Taylor series there -- the first term left out, q^10 / 10!, is below
+// 2^-27 of q^2 / 2 for |q| <= 1/2 -- and em1 is q + kl.  Beyond, the
+// differences keep all but 3 of their bits.
+__device__ __forceinline__ void kl_terms(float q, float& kl, float& em1) {
   float s = 1.0f / 362880.0f;
   s = fmaf(s, q, 1.0f / 40320.0f);
   s = fmaf(s, q, 1.0f / 5040.0f);
@@ -95,20 +95,29 @@ __device__ __forceinline__ float kl_estimate(float q, float em1) {
   s = fmaf(s, q, 1.0f / 24.0f);
   s = fmaf(s, q, 1.0f / 6.0f);
   s = fmaf(s, q, 0.5f);
-  return s * q * q;
+  kl = s * q * q;
+  em1 = fmaf(s * q, q, q);
+  if (!(fabsf(q) <= 0.5f)) {
+    em1 = expf(q) - 1.0f;
+    kl = em1 - q;
+  }
 }
 
-// Whether logp - old lies above (or, with kBelow, below) a border that is held
-// as the sum of two fp32 numbers, hi the nearest one.  Rounding keeps order, so
-// the fp32 difference decides unless it equals hi; then its own rounding error
-// (exact in fp32) is compared with lo.  FP64 instructions would decide the
-// same and cost more than all else here: 97 us instead of 20 for 4.2 M tokens.
-template <bool kBelow>
-__device__ __forceinline__ bool beyond(float d, float logp, float old, float2 border) {
-  if (d != border.x) return kBelow ? d < border.x : d > border.x;
-  const float v = logp - d;                     // d + err = logp - old, exactly
-  const float err = (logp - (d + v)) + (v - old);
-  return kBelow ? err < border.y : err > border.y;
+// Whether a token of advantage A is clipped: logp - old above hi (A > 0) or
+// below lo (A < 0).  The borders are held as sums of two fp32 numbers, x the
+// nearest one.  Rounding keeps order, so the fp32 difference d decides unless
+// it equals x; then its own rounding error (exact in fp32) is compared with y.
+// FP64 instructions would decide the same, but they alone took 60 us for 4.2 M
+// tokens.
+__device__ __forceinline__ bool is_clipped(float A, float d, float logp, float old, float2 hi, float2 lo) {
+  bool above = d > hi.x, below = d < lo.x;
+  if (d == hi.x || d == lo.x) {
+    const float v = logp - d;                   // d + err = logp - old, exactly
+    const float err = (logp - (d + v)) + (v - old);
+    above |= d == hi.x && err > hi.y;
+    below |= d == lo.x && err < lo.y;
+  }
+  return A > 0.0f ? above : A < 0.0f && below;
 }
 
 // Sums of one thread over kFlush rounds, in fp32; they are added up in fp64.
@@ -124,7 +133,8 @@ struct Weights {
 // The sequence that token i belongs to: the last one that starts at or before
 // it.  Always in [0, n_seqs), whatever the offsets hold.
 __device__ __forceinline__ int64_t sequence_of(const PolicyProblem& p, int64_t i) {
-  if (p.starts == nullptr) return i / p.row_len;
+  if (p.starts == nullptr)
+    return p.N < (int64_t(1) << 31) ? static_cast<uint32_t>(i) / static_cast<uint32_t>(p.row_len) : i / p.row_len;
   int64_t lo = 0, hi = p.n_seqs;                // starts[lo] <= i < starts[hi]
   while (hi - lo > 1) {
     const int64_t mid = (lo + hi) >> 1;
@@ -133,158 +143,166 @@ __device__ __forceinline__ int64_t sequence_of(const PolicyProblem& p, int64_t i
   return lo;
 }
 
-// Tokens [i, i + kVec) of one thread.
+// What tokens [i, i + kVec) of one thread hold.
 template <int kVec>
-__device__ __forceinline__ void tokens(const PolicyProblem& p, const Weights& w, int64_t i, Sums& sums) {
-  float lp[kVec], old[kVec], ref[kVec], adv[kVec], g[kVec];
+struct Loaded {
+  float lp[kVec], old[kVec], ref[kVec], adv[kVec];
   bool on[kVec];
-  if constexpr (kVec == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p.logp + i);
-    const float4 b = *reinterpret_cast<const float4*>(p.old_logp + i);
-    lp[0] = a.x; lp[1] = a.y; lp[2] = a.z; lp[3] = a.w;
-    old[0] = b.x; old[1] = b.y; old[2] = b.z; old[3] = b.w;
-    if (p.ref_logp != nullptr) {
-      const float4 c = *reinterpret_cast<const float4*>(p.ref_logp + i);
+
+  __device__ __forceinline__ void load(const PolicyProblem& p, int64_t i) {
+    if constexpr (kVec == 4) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(p.logp + i));
+      const float4 b = __ldcs(reinterpret_cast<const float4*>(p.old_logp + i));
+      float4 c = make_float4(0.0f, 0.0f, 0.0f, 0.0f), e = c;
+      uchar4 m = make_uchar4(1, 1, 1, 1);
+      if (p.ref_logp != nullptr) c = __ldcs(reinterpret_cast<const float4*>(p.ref_logp + i));
+      if (!p.adv_per_seq) e = __ldcs(reinterpret_cast<const float4*>(p.adv + i));
+      if (p.mask != nullptr) m = __ldcs(reinterpret_cast<const uchar4*>(p.mask + i));
+      lp[0] = a.x; lp[1] = a.y; lp[2] = a.z; lp[3] = a.w;
+      old[0] = b.x; old[1] = b.y; old[2] = b.z; old[3] = b.w;
       ref[0] = c.x; ref[1] = c.y; ref[2] = c.z; ref[3] = c.w;
+      adv[0] = e.x; adv[1] = e.y; adv[2] = e.z; adv[3] = e.w;
+      on[0] = m.x != 0; on[1] = m.y != 0; on[2] = m.z != 0; on[3] = m.w != 0;
+    } else {
+      lp[0] = p.logp[i];
+      old[0] = p.old_logp[i];
+      ref[0] = p.ref_logp != nullptr ? p.ref_logp[i] : 0.0f;
+      adv[0] = p.adv_per_seq ? 0.0f : p.adv[i];
+      on[0] = p.mask == nullptr || p.mask[i] != 0;
     }
-    if (!p.adv_per_seq) {
-      const float4 c = *reinterpret_cast<const float4*>(p.adv + i);
-      adv[0] = c.x; adv[1] = c.y; adv[2] = c.z; adv[3] = c.w;
-    }
-    uchar4 m = make_uchar4(1, 1, 1, 1);
-    if (p.mask != nullptr) m = *reinterpret_cast<const uchar4*>(p.mask + i);
-    on[0] = m.x != 0; on[1] = m.y != 0; on[2] = m.z != 0; on[3] = m.w != 0;
-  } else {
-    lp[0] = p.logp[i];
-    old[0] = p.old_logp[i];
-    if (p.ref_logp != nullptr) ref[0] = p.ref_logp[i];
-    if (!p.adv_per_seq) adv[0] = p.adv[i];
-    on[0] = p.mask == nullptr || p.mask[i] != 0;
   }
-  const bool by_seq = p.adv_per_seq || p.mean == FS_MEAN_SEQUENCE;
-  int64_t s = by_seq ? sequence_of(p, i) : 0;
+};
+
+// Their terms and gradients.  Masked tokens go through the arithmetic like the
+// others and are selected away (their values may be NaN): branches around them
+// would split nearly every warp.
+// kBySeq: something depends on the token's sequence (its advantage or weight).
+template <int kVec, bool kBySeq>
+__device__ __forceinline__ void tokens(const PolicyProblem& p, const Weights& w, int64_t i, const Loaded<kVec>& x,
+                                       Sums& sums) {
+  int64_t s = kBySeq ? sequence_of(p, i) : 0;
   int64_t end = 0;
-  if (by_seq) end = p.starts != nullptr ? p.starts[s + 1] : (s + 1) * p.row_len;
+  if (kBySeq) end = p.starts != nullptr ? p.starts[s + 1] : (s + 1) * p.row_len;
   float seq_adv = 0.0f, weight = w.token;
   auto enter = [&]() {
     if (p.adv_per_seq) seq_adv = p.adv[s];
     if (p.mean == FS_MEAN_SEQUENCE) weight = 1.0f / (static_cast<float>(p.counts[s]) * w.seqs);
   };
-  if (by_seq) enter();
-  float policy = 0.0f, kl = 0.0f, clipped = 0.0f;
+  if (kBySeq) enter();
+  float policy = 0.0f, kl = 0.0f, clipped = 0.0f, g[kVec];
 #pragma unroll
   for (int j = 0; j < kVec; ++j) {
-    while (by_seq && i + j >= end && s + 1 < p.n_seqs) {       // into the next sequence that has tokens
+    while (kBySeq && i + j >= end && s + 1 < p.n_seqs) {       // into the next sequence that has tokens
       ++s;
       end = p.starts != nullptr ? p.starts[s + 1] : end + p.row_len;
       if (i + j < end) enter();
     }
-    g[j] = 0.0f;
-    if (!on[j]) continue;
-    const float A = p.adv_per_seq ? seq_adv : adv[j];
-    const float d = lp[j] - old[j];
-    const bool cut = A > 0.0f ? beyond<false>(d, lp[j], old[j], p.log_hi)
-                              : A < 0.0f && beyond<true>(d, lp[j], old[j], p.log_lo);
+    const float A = kBySeq && p.adv_per_seq ? seq_adv : x.adv[j];
+    const float d = x.lp[j] - x.old[j];
+    const bool cut = is_clipped(A, d, x.lp[j], x.old[j], p.log_hi, p.log_lo);
     const float rA = expf(d) * A;
     const float term = cut ? (A > 0.0f ? p.hi : p.lo) * A : rA;
-    policy = fmaf(-term, weight, policy);
+    policy = x.on[j] ? fmaf(-term, weight, policy) : policy;
     float grad = cut ? 0.0f : -rA;
-    if (cut) clipped += weight;
+    clipped += x.on[j] && cut ? weight : 0.0f;
     if (p.ref_logp != nullptr) {
-      const float q = ref[j] - lp[j];
-      const float em1 = expm1f(q);
-      kl = fmaf(kl_estimate(q, em1), weight, kl);
+      float estimate, em1;
+      kl_terms(x.ref[j] - x.lp[j], estimate, em1);
+      kl = x.on[j] ? fmaf(estimate, weight, kl) : kl;
       grad = fmaf(-p.kl_coef, em1, grad);
     }
-    g[j] = grad * weight;
+    g[j] = x.on[j] ? grad * weight : 0.0f;
   }
   sums.policy += policy;
   sums.kl += kl;
   sums.clipped += clipped;
   if constexpr (kVec == 4)
-    *reinterpret_cast<float4*>(p.grad + i) = make_float4(g[0], g[1], g[2], g[3]);
+    __stcs(reinterpret_cast<float4*>(p.grad + i), make_float4(g[0], g[1], g[2], g[3]));
   else
     p.grad[i] = g[0];
 }
 
-// The block's sums of three values, added in fp64 in a fixed order, 32 values
-// by each of 24 threads; valid in thread 0.  (A tree of FP64 shuffles over all
-// threads takes three times as many FP64 additions.)
+// The block's sums of three values, added in fp64 in a fixed order: a warp for
+// each value, 8 of them a lane and then the lanes as a tree.  FP64 additions
+// are few and slow here, so the chain of 13 counts: one of 40 made the
+// smallest call 4 us longer.
 template <typename T>
 __device__ void block_sums(const T (&mine)[3], double (&total)[3]) {
   __shared__ T all[3][kThreads];
-  __shared__ double part[3][kThreads / 32];
+  __shared__ double sum[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) all[k][threadIdx.x] = mine[k];
   __syncthreads();
-  if (threadIdx.x < 3 * (kThreads / 32)) {
-    const int k = threadIdx.x / (kThreads / 32), g = threadIdx.x % (kThreads / 32);
+  const int k = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (k < 3) {
     double v = 0.0;
-#pragma unroll 8
-    for (int i = 0; i < 32; ++i) v += static_cast<double>(all[k][g + i * (kThreads / 32)]);
-    part[k][g] = v;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) v += static_cast<double>(all[k][lane + 32 * i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) sum[k] = v;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      total[k] = 0.0;
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) total[k] += part[k][i];
-    }
-  }
+  for (int k = 0; k < 3; ++k) total[k] = sum[k];
   __syncthreads();
 }
 
-template <bool kAligned>
+template <bool kAligned, bool kBySeq>
 __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const PolicyProblem p, const bool counted) {
   __shared__ bool last;
-  pdl_wait();                                   // the counts, and whatever wrote the inputs
+  Sums sums{0.0f, 0.0f, 0.0f};
+  double v[3] = {0.0, 0.0, 0.0}, t[3];
+  constexpr int kVec = kAligned ? 4 : 1;
+  const int64_t items = p.N / kVec;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
+  int64_t k = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  Loaded<kVec> now, then;
+  if (k < items) now.load(p, k * kVec);
+  // The counting kernel starts after whatever wrote the inputs has ended, so
+  // only its counts are waited for, with the first loads in flight.
+  pdl_wait();
   Weights w{1.0f, 1.0f};
   const unsigned long long count = counted ? *reinterpret_cast<volatile unsigned long long*>(&p.scratch->count) : 0ull;
   if (p.mean == FS_MEAN_TOKEN) w.token = 1.0f / static_cast<float>(counted ? max(count, 1ull) : p.N);
   if (p.mean == FS_MEAN_SEQUENCE) w.seqs = static_cast<float>(count);
-  Sums sums{0.0f, 0.0f, 0.0f};
-  double v[3] = {0.0, 0.0, 0.0}, t[3];
-  int rounds = 0;
-  auto next_round = [&]() {                     // long sums do not stay in fp32 (the same in every thread)
-    if (++rounds % kFlush != 0) return;
-    block_sums({sums.policy, sums.kl, sums.clipped}, t);
-    for (int k = 0; k < 3; ++k) v[k] += t[k];
-    sums = Sums{0.0f, 0.0f, 0.0f};
-  };
-  const int64_t tid = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-  if constexpr (kAligned) {
-    const int64_t quads = p.N / 4;
-    for (int64_t k = tid; k - threadIdx.x < quads; k += stride) {
-      if (k < quads) tokens<4>(p, w, k * 4, sums);
-      next_round();
-    }
-    if (tid < p.N - quads * 4) tokens<1>(p, w, quads * 4 + tid, sums);
-  } else {
-    for (int64_t k = tid; k - threadIdx.x < p.N; k += stride) {
-      if (k < p.N) tokens<1>(p, w, k, sums);
-      next_round();
+  if (kAligned && k < p.N - items * kVec) {      // the last few tokens
+    Loaded<1> x;
+    x.load(p, items * kVec + k);
+    tokens<1, kBySeq>(p, w, items * kVec + k, x, sums);
+  }
+  for (int round = 1; k - threadIdx.x < items; k += stride, ++round) {
+    if (k + stride < items) then.load(p, (k + stride) * kVec);     // in flight while this round computes
+    if (k < items) tokens<kVec, kBySeq>(p, w, k * kVec, now, sums);
+    now = then;
+    if (round % kFlush == 0) {                   // long sums do not stay in fp32
+      block_sums({sums.policy, sums.kl, sums.clipped}, t);
+#pragma unroll
+      for (int j = 0; j < 3; ++j) v[j] += t[j];
+      sums = Sums{0.0f, 0.0f, 0.0f};
     }
   }
   block_sums({sums.policy, sums.kl, sums.clipped}, t);
-  if (threadIdx.x == 0) {
-    double* mine = p.scratch->sums[blockIdx.x];
-    for (int k = 0; k < 3; ++k) mine[k] = v[k] + t[k];
-    __threadfence();
-    last = atomicAdd(&p.scratch->ticket, 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!last) return;
-  // the block that finishes last adds the blocks' sums, in their order
-  __threadfence();
-  for (int k = 0; k < 3; ++k) v[k] = 0.0;
-  for (unsigned b = threadIdx.x; b < gridDim.x; b += kThreads) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) v[k] += __ldcg(&p.scratch->sums[b][k]);
+  for (int k = 0; k < 3; ++k) t[k] += v[k];
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      double* mine = p.scratch->sums[blockIdx.x];
+      for (int k = 0; k < 3; ++k) mine[k] = t[k];
+      __threadfence();
+      last = atomicAdd(&p.scratch->ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    // the block that finishes last adds the blocks' sums, in their order
+    __threadfence();
+    for (int k = 0; k < 3; ++k) v[k] = 0.0;
+    for (unsigned b = threadIdx.x; b < gridDim.x; b += kThreads) {
+#pragma unroll
+      for (int k = 0; k < 3; ++k) v[k] += __ldcg(&p.scratch->sums[b][k]);
+    }
+    block_sums(v, t);
   }
-  block_sums(v, t);
   if (threadIdx.x == 0) {
     p.stats[0] = static_cast<float>(t[0] + static_cast<double>(p.kl_coef) * t[1]);
     p.stats[1] = static_cast<float>(t[0]);
@@ -315,7 +333,10 @@ cudaError_t launch_policy_loss(const PolicyProblem& p, cudaStream_t stream) {
                    (p.adv_per_seq || aligned_to(p.adv, 16)) && aligned_to(p.mask, 4) && aligned_to(p.grad, 16);
   const int64_t items = vec ? (p.N + 3) / 4 : p.N;
   const int64_t blocks = std::min<int64_t>({(items + kThreads - 1) / kThreads, kBlocksPerSm * sms, kTrainMaxBlocks});
-  return launch_kernel(vec ? policy_loss_kernel<true> : policy_loss_kernel<false>,
+  const bool by_seq = p.adv_per_seq || p.mean == FS_MEAN_SEQUENCE;
+  const auto kernel = vec ? (by_seq ? policy_loss_kernel<true, true> : policy_loss_kernel<true, false>)
+                          : (by_seq ? policy_loss_kernel<false, true> : policy_loss_kernel<false, false>);
+  return launch_kernel(kernel,
                        dim3(static_cast<unsigned>(std::max<int64_t>(blocks, 1))), dim3(kThreads), 0, stream, counted,
                        p, counted);
 }

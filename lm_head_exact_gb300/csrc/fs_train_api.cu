@@ -105,6 +105,16 @@ float2 two_floats(double v) {
   return make_float2(hi, static_cast<float>(v - hi));
 }
 
+// No C++ exception leaves a C entry (the library's maps can run out of memory).
+template <typename Body>
+fs_status guarded(Body body) {
+  try {
+    return body();
+  } catch (...) {
+    return api_fail(FS_ERR_WORKSPACE, "out of host memory");
+  }
+}
+
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const char* x = static_cast<const char*>(a);
   const char* y = static_cast<const char*>(b);
@@ -128,6 +138,7 @@ fs_status fs_token_logprobs(const void* h, const void* W, int64_t n, int64_t d, 
                             const float* temp, const float* bias, int64_t bias_row_stride, float* logp, float* lse,
                             float* kept, void* workspace, size_t workspace_bytes, void* stream_) {
   api_begin();
+  return guarded([&]() -> fs_status {
   FS_API_TRY(api_check_shapes(n, d, V));
   if (n == 0) return FS_OK;
   const HeadProblem p{h, W, n, d, V, ids, temp, bias, bias_row_stride};
@@ -144,6 +155,7 @@ fs_status fs_token_logprobs(const void* h, const void* W, int64_t n, int64_t d, 
   if (V > 0) FS_API_TRY(api_launched(launch_head_parts(p, w.parts, w.own_x, kept, err, stream), "scoring kernel launch"));
   return api_launched(launch_head_merge(p, w.parts, V > 0 ? w.n_parts : 0, w.own_x, logp, lse, stream),
                       "log-sum merge launch");
+  });
 }
 
 size_t fs_token_logprobs_backward_workspace_bytes(int64_t n, int64_t d, int64_t V) {
@@ -156,6 +168,7 @@ fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, in
                                      const float* grad_logp, const float* kept, void* grad_h, void* grad_W,
                                      void* workspace, size_t workspace_bytes, void* stream_) {
   api_begin();
+  return guarded([&]() -> fs_status {
   FS_API_TRY(api_check_shapes(n, d, V));
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (grad_h != nullptr && n > 0) FS_API_TRY(api_check_array(grad_h, 16, "grad_h"));
@@ -198,6 +211,7 @@ fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, in
   if (grad_h != nullptr)
     FS_API_TRY(api_launched(launch_head_dh_sum(p, w.partials, w.splits, w.coef, grad_h, stream), "grad_h sum launch"));
   return FS_OK;
+  });
 }
 
 size_t fs_policy_loss_workspace_bytes(int64_t n_seqs) {
@@ -209,6 +223,7 @@ fs_status fs_policy_loss(const float* logp, const float* old_logp, const float* 
                          double clip_low, double clip_high, double kl_coef, int mean, float* stats, float* grad,
                          void* workspace, size_t workspace_bytes, void* stream_) {
   api_begin();
+  return guarded([&]() -> fs_status {
   if (N < 0 || n_seqs < 0) return api_fail(FS_ERR_INVALID_ARG, "need N >= 0 and n_seqs >= 0 (got %lld, %lld)",
                                            (long long)N, (long long)n_seqs);
   if (n_seqs >= (int64_t(1) << 31) || N >= (int64_t(1) << 40))
@@ -250,11 +265,13 @@ fs_status fs_policy_loss(const float* logp, const float* old_logp, const float* 
   p.counts = static_cast<int*>(workspace);
   p.scratch = scratch;
   return api_launched(launch_policy_loss(p, stream), "policy loss launch");
+  });
 }
 
 fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes, const int* types,
                             int n_tensors, double max_norm, int norm_type, float* norm, void* stream_) {
   api_begin();
+  return guarded([&]() -> fs_status {
   if (n_tensors < 0) return api_fail(FS_ERR_INVALID_ARG, "need n_tensors >= 0 (got %d)", n_tensors);
   if (!(max_norm >= 0.0)) return api_fail(FS_ERR_INVALID_ARG, "max_norm must be >= 0 and not NaN");
   if (norm_type != FS_NORM_L2 && norm_type != FS_NORM_MAX)
@@ -285,6 +302,7 @@ fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, const i
   return api_launched(launch_clip_grad_norm(grads, outs, sizes, types, n_tensors, max_norm, norm_type, norm, scratch,
                                             stream),
                       "gradient norm launch");
+  });
 }
 
 }  // extern "C"

@@ -125,6 +125,54 @@ def test_scores_and_gradients(fs, torch_cuda, n, d, V, bias, kept):
     assert fs.device_error() == 0
 
 
+@pytest.mark.parametrize("n,d,V", [(40, 4104, 300), (300, 2056, 515), (1031, 72, 2000), (513, 520, 1030)])
+def test_long_sums_and_several_column_tiles(fs, torch_cuda, n, d, V):
+    """Widths whose logits are formed in several pieces; more tokens than one
+    and than four tiles hold."""
+    test_scores_and_gradients(fs, torch_cuda, n, d, V, "shared", True)
+    test_scores_and_gradients(fs, torch_cuda, n, d, V, "rows", False)
+
+
+def test_vocabulary_in_pieces(fs, torch_cuda):
+    """So many tokens that ds is formed for a part of the vocabulary at a time
+    (4 GiB): both pieces' grad_W, and grad_h over both."""
+    torch = torch_cuda
+    n, d, V = 70000, 8, 33000
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    h = torch.randn(n, d, generator=gen, device="cuda").bfloat16()
+    W = torch.randn(V, d, generator=gen, device="cuda").bfloat16()
+    ids = torch.randint(0, V, (n,), generator=gen, device="cuda")
+    temp, g = torch.ones(n, device="cuda"), torch.randn(n, generator=gen, device="cuda")
+    logp, lse = fs.token_logprobs(h, W, ids, temp)
+    gh, gW = fs.token_logprobs_backward(h, W, ids, temp, logp, lse, g)
+    keep = fs.logprob_buffer(n, V)
+    logp2, lse2 = fs.token_logprobs(h, W, ids, temp, kept=keep)
+    gh2, gW2 = fs.token_logprobs_backward(h, W, ids, temp, logp2, lse2, g, kept=keep)
+    assert torch.equal(logp, logp2) and torch.equal(lse, lse2)
+    W64 = W.double()
+    want_W = torch.zeros(V, d, dtype=torch.float64, device="cuda")
+    size_W = torch.zeros_like(want_W)
+    for i in range(0, n, 5000):
+        at = slice(i, i + 5000)
+        h64 = h[at].double()
+        x = h64 @ W64.T
+        z = x.logsumexp(1)
+        assert float((lse[at].double() - z).abs().max()) < 1e-4
+        ds = -(x - z[:, None]).exp()
+        ds[torch.arange(ds.shape[0], device="cuda"), ids[at]] += 1
+        ds *= g[at].double()[:, None]
+        want = ds @ W64
+        # ds and the result rounded to bf16, fp32 sums of V terms
+        tol = (2.0 ** -8 + 2.0 ** -12) * (ds.abs() @ W64.abs()) + 2.0 ** -8 * want.abs()
+        for got in (gh, gh2):
+            assert bool(((got[at].double() - want).abs() <= tol).all())
+        want_W += ds.T @ h64
+        size_W += ds.abs().T @ h64.abs()
+    tol = (2.0 ** -8 + 2.0 ** -10) * size_W + 2.0 ** -8 * want_W.abs()
+    for got in (gW, gW2):
+        assert bool(((got.double() - want_W).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("kept", [True, False])
 @pytest.mark.parametrize("n", [9, 150])
 def test_rows_that_take_no_part(fs, torch_cuda, n, kept):

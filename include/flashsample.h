@@ -385,7 +385,9 @@ FS_API int64_t fs_logprob_buffer_elems(int64_t n, int64_t V);
  * its buffer, or NULL to form the logits again from h, W and bias.
  * Rows that are not scored, have g == 0, lse == -inf or logp == -inf carry no
  * gradient: their grad_h is zero and their h may hold anything.
- * Products take ds rounded to bf16 and accumulate in fp32.
+ * Products take ds rounded to bf16 and accumulate in fp32; what the rounding
+ * leaves over of each token's own entry, the largest of its row, is added in
+ * fp32.
  *   workspace: fs_token_logprobs_backward_workspace_bytes(n, d, V) bytes.
  */
 FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, int64_t d, int64_t V,

@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(kMergeThreads) head_merge_kernel(const HeadPro
 }
 
 __global__ void __launch_bounds__(256) head_rows_kernel(const HeadProblem p, const float* logp, const float* lse,
-                                                        const float* g, float* coef, __nv_bfloat16* h_live) {
+                                                        const float* g, float* coef, int* own, float* rest,
+                                                        __nv_bfloat16* h_live) {
   const int64_t t = blockIdx.x;
   pdl_launch_dependents();
   pdl_wait();
@@ -82,7 +83,11 @@ __global__ void __launch_bounds__(256) head_rows_kernel(const HeadProblem p, con
   const int64_t id = p.ids[t];
   const bool live = rt.mode != kRowInvalid && id >= 0 && id < p.V && g[t] != 0.0f && lse[t] != -INFINITY &&
                     logp[t] != -INFINITY;
-  if (threadIdx.x == 0) coef[t] = live ? g[t] * rt.inv_t : 0.0f;
+  if (threadIdx.x == 0) {
+    coef[t] = live ? g[t] * rt.inv_t : 0.0f;
+    own[t] = live ? static_cast<int>(id) : -1;
+    rest[t] = 0.0f;
+  }
   if (h_live == nullptr) return;
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.h) + t * p.d);
   uint4* dst = reinterpret_cast<uint4*>(h_live + t * p.d);
@@ -95,7 +100,7 @@ __global__ void __launch_bounds__(256) head_rows_kernel(const HeadProblem p, con
 // pitch) hold what the padding of `kept` gives and are never read.
 __global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, const float* lse, const float* coef,
                                                            const float* kept, int64_t kept_pitch, int64_t v0,
-                                                           __nv_bfloat16* ds, int64_t pitch) {
+                                                           __nv_bfloat16* ds, int64_t pitch, float* rest) {
   const int64_t t = blockIdx.x;
   pdl_launch_dependents();
   pdl_wait();
@@ -114,23 +119,27 @@ __global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, 
       const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float q = __expf(x[j] - z);
-        o[j] = __float2bfloat16_rn(v + j == id ? c * (1.0f - q) : -c * q);
+        o[j] = v + j == id ? head::own_ds_of(x[j], z, c, rest[t]) : head::ds_of(x[j], z, c);
       }
     }
     *reinterpret_cast<uint4*>(dst + v) = *reinterpret_cast<uint4*>(o);
   }
 }
 
-// grad_h: the splits' partials added in their order and rounded once.
+// grad_h: the splits' partials added in their order, then what the rounding of
+// the tokens' own entries left over, and rounded once.
 __global__ void __launch_bounds__(256) head_dh_sum_kernel(const HeadProblem p, const float* partials, int64_t splits,
-                                                          const float* coef, __nv_bfloat16* grad_h) {
+                                                          const int* own, const float* rest, __nv_bfloat16* grad_h) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;     // d is a multiple of 8
   pdl_launch_dependents();
   pdl_wait();
   if (i >= p.n * p.d) return;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (coef[i / p.d] != 0.0f) {
+  const int64_t t = i / p.d;
+  const int id = own[t];
+  if (id >= 0) {                                        // else the row carries no gradient
+    const uint2 raw = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.W) + id * p.d + (i - t * p.d)));
+    const float r = rest[t];
 #pragma unroll 4
     for (int64_t k = 0; k < splits; ++k) {
       const float4 x = __ldcs(reinterpret_cast<const float4*>(partials + k * p.n * p.d + i));
@@ -139,6 +148,12 @@ __global__ void __launch_bounds__(256) head_dh_sum_kernel(const HeadProblem p, c
       s.z += x.z;
       s.w += x.w;
     }
+    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.x));
+    const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw.y));
+    s.x = fmaf(r, lo.x, s.x);
+    s.y = fmaf(r, lo.y, s.y);
+    s.z = fmaf(r, hi.x, s.z);
+    s.w = fmaf(r, hi.y, s.w);
   }
   __align__(8) __nv_bfloat16 o[4] = {__float2bfloat16_rn(s.x), __float2bfloat16_rn(s.y), __float2bfloat16_rn(s.z),
                                      __float2bfloat16_rn(s.w)};
@@ -276,19 +291,19 @@ cudaError_t launch_head_merge(const HeadProblem& p, const LsePart* parts, int64_
 }
 
 cudaError_t launch_head_rows(const HeadProblem& p, const float* logp, const float* lse, const float* g, float* coef,
-                             void* h_live, cudaStream_t stream) {
+                             int* own, float* rest, void* h_live, cudaStream_t stream) {
   return launch_kernel(head_rows_kernel, dim3(static_cast<unsigned>(p.n)), dim3(256), 0, stream, true, p, logp, lse,
-                       g, coef, static_cast<__nv_bfloat16*>(h_live));
+                       g, coef, own, rest, static_cast<__nv_bfloat16*>(h_live));
 }
 
 cudaError_t launch_head_ds(const HeadProblem& p, const float* lse, const float* coef, const float* kept, int64_t v0,
-                           int64_t vc, void* ds, int* err, cudaStream_t stream) {
+                           int64_t vc, void* ds, float* rest, int* err, cudaStream_t stream) {
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(ds);
   const int64_t pitch = padded_cols(vc);
   if (kept != nullptr) {
     const int64_t blocks = std::min<int64_t>((pitch + 2047) / 2048, 64);
     return launch_kernel(head_ds_kept_kernel, dim3(static_cast<unsigned>(p.n), static_cast<unsigned>(blocks)),
-                         dim3(256), 0, stream, true, p, lse, coef, kept, padded_cols(p.V), v0, out, pitch);
+                         dim3(256), 0, stream, true, p, lse, coef, kept, padded_cols(p.V), v0, out, pitch, rest);
   }
   Args a{};
   a.p = p;
@@ -296,6 +311,7 @@ cudaError_t launch_head_ds(const HeadProblem& p, const float* lse, const float* 
   a.coef = coef;
   a.ds = out;
   a.ds_pitch = pitch;
+  a.rest = rest;
   a.err = err;
   return launch_logits<head::kDs>(a, v0, vc, stream);
 }
@@ -347,14 +363,14 @@ cudaError_t launch_head_dh(const HeadProblem& p, const void* ds, int64_t v0, int
   return launch<head::kDh, false>(a, tw, ts, tw, stream);
 }
 
-cudaError_t launch_head_dh_sum(const HeadProblem& p, const float* partials, int64_t splits, const float* coef,
-                               void* grad_h, cudaStream_t stream) {
+cudaError_t launch_head_dh_sum(const HeadProblem& p, const float* partials, int64_t splits, const int* own,
+                               const float* rest, void* grad_h, cudaStream_t stream) {
   return launch_kernel(head_dh_sum_kernel, dim3(static_cast<unsigned>((p.n * p.d / 4 + 255) / 256)), dim3(256), 0,
-                       stream, false, p, partials, splits, coef, static_cast<__nv_bfloat16*>(grad_h));
+                       stream, false, p, partials, splits, own, rest, static_cast<__nv_bfloat16*>(grad_h));
 }
 
-cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_live, int64_t v0, int64_t vc,
-                           void* grad_W, int* err, cudaStream_t stream) {
+cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_live, const int* own, float* rest,
+                           int64_t v0, int64_t vc, void* grad_W, int* err, cudaStream_t stream) {
   Args a{};
   a.p = p;
   a.M = vc;
@@ -372,6 +388,9 @@ cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_l
   a.splits = 1;
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
   a.v0 = v0;
+  a.rest = rest;
+  a.own = own;
+  a.h = static_cast<const __nv_bfloat16*>(h_live);
   a.err = err;
   return launch<head::kDw, false>(a, ts, th, tg, stream);
 }

@@ -92,6 +92,11 @@ struct Args {
   // kDh
   float* partials;
   bool add;
+  // kDs writes, kDw reads: a token's own entry of ds, what rounding it to bf16
+  // left over [n]; kDw: the tokens' ids (-1: no gradient) and h [n, N]
+  float* rest;
+  const int* own;
+  const __nv_bfloat16* h;
   int* err;
 };
 
@@ -179,8 +184,19 @@ __device__ __forceinline__ LsePart lse_join(LsePart a, LsePart b) {
   return LsePart{m, a.s * __expf(a.m - m) + b.s * __expf(b.m - m)};
 }
 
-// ds of a token that is not the row's own; rows without a gradient hold zeros
-// whatever their logits are.
+// A token's own entry of ds, c (1 - p), is by far the largest of its row, so
+// its rounding to bf16 alone would make the gradients' error half again as
+// large as rounding the results does.  What the rounding leaves over is kept
+// and added in fp32: rest W[id] to grad_h, rest h to row id of grad_W.
+__device__ __forceinline__ __nv_bfloat16 own_ds_of(float x, float lse, float coef, float& rest) {
+  const float v = coef * (1.0f - __expf(x - lse));
+  const __nv_bfloat16 r = __float2bfloat16_rn(v);
+  rest = v - __bfloat162float(r);
+  return r;
+}
+
+// ds of another token; rows without a gradient hold zeros whatever their
+// logits are.
 __device__ __forceinline__ __nv_bfloat16 ds_of(float x, float lse, float coef) {
   return __float2bfloat16_rn(coef == 0.0f ? 0.0f : -coef * __expf(x - lse));
 }
@@ -485,7 +501,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
               if constexpr (kKind == kLse) {
                 a.own_x[t_first + c] = mine;
               } else if (third[c] != 0.0f) {
-                a.ds[(t_first + c) * a.ds_pitch + m] = __float2bfloat16_rn(third[c] * (1.0f - __expf(mine - second[c])));
+                a.ds[(t_first + c) * a.ds_pitch + m] = own_ds_of(mine, second[c], third[c], a.rest[t_first + c]);
               }
             }
           }
@@ -530,11 +546,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
           }
           release(acc);
         } else {
-          // 32 rows x 64 columns to the warp's box, its 16-byte pieces swizzled
-          // as the tensor map says (no bank conflicts), then out by TMA
-          uint8_t* box = out + warp * kBoxBytes;
-          if (lane == 0) bulk_wait_read();                // the box's last store has been read
-          __syncwarp();
+          // 32 rows x 64 columns, and what the rounding of the tokens' own
+          // entries left over for these rows
+          float x[kBoxCols];
 #pragma unroll
           for (int c = 0; c < kBoxCols; c += 16) {
             if (c >= cols) break;
@@ -542,19 +556,56 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
             tmem_ld_16(lane_addr + acc * kMaxN + c, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint4 v;
-              uint32_t* w = &v.x;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(r[q * 8 + 2 * j]),
-                                                                 __uint_as_float(r[q * 8 + 2 * j + 1]));
-                w[j] = *reinterpret_cast<const uint32_t*>(&two);
-              }
-              *reinterpret_cast<uint4*>(box + lane * 128 + (((c / 8 + q) ^ (lane & 7)) * 16)) = v;
-            }
+            for (int j = 0; j < 16; ++j) x[c + j] = __uint_as_float(r[j]);
           }
           release(acc);
+          const int first = static_cast<int>(a.v0) + m_warp;
+          for (int64_t t0 = 0; t0 < a.p.n && cols > 0; t0 += 128) {
+            int id[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) id[k] = t0 + k * 32 + lane < a.p.n ? __ldg(a.own + t0 + k * 32 + lane) : -1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t hits = __ballot_sync(0xffffffffu, static_cast<unsigned>(id[k] - first) < 32u);
+              while (hits != 0) {
+                const int src = __ffs(hits) - 1;
+                hits &= hits - 1;
+                if (__shfl_sync(0xffffffffu, id[k], src) - first != lane) continue;
+                const int64_t t = t0 + k * 32 + src;
+                const float rest = a.rest[t];
+                const uint4* h = reinterpret_cast<const uint4*>(a.h + t * a.N + n_first);
+#pragma unroll
+                for (int q = 0; q < kBoxCols / 8; ++q) {
+                  if (n_first + q * 8 >= a.N) break;
+                  const uint4 v = __ldg(h + q);
+                  const __nv_bfloat162* two = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    const float2 f = __bfloat1622float2(two[j]);
+                    x[q * 8 + 2 * j] = fmaf(rest, f.x, x[q * 8 + 2 * j]);
+                    x[q * 8 + 2 * j + 1] = fmaf(rest, f.y, x[q * 8 + 2 * j + 1]);
+                  }
+                }
+              }
+              __syncwarp();
+            }
+          }
+          // to the warp's box, its 16-byte pieces swizzled as the tensor map
+          // says (no bank conflicts), then out by TMA
+          uint8_t* box = out + warp * kBoxBytes;
+          if (lane == 0) bulk_wait_read();                // the box's last store has been read
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < kBoxCols / 8; ++q) {
+            uint4 v;
+            uint32_t* w = &v.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 two = __floats2bfloat162_rn(x[q * 8 + 2 * j], x[q * 8 + 2 * j + 1]);
+              w[j] = *reinterpret_cast<const uint32_t*>(&two);
+            }
+            *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) * 16)) = v;
+          }
           fence_async_shared();
           __syncwarp();
           if (lane == 0 && cols > 0 && m_warp < a.M && n_first < a.N) {

@@ -605,6 +605,7 @@ def test_policy_and_clip_in_a_graph(fs, torch_cuda):
     src = g.clone()
     stream = torch.cuda.Stream()
     torch.cuda.synchronize()
+    fs.check(fs.library().fs_workspace_release())          # another test may have used this stream
     with pytest.raises(fs.FlashSampleError) as e:
         with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=stream):
             fs.clip_grad_norm([g], 1.0)

@@ -118,8 +118,11 @@ __global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, 
       const float4 b = __ldcs(reinterpret_cast<const float4*>(src + v + 4));
       const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        o[j] = v + j == id ? head::own_ds_of(x[j], z, c, rest[t]) : head::ds_of(x[j], z, c);
+      for (int j = 0; j < 8; ++j) o[j] = head::ds_of(x[j], z, c);
+      if (id >= v && id < v + 8) {                       // the token's own entry is one of these
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (v + j == id) o[j] = head::own_ds_of(x[j], z, c, rest[t]);
       }
     }
     *reinterpret_cast<uint4*>(dst + v) = *reinterpret_cast<uint4*>(o);

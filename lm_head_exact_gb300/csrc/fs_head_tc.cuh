@@ -201,6 +201,34 @@ __device__ __forceinline__ __nv_bfloat16 ds_of(float x, float lse, float coef) {
   return __float2bfloat16_rn(coef == 0.0f ? 0.0f : -coef * __expf(x - lse));
 }
 
+// The tokens t whose own rows are among the 32 rows from m_warp on, in order,
+// with the row's number; the whole warp looks at 128 tokens at a time and
+// visits each one found together.
+template <typename Visit>
+__device__ __forceinline__ void each_own(const Args& a, int m_warp, Visit visit) {
+  const int lane = threadIdx.x & 31;
+  const int n = static_cast<int>(a.p.n), first = static_cast<int>(a.v0) + m_warp;
+  for (int t0 = 0; t0 < n; t0 += 128) {
+    int row[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = t0 + k * 32 + lane;
+      row[k] = t >= 0 && t < n ? __ldg(a.own + t) - first : -1;     // (t may pass 2^31)
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t found = __ballot_sync(0xffffffffu, static_cast<unsigned>(row[k]) < 32u);
+      while (found != 0) {
+        const int src = __ffs(found) - 1;
+        found &= found - 1;
+        visit(t0 + k * 32 + src, __shfl_sync(0xffffffffu, row[k], src));
+        __syncwarp();
+      }
+    }
+    if (n - t0 <= 128) break;
+  }
+}
+
 template <Kind kKind, bool kBias>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -523,9 +551,21 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       int use = 0;
       for (Units<kKind> u(a, pair); u.more(); u.next(), ++use) {
         const int acc = use & 1;
+        const int m_warp = u.mt() * kTileM + static_cast<int>(rank) * 128 + quad * 32;
+        // kDw: the tokens whose own rows these are, looked for while the tile
+        // is still being multiplied; the first two are kept
+        int hits = 0, hit_t[2] = {0, 0}, hit_row[2] = {-1, -1};
+        if constexpr (kKind == kDw) {
+          if (cols > 0) {
+            each_own(a, m_warp, [&](int t, int row) {
+              if (hits == 0) { hit_t[0] = t; hit_row[0] = row; }
+              if (hits == 1) { hit_t[1] = t; hit_row[1] = row; }
+              ++hits;
+            });
+          }
+        }
         if (!mbar_wait(&tfull_bar[acc], (use >> 1) & 1, a.err, abort_flag)) break;
         tc_fence_after();
-        const int m_warp = u.mt() * kTileM + static_cast<int>(rank) * 128 + quad * 32;
         const int64_t n_first = static_cast<int64_t>(u.nt()) * a.bn + col0;
         if constexpr (kKind == kDh) {
           const int64_t m = m_warp + lane;
@@ -559,37 +599,30 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
             for (int j = 0; j < 16; ++j) x[c + j] = __uint_as_float(r[j]);
           }
           release(acc);
-          const int first = static_cast<int>(a.v0) + m_warp;
-          for (int64_t t0 = 0; t0 < a.p.n && cols > 0; t0 += 128) {
-            int id[4];
+          auto add_rest = [&](int t, int row) {
+            if (row != lane) return;
+            const float rest = a.rest[t];
+            const uint4* h = reinterpret_cast<const uint4*>(a.h + t * a.N + n_first);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) id[k] = t0 + k * 32 + lane < a.p.n ? __ldg(a.own + t0 + k * 32 + lane) : -1;
+            for (int q = 0; q < kBoxCols / 8; ++q) {
+              if (n_first + q * 8 >= a.N) break;
+              const uint4 v = __ldg(h + q);
+              const __nv_bfloat162* two = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t hits = __ballot_sync(0xffffffffu, static_cast<unsigned>(id[k] - first) < 32u);
-              while (hits != 0) {
-                const int src = __ffs(hits) - 1;
-                hits &= hits - 1;
-                if (__shfl_sync(0xffffffffu, id[k], src) - first != lane) continue;
-                const int64_t t = t0 + k * 32 + src;
-                const float rest = a.rest[t];
-                const uint4* h = reinterpret_cast<const uint4*>(a.h + t * a.N + n_first);
-#pragma unroll
-                for (int q = 0; q < kBoxCols / 8; ++q) {
-                  if (n_first + q * 8 >= a.N) break;
-                  const uint4 v = __ldg(h + q);
-                  const __nv_bfloat162* two = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const float2 f = __bfloat1622float2(two[j]);
-                    x[q * 8 + 2 * j] = fmaf(rest, f.x, x[q * 8 + 2 * j]);
-                    x[q * 8 + 2 * j + 1] = fmaf(rest, f.y, x[q * 8 + 2 * j + 1]);
-                  }
-                }
+              for (int j = 0; j < 4; ++j) {
+                const float2 f = __bfloat1622float2(two[j]);
+                x[q * 8 + 2 * j] = fmaf(rest, f.x, x[q * 8 + 2 * j]);
+                x[q * 8 + 2 * j + 1] = fmaf(rest, f.y, x[q * 8 + 2 * j + 1]);
               }
-              __syncwarp();
             }
+          };
+          if (hits <= 2) {
+            if (hits > 0) add_rest(hit_t[0], hit_row[0]);
+            if (hits > 1) add_rest(hit_t[1], hit_row[1]);
+          } else {
+            each_own(a, m_warp, add_rest);
           }
+          __syncwarp();
           // to the warp's box, its 16-byte pieces swizzled as the tensor map
           // says (no bank conflicts), then out by TMA
           uint8_t* box = out + warp * kBoxBytes;

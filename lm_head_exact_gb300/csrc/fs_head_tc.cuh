@@ -289,9 +289,11 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
     const uint32_t elected = elect_one();
     // A comes from HBM once and is read by every column tile: where there are
     // several, what one of them loaded must outlast the output written in
-    // between (grad_W of 528 rows: 427 us with evict_first, 361 so).
-    const uint64_t pol_a = a.n_nt > 1 ? policy_evict_last() : policy_evict_first();
-    const uint64_t pol_b = policy_evict_last();
+    // between (grad_W of 528 rows: 427 us with evict_first, 363 with the normal
+    // priority; the highest one, 361, would stay in L2 after the kernel).  B is
+    // h, small and read by all, but for kDh, where it is streamed like A.
+    const uint64_t pol_a = a.n_nt > 1 ? policy_evict_normal() : policy_evict_first();
+    const uint64_t pol_b = kKind == kDh ? policy_evict_normal() : policy_evict_last();
     const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
     const uint32_t leader0 = mapa_shared(full0, 0);
     const uint32_t smem0 = smem_u32(smem);

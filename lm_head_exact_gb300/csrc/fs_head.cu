@@ -73,42 +73,54 @@ __global__ void __launch_bounds__(kMergeThreads) head_merge_kernel(const HeadPro
   logp[t] = lp;
 }
 
-__global__ void __launch_bounds__(256) head_rows_kernel(const HeadProblem p, const float* logp, const float* lse,
-                                                        const float* g, float* coef, int* own, float* rest,
-                                                        __nv_bfloat16* h_live) {
-  const int64_t t = blockIdx.x;
-  pdl_launch_dependents();
-  pdl_wait();
+// A row's coefficient c = g / T, 0 where it carries no gradient.
+__device__ __forceinline__ float row_coef(const HeadRows& r, const HeadProblem& p, int64_t t) {
   const RowTemp rt = row_temp(p.temp[t]);
   const int64_t id = p.ids[t];
-  const bool live = rt.mode != kRowInvalid && id >= 0 && id < p.V && g[t] != 0.0f && lse[t] != -INFINITY &&
-                    logp[t] != -INFINITY;
+  const float g = r.g[t];
+  const bool live = rt.mode != kRowInvalid && id >= 0 && id < p.V && g != 0.0f && r.lse[t] != -INFINITY &&
+                    r.logp[t] != -INFINITY;
+  return live ? g * rt.inv_t : 0.0f;
+}
+
+// What the later launches need of a row, written by one block of 256 threads.
+// (rest is written with the token's own entry of ds; rows without one have
+// own = -1.)
+__device__ __forceinline__ void write_row(const HeadRows& r, const HeadProblem& p, int64_t t, float coef) {
   if (threadIdx.x == 0) {
-    coef[t] = live ? g[t] * rt.inv_t : 0.0f;
-    own[t] = live ? static_cast<int>(id) : -1;
-    rest[t] = 0.0f;
+    r.coef[t] = coef;
+    r.own[t] = coef != 0.0f ? static_cast<int>(p.ids[t]) : -1;
   }
-  if (h_live == nullptr) return;
+  if (r.h_live == nullptr) return;
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.h) + t * p.d);
-  uint4* dst = reinterpret_cast<uint4*>(h_live + t * p.d);
-  for (int64_t i = threadIdx.x; i < p.d / 8; i += 256) dst[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(r.h_live) + t * p.d);
+  for (int64_t i = threadIdx.x; i < p.d / 8; i += 256) dst[i] = coef != 0.0f ? src[i] : make_uint4(0, 0, 0, 0);
+}
+
+__global__ void __launch_bounds__(256) head_rows_kernel(const HeadProblem p, const HeadRows r) {
+  pdl_launch_dependents();
+  pdl_wait();
+  write_row(r, p, blockIdx.x, row_coef(r, p, blockIdx.x));
 }
 
 // ds of vocabulary rows [v0, v0 + vc) from the kept logits: 4 bytes read and 2
-// written per element, 8 elements a thread.  The pitches are multiples of 64
-// elements and v0 of 256, so every group of 8 is aligned; columns in [vc,
-// pitch) hold what the padding of `kept` gives and are never read.
-__global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, const float* lse, const float* coef,
-                                                           const float* kept, int64_t kept_pitch, int64_t v0,
-                                                           __nv_bfloat16* ds, int64_t pitch, float* rest) {
+// written per element, 8 elements a thread; the first piece's blocks write the
+// rows besides.  The pitches are multiples of 64 elements and v0 of 256, so
+// every group of 8 is aligned; columns in [vc, pitch) hold what the padding of
+// `kept` gives and are never read.
+__global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, const HeadRows r, const float* kept,
+                                                           int64_t kept_pitch, int64_t v0, __nv_bfloat16* ds,
+                                                           int64_t pitch) {
   const int64_t t = blockIdx.x;
   pdl_launch_dependents();
   pdl_wait();
-  const float c = coef[t], z = lse[t];
+  const float c = row_coef(r, p, t), z = r.lse[t];
+  if (v0 == 0 && blockIdx.y == 0) write_row(r, p, t, c);
   const int64_t id = p.ids[t] - v0;
   const float* src = kept + t * kept_pitch + v0;
   __nv_bfloat16* dst = ds + t * pitch;
   const int64_t stride = static_cast<int64_t>(gridDim.y) * 256 * 8;
+#pragma unroll 2
   for (int64_t v = (static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x) * 8; v < pitch; v += stride) {
     __align__(16) __nv_bfloat16 o[8];
     if (c == 0.0f) {
@@ -122,7 +134,7 @@ __global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, 
       if (id >= v && id < v + 8) {                       // the token's own entry is one of these
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (v + j == id) o[j] = head::own_ds_of(x[j], z, c, rest[t]);
+          if (v + j == id) o[j] = head::own_ds_of(x[j], z, c, r.rest[t]);
       }
     }
     *reinterpret_cast<uint4*>(dst + v) = *reinterpret_cast<uint4*>(o);
@@ -242,6 +254,11 @@ cudaError_t launch(const Args& a, const CUtensorMap& ta, const CUtensorMap& tb, 
                        dim3(head::kThreads), smem, stream, true, ta, tb, tout, a);
 }
 
+// The priority of a bf16 operand that `readers` tiles read each part of.
+head::Keep keep_of(int64_t elements, int readers) {
+  return 2 * elements <= head::kKeepBytes ? head::kLong : readers > 1 ? head::kNormal : head::kStream;
+}
+
 int pairs_for(int64_t units) { return static_cast<int>(std::min<int64_t>(resident_pairs(), units)); }
 
 // The product x^T = W h^T over vocabulary rows [v0, v0 + vc).
@@ -262,6 +279,8 @@ cudaError_t launch_logits(Args a, int64_t v0, int64_t vc, cudaStream_t stream) {
   a.n_kb = k_blocks(p.d);
   a.splits = 1;
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
+  a.keep_a = keep_of(vc * p.d, a.n_nt);
+  a.keep_b = keep_of(p.n * p.d, a.n_mt);
   a.v0 = v0;
   return p.bias != nullptr ? launch<kKind, true>(a, tw, th, tw, stream) : launch<kKind, false>(a, tw, th, tw, stream);
 }
@@ -293,28 +312,30 @@ cudaError_t launch_head_merge(const HeadProblem& p, const LsePart* parts, int64_
                        dim3(kMergeThreads), 0, stream, false, p, parts, n_parts, own_x, logp, lse);
 }
 
-cudaError_t launch_head_rows(const HeadProblem& p, const float* logp, const float* lse, const float* g, float* coef,
-                             int* own, float* rest, void* h_live, cudaStream_t stream) {
-  return launch_kernel(head_rows_kernel, dim3(static_cast<unsigned>(p.n)), dim3(256), 0, stream, true, p, logp, lse,
-                       g, coef, own, rest, static_cast<__nv_bfloat16*>(h_live));
-}
-
-cudaError_t launch_head_ds(const HeadProblem& p, const float* lse, const float* coef, const float* kept, int64_t v0,
-                           int64_t vc, void* ds, float* rest, int* err, cudaStream_t stream) {
+cudaError_t launch_head_ds(const HeadProblem& p, const HeadRows& r, const float* kept, int64_t v0, int64_t vc, void* ds,
+                           int* err, cudaStream_t stream) {
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(ds);
   const int64_t pitch = padded_cols(vc);
   if (kept != nullptr) {
-    const int64_t blocks = std::min<int64_t>((pitch + 2047) / 2048, 64);
+    // a block of a large batch takes 8192 columns, so that reading the row's
+    // scalars is paid for; a block of a small one 2048, so that there are enough
+    const int64_t span = p.n * pitch >= (int64_t(1) << 24) ? 8192 : 2048;
+    const int64_t blocks = std::min<int64_t>((pitch + span - 1) / span, 65535);
     return launch_kernel(head_ds_kept_kernel, dim3(static_cast<unsigned>(p.n), static_cast<unsigned>(blocks)),
-                         dim3(256), 0, stream, true, p, lse, coef, kept, padded_cols(p.V), v0, out, pitch, rest);
+                         dim3(256), 0, stream, true, p, r, kept, padded_cols(p.V), v0, out, pitch);
+  }
+  if (v0 == 0) {
+    const cudaError_t e = launch_kernel(head_rows_kernel, dim3(static_cast<unsigned>(p.n)), dim3(256), 0, stream, true,
+                                        p, r);
+    if (e != cudaSuccess) return e;
   }
   Args a{};
   a.p = p;
-  a.lse = lse;
-  a.coef = coef;
+  a.lse = r.lse;
+  a.coef = r.coef;
   a.ds = out;
   a.ds_pitch = pitch;
-  a.rest = rest;
+  a.rest = r.rest;
   a.err = err;
   return launch_logits<head::kDs>(a, v0, vc, stream);
 }
@@ -360,20 +381,23 @@ cudaError_t launch_head_dh(const HeadProblem& p, const void* ds, int64_t v0, int
   a.n_kb = k_blocks(vc);
   a.splits = static_cast<int>(std::min<int64_t>(splits, a.n_kb));
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt * a.splits);
+  a.keep_a = keep_of(vc * p.d, a.n_nt);
+  a.keep_b = keep_of(p.n * padded_cols(vc), a.n_mt);
   a.partials = partials;
   a.add = add;
   a.err = err;
   return launch<head::kDh, false>(a, tw, ts, tw, stream);
 }
 
-cudaError_t launch_head_dh_sum(const HeadProblem& p, const float* partials, int64_t splits, const int* own,
-                               const float* rest, void* grad_h, cudaStream_t stream) {
+cudaError_t launch_head_dh_sum(const HeadProblem& p, const HeadRows& r, const float* partials, int64_t splits,
+                               void* grad_h, cudaStream_t stream) {
   return launch_kernel(head_dh_sum_kernel, dim3(static_cast<unsigned>((p.n * p.d / 4 + 255) / 256)), dim3(256), 0,
-                       stream, false, p, partials, splits, own, rest, static_cast<__nv_bfloat16*>(grad_h));
+                       stream, false, p, partials, splits, static_cast<const int*>(r.own), static_cast<const float*>(r.rest),
+                       static_cast<__nv_bfloat16*>(grad_h));
 }
 
-cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_live, const int* own, float* rest,
-                           int64_t v0, int64_t vc, void* grad_W, int* err, cudaStream_t stream) {
+cudaError_t launch_head_dw(const HeadProblem& p, const HeadRows& r, const void* ds, int64_t v0, int64_t vc,
+                           void* grad_W, int* err, cudaStream_t stream) {
   Args a{};
   a.p = p;
   a.M = vc;
@@ -381,7 +405,7 @@ cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_l
   a.bn = p.d <= 128 ? 128 : head::kMaxN;
   CUtensorMap th, ts, tg;
   if (!encode_rows_bf16(&ts, ds, p.n, vc, padded_cols(vc), head::kBK) ||
-      !encode_rows_bf16(&th, h_live, p.n, p.d, p.d, head::kBK) ||
+      !encode_rows_bf16(&th, r.h_live, p.n, p.d, p.d, head::kBK) ||
       !encode_rows_bf16(&tg, static_cast<uint16_t*>(grad_W) + v0 * p.d, vc, p.d, p.d, 32))
     return cudaErrorInvalidValue;
   a.n_stages = stages_for<head::kDw>(a.bn);
@@ -390,10 +414,12 @@ cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_l
   a.n_kb = k_blocks(p.n);
   a.splits = 1;
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
+  a.keep_a = keep_of(p.n * padded_cols(vc), a.n_nt);
+  a.keep_b = keep_of(p.n * p.d, a.n_mt);
   a.v0 = v0;
-  a.rest = rest;
-  a.own = own;
-  a.h = static_cast<const __nv_bfloat16*>(h_live);
+  a.rest = r.rest;
+  a.own = r.own;
+  a.h = static_cast<const __nv_bfloat16*>(r.h_live);
   a.err = err;
   return launch<head::kDw, false>(a, ts, th, tg, stream);
 }

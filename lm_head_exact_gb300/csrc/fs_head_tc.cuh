@@ -68,6 +68,20 @@ constexpr int kBoxBytes = 32 * kBoxCols * 2;
 constexpr int out_bytes(Kind k) { return k == kDw ? kEpiWarps * kBoxBytes : 0; }
 constexpr int kSmemLimit = 232448;
 
+// L2 priority of an operand.  One that is read once gives way first.  One that
+// several tiles read must outlast the output written in between (grad_W of 528
+// rows: 427 us with kStream, 363 with kNormal).  One of at most kKeepBytes is
+// read again by the next launches (W by the backward pass, ds by both products)
+// and gives way last: a training pass over 257 rows of a 520 x 32001 head takes
+// 107 us so and 117 without.  A larger one would not be there any more, and
+// would only stay in the way of what follows.
+enum Keep : int { kStream, kNormal, kLong };
+constexpr int64_t kKeepBytes = int64_t(48) << 20;
+
+__device__ __forceinline__ uint64_t policy_of(Keep k) {
+  return k == kStream ? policy_evict_first() : k == kNormal ? policy_evict_normal() : policy_evict_last();
+}
+
 struct Args {
   HeadProblem p;
   int64_t M, N;              // extents of this launch's product
@@ -78,6 +92,7 @@ struct Args {
   int n_kb;                  // k blocks of the whole product
   int splits;                // kDh
   int n_pairs;               // pairs of the grid
+  Keep keep_a, keep_b;       // the operands' L2 priorities
   // kLse
   LsePart* parts;            // [parts, n]
   float* own_x;              // [n]
@@ -287,13 +302,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
     // tile of 256 columns multiplies and twice as long as one of 128.
     pdl_wait();
     const uint32_t elected = elect_one();
-    // A comes from HBM once and is read by every column tile: where there are
-    // several, what one of them loaded must outlast the output written in
-    // between (grad_W of 528 rows: 427 us with evict_first, 363 with the normal
-    // priority; the highest one, 361, would stay in L2 after the kernel).  B is
-    // h, small and read by all, but for kDh, where it is streamed like A.
-    const uint64_t pol_a = a.n_nt > 1 ? policy_evict_normal() : policy_evict_first();
-    const uint64_t pol_b = kKind == kDh ? policy_evict_normal() : policy_evict_last();
+    const uint64_t pol_a = policy_of(a.keep_a), pol_b = policy_of(a.keep_b);
     const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
     const uint32_t leader0 = mapa_shared(full0, 0);
     const uint32_t smem0 = smem_u32(smem);

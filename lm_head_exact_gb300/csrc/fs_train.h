@@ -40,23 +40,30 @@ cudaError_t launch_head_parts(const HeadProblem& p, LsePart* parts, float* own_x
 cudaError_t launch_head_merge(const HeadProblem& p, const LsePart* parts, int64_t n_parts, const float* own_x,
                               float* logp, float* lse, cudaStream_t stream);
 
-// Backward.  Rows' coefficients c = g / T, their tokens' ids (0 and -1 for rows
-// without a gradient) and h with those rows zeroed (nullable); ds of
-// vocabulary rows [v0, v0 + vc) as bf16 [n, padded_cols(vc)], from kept logits
-// or from h and W, and what rounding left over of each token's own entry
-// (rest, cleared with the coefficients); the two products; and the sum of
-// grad_h's split partials.
-cudaError_t launch_head_rows(const HeadProblem& p, const float* logp, const float* lse, const float* g, float* coef,
-                             int* own, float* rest, void* h_live, cudaStream_t stream);
-cudaError_t launch_head_ds(const HeadProblem& p, const float* lse, const float* coef, const float* kept, int64_t v0,
-                           int64_t vc, void* ds, float* rest, int* err, cudaStream_t stream);
+// Backward: what is known of the rows, and what launch_head_ds() leaves of them
+// for the products.
+struct HeadRows {
+  const float* logp;
+  const float* lse;
+  const float* g;
+  float* coef;              // [n] g / T, 0 for rows without a gradient
+  int* own;                 // [n] their tokens' ids, -1 for rows without a gradient
+  float* rest;              // [n] what rounding left over of the tokens' own entries of ds
+  void* h_live;             // bf16 [n, d] h, those rows zeroed; nullable (no grad_W)
+};
+
+// ds of vocabulary rows [v0, v0 + vc) as bf16 [n, padded_cols(vc)], from kept
+// logits or from h and W; the two products; and the sum of grad_h's split
+// partials.
+cudaError_t launch_head_ds(const HeadProblem& p, const HeadRows& r, const float* kept, int64_t v0, int64_t vc, void* ds,
+                           int* err, cudaStream_t stream);
 int64_t head_dh_splits(int64_t n, int64_t d, int64_t vc);
 cudaError_t launch_head_dh(const HeadProblem& p, const void* ds, int64_t v0, int64_t vc, int64_t splits, bool add,
                            float* partials, int* err, cudaStream_t stream);
-cudaError_t launch_head_dh_sum(const HeadProblem& p, const float* partials, int64_t splits, const int* own,
-                               const float* rest, void* grad_h, cudaStream_t stream);
-cudaError_t launch_head_dw(const HeadProblem& p, const void* ds, const void* h_live, const int* own, float* rest,
-                           int64_t v0, int64_t vc, void* grad_W, int* err, cudaStream_t stream);
+cudaError_t launch_head_dh_sum(const HeadProblem& p, const HeadRows& r, const float* partials, int64_t splits,
+                               void* grad_h, cudaStream_t stream);
+cudaError_t launch_head_dw(const HeadProblem& p, const HeadRows& r, const void* ds, int64_t v0, int64_t vc,
+                           void* grad_W, int* err, cudaStream_t stream);
 
 struct PolicyProblem {
   const float* logp;

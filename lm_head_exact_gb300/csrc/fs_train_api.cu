@@ -201,19 +201,18 @@ fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, in
   int* err = nullptr;
   FS_API_TRY(api_error_word(&err, stream));
   FS_API_TRY(api_check_launch());
-  FS_API_TRY(api_launched(launch_head_rows(p, logp, lse, grad_logp, w.coef, w.own, w.rest, grad_W != nullptr ? w.h_live : nullptr, stream),
-                          "row coefficient launch"));
+  const HeadRows r{logp, lse, grad_logp, w.coef, w.own, w.rest, grad_W != nullptr ? w.h_live : nullptr};
   for (int64_t v0 = 0; v0 < V; v0 += w.chunk) {
     const int64_t vc = std::min(w.chunk, V - v0);
-    FS_API_TRY(api_launched(launch_head_ds(p, lse, w.coef, kept, v0, vc, w.ds, w.rest, err, stream), "logit gradient launch"));
+    FS_API_TRY(api_launched(launch_head_ds(p, r, kept, v0, vc, w.ds, err, stream), "logit gradient launch"));
     if (grad_W != nullptr)
-      FS_API_TRY(api_launched(launch_head_dw(p, w.ds, w.h_live, w.own, w.rest, v0, vc, grad_W, err, stream), "grad_W launch"));
+      FS_API_TRY(api_launched(launch_head_dw(p, r, w.ds, v0, vc, grad_W, err, stream), "grad_W launch"));
     if (grad_h != nullptr)
       FS_API_TRY(api_launched(launch_head_dh(p, w.ds, v0, vc, w.splits, v0 > 0, w.partials, err, stream),
                               "grad_h launch"));
   }
   if (grad_h != nullptr)
-    FS_API_TRY(api_launched(launch_head_dh_sum(p, w.partials, w.splits, w.own, w.rest, grad_h, stream), "grad_h sum launch"));
+    FS_API_TRY(api_launched(launch_head_dh_sum(p, r, w.partials, w.splits, grad_h, stream), "grad_h sum launch"));
   return FS_OK;
   });
 }

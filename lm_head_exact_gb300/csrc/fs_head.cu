@@ -278,6 +278,7 @@ cudaError_t launch_logits(Args a, int64_t v0, int64_t vc, cudaStream_t stream) {
   a.n_mt = row_tiles(vc);
   a.n_kb = k_blocks(p.d);
   a.splits = 1;
+  a.sub = head::sub_blocks(p.n);
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
   a.keep_a = keep_of(vc * p.d, a.n_nt);
   a.keep_b = keep_of(p.n * p.d, a.n_mt);
@@ -380,6 +381,7 @@ cudaError_t launch_head_dh(const HeadProblem& p, const void* ds, int64_t v0, int
   a.n_mt = row_tiles(p.d);
   a.n_kb = k_blocks(vc);
   a.splits = static_cast<int>(std::min<int64_t>(splits, a.n_kb));
+  a.sub = head::kWhole;
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt * a.splits);
   a.keep_a = keep_of(vc * p.d, a.n_nt);
   a.keep_b = keep_of(p.n * padded_cols(vc), a.n_mt);
@@ -413,6 +415,7 @@ cudaError_t launch_head_dw(const HeadProblem& p, const HeadRows& r, const void* 
   a.n_mt = row_tiles(vc);
   a.n_kb = k_blocks(p.n);
   a.splits = 1;
+  a.sub = head::kWhole;
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
   a.keep_a = keep_of(p.n * padded_cols(vc), a.n_nt);
   a.keep_b = keep_of(p.n * p.d, a.n_mt);

@@ -54,14 +54,16 @@ constexpr int epi_bytes(Kind k) { return epi_arrays(k) * kEpiWarps * kPartCols *
 // The tensor cores add to an accumulator in TMEM by cutting, not rounding: each
 // of the d / 16 additions of a logit loses half a step of the running sum on
 // average, always toward zero, which for d = 4096 shrinks x by 5e-6 and moves
-// lse by 1e-6 of itself.  So logits are accumulated 32 k blocks (2048 products)
-// at a time and the pieces are added in registers, rounding to nearest: half
-// of that at d = 4096, and no more at larger d.  (16 k blocks halve it again,
-// but then the epilogue of a tile outlasts the two accumulators' products:
-// 405 instead of 345 us for 528 rows of a 4096 x 128256 head.)  The gradients,
-// rounded to 8 bits in the end, take their whole sums.
-constexpr int kSubBlocks = 32;
-constexpr int sub_blocks(Kind k) { return k == kLse || k == kDs ? kSubBlocks : 0x7fffffff; }
+// lse by 1e-6 of itself.  So logits are accumulated sub_blocks k blocks of 64
+// products at a time and the pieces are added in registers, rounding to
+// nearest: 16 blocks for up to 256 tokens, one column tile, where the head's way
+// from HBM hides it (2e-7 of lse at any d; 8 blocks halve that and cost 10 of
+// 165 us), and 32 beyond (4e-7), where smaller pieces end sooner than the
+// epilogue of the tile before (528 rows of a 4096 x 128256 head: 350 us with
+// 32, 405 with 16).  The gradients, rounded to 8 bits in the end, take their
+// whole sums.
+constexpr int sub_blocks(int64_t n) { return n <= 256 ? 16 : 32; }
+constexpr int kWhole = 0x7fffffff;
 // kDw: a box of 32 vocabulary rows x 64 columns of bf16 a warp, on its way out.
 constexpr int kBoxCols = 64;
 constexpr int kBoxBytes = 32 * kBoxCols * 2;
@@ -91,6 +93,7 @@ struct Args {
   int n_mt;                  // row tiles
   int n_kb;                  // k blocks of the whole product
   int splits;                // kDh
+  int sub;                   // k blocks that one accumulator takes
   int n_pairs;               // pairs of the grid
   Keep keep_a, keep_b;       // the operands' L2 priorities
   // kLse
@@ -363,7 +366,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       for (Units<kKind> u(a, pair); ok && u.more(); u.next()) {
         const int k1 = u.k1();
         for (int kb0 = u.k0(), n_kb; ok && kb0 < k1; kb0 += n_kb, ++use) {
-          n_kb = min(sub_blocks(kKind), k1 - kb0);
+          n_kb = min(a.sub, k1 - kb0);
           const int acc = use & 1;
           ok = mbar_wait_warp(smem_u32(&tempty_bar[acc]), ((use >> 1) & 1) ^ 1, a.err, abort_flag);
           if (!ok) break;
@@ -461,7 +464,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
             }
           }
         }
-        for (int kb0 = 0; kb0 < a.n_kb; kb0 += kSubBlocks, ++use) {
+        for (int kb0 = 0; kb0 < a.n_kb; kb0 += a.sub, ++use) {
           const int acc = use & 1;
           if (!mbar_wait(&tfull_bar[acc], (use >> 1) & 1, a.err, abort_flag)) { ok = false; break; }
           tc_fence_after();

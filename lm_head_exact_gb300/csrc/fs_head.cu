@@ -19,19 +19,21 @@ namespace {
 using head::lse_join;
 
 // Merge of the parts [n_parts, n] of kMergeRows tokens a block.  Every thread
-// joins every 64th part of one token, 8 loads in flight and one rescaling for
-// each 8 (one at a time took three times as long: the loads waited for the
-// exponentials); then the block's threads are joined.
+// joins every (kThreads / 4)th part of one token, 8 loads in flight and one
+// rescaling for each 8 (one at a time took three times as long: the loads
+// waited for the exponentials); then the block's threads are joined.  Blocks of
+// 1024 threads where there are few, of 256 where there are enough (10 and 7 us
+// for 528 tokens of 128256 words, 20 and 28 for 2048).
 constexpr int kMergeRows = 4;
-constexpr int kMergeThreads = 256;
 
-__global__ void __launch_bounds__(kMergeThreads) head_merge_kernel(const HeadProblem p, const LsePart* parts,
-                                                                   int64_t n_parts, const float* own_x, float* logp,
-                                                                   float* lse) {
-  __shared__ LsePart warps[kMergeThreads / 32][kMergeRows];
-  constexpr int kSlices = kMergeThreads / kMergeRows;
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) head_merge_kernel(const HeadProblem p, const LsePart* parts,
+                                                              int64_t n_parts, const float* own_x, float* logp,
+                                                              float* lse) {
+  __shared__ LsePart warps[32][kMergeRows];
+  constexpr int kSlices = kThreads / kMergeRows;
   const int row = threadIdx.x & (kMergeRows - 1);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kMergeRows + row;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kMergeRows + row;
   pdl_launch_dependents();
   pdl_wait();
   LsePart part{head::kLowest, 0.0f};
@@ -57,9 +59,15 @@ __global__ void __launch_bounds__(kMergeThreads) head_merge_kernel(const HeadPro
     part = lse_join(part, LsePart{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o)});
   if ((threadIdx.x & 31) < kMergeRows) warps[threadIdx.x >> 5][row] = part;
   __syncthreads();
-  if (threadIdx.x >= kMergeRows || t >= p.n) return;
+  // a warp for each token
+  const int lane = threadIdx.x & 31;
+  t = static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 5);
+  if (threadIdx.x >= 32 * kMergeRows || t >= p.n) return;
+  part = lane < kThreads / 32 ? warps[lane][threadIdx.x >> 5] : LsePart{head::kLowest, 0.0f};
 #pragma unroll
-  for (int w = 1; w < kMergeThreads / 32; ++w) part = lse_join(part, warps[w][row]);
+  for (int o = 16; o > 0; o >>= 1)
+    part = lse_join(part, LsePart{__shfl_xor_sync(0xffffffffu, part.m, o), __shfl_xor_sync(0xffffffffu, part.s, o)});
+  if (lane != 0) return;
   const bool valid = row_temp(p.temp[t]).mode != kRowInvalid;
   const int64_t id = p.ids[t];
   float z = !valid || part.s == 0.0f ? -INFINITY : part.m + logf(part.s);
@@ -309,8 +317,10 @@ cudaError_t launch_head_parts(const HeadProblem& p, LsePart* parts, float* own_x
 
 cudaError_t launch_head_merge(const HeadProblem& p, const LsePart* parts, int64_t n_parts, const float* own_x,
                               float* logp, float* lse, cudaStream_t stream) {
-  return launch_kernel(head_merge_kernel, dim3(static_cast<unsigned>((p.n + kMergeRows - 1) / kMergeRows)),
-                       dim3(kMergeThreads), 0, stream, false, p, parts, n_parts, own_x, logp, lse);
+  const int64_t blocks = (p.n + kMergeRows - 1) / kMergeRows;
+  const bool few = blocks <= 192;
+  return launch_kernel(few ? head_merge_kernel<1024> : head_merge_kernel<256>, dim3(static_cast<unsigned>(blocks)),
+                       dim3(few ? 1024 : 256), 0, stream, false, p, parts, n_parts, own_x, logp, lse);
 }
 
 cudaError_t launch_head_ds(const HeadProblem& p, const HeadRows& r, const float* kept, int64_t v0, int64_t vc, void* ds,

@@ -20,8 +20,8 @@
 
 #include <algorithm>
 
-#include "fs_sm100.cuh"
-#include "fs_tmap.h"
+#include "fs_head_ptx.cuh"
+#include "fs_head_tmap.h"
 #include "fs_train.h"
 
 namespace fs {

@@ -15,9 +15,4 @@ namespace fs {
 bool encode_kmajor_bf16(CUtensorMap* tm, const void* base, int64_t rows, int64_t d, int box_cols,
                         int box_rows);
 
-// The same for a matrix [rows, cols] whose rows lie `pitch` elements apart
-// (a multiple of 8).  Boxes of 64 columns; 64 columns by k rows of an operand
-// stored along its M or N axis are what the MN-major descriptors expect.
-bool encode_rows_bf16(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int64_t pitch, int box_rows);
-
 }  // namespace fs

@@ -364,6 +364,7 @@ FS_API fs_status fs_sample_noalloc(const void* h, const void* W, int64_t B, int6
  *   kept (nullable): fp32 [fs_logprob_buffer_elems(n, V)] where the call
  *     leaves the logits for fs_token_logprobs_backward, 16-byte aligned.
  *     Without it the n x V logits never reach device memory.
+ *   n, V <= 2^31 - 1024 (else FS_ERR_UNSUPPORTED).
  *   workspace: fs_token_logprobs_workspace_bytes(n, d, V) bytes.
  */
 FS_API fs_status fs_token_logprobs(const void* h, const void* W, int64_t n, int64_t d, int64_t V,

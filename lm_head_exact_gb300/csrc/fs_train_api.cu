@@ -11,6 +11,7 @@
 namespace fs {
 namespace {
 
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1024;
 constexpr size_t kAlign = 256;
 size_t aligned(size_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
 
@@ -91,6 +92,15 @@ fs_status find_workspace(void** workspace, size_t have, size_t need, cudaStream_
   return api_check_array(*workspace, 16, "workspace");
 }
 
+// Sizes that the sampler takes, less the last few: tile coordinates, which may
+// run past the end by a tile, stay within 31 bits.
+fs_status check_sizes(int64_t n, int64_t d, int64_t V) {
+  FS_API_TRY(api_check_shapes(n, d, V));
+  if (n > kMaxRows || V > kMaxRows)
+    return api_fail(FS_ERR_UNSUPPORTED, "n and V must be <= %lld", static_cast<long long>(kMaxRows));
+  return FS_OK;
+}
+
 fs_status check_head(const HeadProblem& p) {
   FS_API_TRY(api_check_array(p.h, 16, "h"));
   FS_API_TRY(api_check_array(p.ids, 8, "ids"));
@@ -143,7 +153,7 @@ fs_status fs_token_logprobs(const void* h, const void* W, int64_t n, int64_t d, 
                             float* kept, void* workspace, size_t workspace_bytes, void* stream_) {
   api_begin();
   return guarded([&]() -> fs_status {
-  FS_API_TRY(api_check_shapes(n, d, V));
+  FS_API_TRY(check_sizes(n, d, V));
   if (n == 0) return FS_OK;
   const HeadProblem p{h, W, n, d, V, ids, temp, bias, bias_row_stride};
   FS_API_TRY(check_head(p));
@@ -173,7 +183,7 @@ fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, in
                                      void* workspace, size_t workspace_bytes, void* stream_) {
   api_begin();
   return guarded([&]() -> fs_status {
-  FS_API_TRY(api_check_shapes(n, d, V));
+  FS_API_TRY(check_sizes(n, d, V));
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (grad_h != nullptr && n > 0) FS_API_TRY(api_check_array(grad_h, 16, "grad_h"));
   if (grad_W != nullptr && V > 0) FS_API_TRY(api_check_array(grad_W, 16, "grad_W"));

@@ -625,3 +625,38 @@ def test_policy_and_clip_in_a_graph(fs, torch_cuda):
         s2, g2 = fs.policy_loss(a[0], a[1], a[2], seq_starts=starts, mask=a[3], ref_logp=a[4], kl_coef=0.1, mean="sequence")
         assert torch.equal(stats, s2) and torch.equal(grad, g2)
         assert abs(float(norm) - k * float(src.double().norm())) <= 40 * U * float(norm) and float(g.norm()) <= 1.0001
+
+
+def test_injected_failures_are_reported_and_passed(fs, torch_cuda):
+    """A failing launch or allocation comes back as the call's error, and the
+    next call works."""
+    torch = torch_cuda
+    hp = Head(20, 64, 200)
+    h, W, ids, temp, _, g = hp.device(torch)
+    logp, lse = fs.token_logprobs(h, W, ids, temp)
+    calls = [lambda s=None: fs.token_logprobs(h, W, ids, temp, stream=s),
+             lambda s=None: fs.token_logprobs_backward(h, W, ids, temp, logp, lse, g, stream=s),
+             lambda s=None: fs.policy_loss(logp, logp, g, stream=s), lambda s=None: fs.clip_grad_norm([g.clone()], 1.0, stream=s)]
+    torch.cuda.synchronize()
+    for call in calls:
+        fs.debug_set_fault(fs.FS_FAULT_LAUNCH)
+        try:
+            with pytest.raises(fs.FlashSampleError) as e:
+                call()
+        finally:
+            fs.debug_set_fault(fs.FS_FAULT_NONE)
+        assert e.value.status == "FS_ERR_CUDA" and "injected" in str(e.value)
+        call()
+    for call in (calls[0], calls[2], calls[3]):              # those that need the library's block on a new stream
+        fs.check(fs.library().fs_workspace_release())
+        stream = torch.cuda.Stream()
+        fs.debug_set_fault(fs.FS_FAULT_ALLOC)
+        try:
+            with pytest.raises(fs.FlashSampleError) as e:
+                call(stream)
+        finally:
+            fs.debug_set_fault(fs.FS_FAULT_NONE)
+        assert e.value.status == "FS_ERR_WORKSPACE"
+        call(stream)
+    torch.cuda.synchronize()
+    assert fs.device_error() == 0

@@ -29,6 +29,7 @@ def test_scores_refuse(lib):
         assert f(4, 0, 10) == 1
         assert f(4, 12, 10) == 2 and "multiple of 8" in _last(lib)
         assert f(4, 64, 1 << 31) == 2
+        assert f(4, 64, (1 << 31) - 1023) == 2 and f((1 << 31) - 1023, 64, 10) == 2 and "n and V" in _last(lib)
         assert f(4, 65544, 10) == 2
         assert f(4, 64, 10) == 1 and "h is NULL" in _last(lib)
         assert f(0, 64, 10) == 0

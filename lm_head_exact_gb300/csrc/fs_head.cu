@@ -429,6 +429,11 @@ cudaError_t launch_head_dw(const HeadProblem& p, const HeadRows& r, const void* 
   a.n_pairs = pairs_for(static_cast<int64_t>(a.n_mt) * a.n_nt);
   a.keep_a = keep_of(p.n * padded_cols(vc), a.n_nt);
   a.keep_b = keep_of(p.n * p.d, a.n_mt);
+  // With few k blocks a tile there is no time to wait for ds behind the writes
+  // of a grad_W larger than L2 (256 tokens of 128256 x 4096: 305 us, with the
+  // next tile's ds brought in ahead 271; 512: 375 and 366; a 32001 x 520 grad_W,
+  // which stays in L2: 32 and 34).
+  a.prefetch = a.n_kb <= 8 && 2 * vc * p.d > (int64_t(128) << 20);
   a.v0 = v0;
   a.rest = r.rest;
   a.own = r.own;

@@ -18,6 +18,14 @@ __device__ __forceinline__ uint64_t policy_evict_normal() {
   return p;
 }
 
+// Bring a box into L2 (no shared memory, no barrier); issued by the lanes that
+// reach it.
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 // 2-D tiled store of a box from shared memory; out-of-range rows and columns
 // of the box are left out.  The writes of ordinary stores to the box are made
 // visible to it by fence_async_shared() first; the group that it is committed

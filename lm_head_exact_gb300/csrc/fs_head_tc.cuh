@@ -96,6 +96,7 @@ struct Args {
   int sub;                   // k blocks that one accumulator takes
   int n_pairs;               // pairs of the grid
   Keep keep_a, keep_b;       // the operands' L2 priorities
+  bool prefetch;             // kDw: bring the next tile's ds into L2 ahead
   // kLse
   LsePart* parts;            // [parts, n]
   float* own_x;              // [n]
@@ -317,6 +318,22 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
       const int m0 = u.mt() * kTileM + static_cast<int>(rank) * 128;
       const int n0 = u.nt() * a.bn + static_cast<int>(rank) * (a.bn / 2);
       const int k1 = u.k1();
+      if constexpr (kKind == kDw) {
+        // The next tile's ds into L2 while this one is multiplied: the column
+        // tiles that share it take a k block each in turn.
+        if (a.prefetch) {
+          Units<kKind> next = u;
+          next.next();
+          if (next.more() && elected) {
+            const int m = next.mt() * kTileM + static_cast<int>(rank) * 128;
+            for (int kb = next.nt(); kb < a.n_kb; kb += a.n_nt) {
+              tma_prefetch_2d(&tmap_a, m, kb * kBK);
+              tma_prefetch_2d(&tmap_a, m + 64, kb * kBK);
+            }
+          }
+          __syncwarp();
+        }
+      }
       for (int kb = u.k0(); kb < k1; ++kb) {
         ok = mbar_wait_warp(empty0 + stage * 8, phase ^ 1, a.err, abort_flag);
         if (!ok) break;

@@ -173,6 +173,38 @@ def test_vocabulary_in_pieces(fs, torch_cuda):
         assert bool(((got.double() - want_W).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("n", [100, 300])
+def test_a_head_larger_than_l2(fs, torch_cuda, n):
+    """139 MB of W and of grad_W, logits formed in several pieces."""
+    torch = torch_cuda
+    d, V = 4096, 17001
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    h = torch.randn(n, d, generator=gen, device="cuda").bfloat16()
+    W = (torch.randn(V, d, generator=gen, device="cuda") * 1.5 / 64).bfloat16()
+    ids = torch.randint(0, V, (n,), generator=gen, device="cuda")
+    ids[3:9] = ids[3]                                      # several tokens with one row of grad_W
+    temp, g = torch.ones(n, device="cuda"), torch.randn(n, generator=gen, device="cuda") / n
+    logp, lse = fs.token_logprobs(h, W, ids, temp)
+    gh, gW = fs.token_logprobs_backward(h, W, ids, temp, logp, lse, g)
+    h64, W64 = h.double(), W.double()
+    x = h64 @ W64.T
+    z = x.logsumexp(1)
+    rows = torch.arange(n, device="cuda")
+    # d / 16 additions, each cut by at most 2u of what they sum up to
+    tol = d / 16 * 2 * U * float((h64.abs() @ W64.abs().T).max())
+    assert float((lse.double() - z).abs().max()) < tol and float((logp.double() - (x[rows, ids] - z)).abs().max()) < 2 * tol
+    ds = -(x - z[:, None]).exp()
+    ds[rows, ids] += 1
+    ds *= g.double()[:, None]
+    own = torch.zeros_like(ds)
+    own[rows, ids] = ds[rows, ids]
+    # every entry of ds but the token's own is rounded to bf16; 2^-10 for the scores' error; results rounded once
+    for got, want, size, own_size in ((gh, ds @ W64, (ds - own).abs() @ W64.abs(), own.abs() @ W64.abs()),
+                                      (gW, ds.T @ h64, (ds - own).abs().T @ h64.abs(), own.abs().T @ h64.abs())):
+        tol = (2.0 ** -8 + 2.0 ** -10) * size + 2.0 ** -10 * own_size + 2.0 ** -8 * want.abs()
+        assert bool(((got.double() - want).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("kept", [True, False])
 @pytest.mark.parametrize("n", [9, 150])
 def test_rows_that_take_no_part(fs, torch_cuda, n, kept):

@@ -455,7 +455,7 @@ FS_API size_t fs_policy_loss_workspace_bytes(int64_t n_seqs);
  * The scaled values are formed in fp32 and rounded once.  A norm that is not
  * finite (a NaN or an infinity among the gradients, or a square above the
  * fp32 range) is reported and scales nothing.  Squares are summed in fp32
- * over 64 elements, then in fp64, in an order that does not depend on the
+ * over some 64 elements, then in fp64, in an order that does not depend on the
  * run.
  */
 FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes,

@@ -193,6 +193,8 @@ __global__ void __launch_bounds__(256) head_dh_sum_kernel(const HeadProblem p, c
 using head::Args;
 using head::Kind;
 
+constexpr int kBox = 64;                                 // columns of a TMA box: 128 bytes
+
 // Columns of a tile for n tokens: as few tiles as 256 columns allow, all of
 // one size.
 struct ColumnTiles {
@@ -275,8 +277,8 @@ cudaError_t launch_logits(Args a, int64_t v0, int64_t vc, cudaStream_t stream) {
   const HeadProblem& p = a.p;
   const ColumnTiles c = column_tiles(p.n);
   CUtensorMap tw, th;
-  if (!encode_rows_bf16(&tw, static_cast<const uint16_t*>(p.W) + v0 * p.d, vc, p.d, p.d, 128) ||
-      !encode_rows_bf16(&th, p.h, p.n, p.d, p.d, c.bn / 2))
+  if (!encode_rows_bf16(&tw, static_cast<const uint16_t*>(p.W) + v0 * p.d, vc, p.d, p.d, kBox, 128) ||
+      !encode_rows_bf16(&th, p.h, p.n, p.d, p.d, kBox, c.bn / 2))
     return cudaErrorInvalidValue;
   a.M = vc;
   a.N = p.n;
@@ -378,8 +380,8 @@ cudaError_t launch_head_dh(const HeadProblem& p, const void* ds, int64_t v0, int
                            float* partials, int* err, cudaStream_t stream) {
   const ColumnTiles c = column_tiles(p.n);
   CUtensorMap tw, ts;
-  if (!encode_rows_bf16(&tw, static_cast<const uint16_t*>(p.W) + v0 * p.d, vc, p.d, p.d, head::kBK) ||
-      !encode_rows_bf16(&ts, ds, p.n, vc, padded_cols(vc), c.bn / 2))
+  if (!encode_rows_bf16(&tw, static_cast<const uint16_t*>(p.W) + v0 * p.d, vc, p.d, p.d, kBox, head::kBK) ||
+      !encode_rows_bf16(&ts, ds, p.n, vc, padded_cols(vc), kBox, c.bn / 2))
     return cudaErrorInvalidValue;
   Args a{};
   a.p = p;
@@ -416,9 +418,9 @@ cudaError_t launch_head_dw(const HeadProblem& p, const HeadRows& r, const void* 
   a.N = p.d;
   a.bn = p.d <= 128 ? 128 : head::kMaxN;
   CUtensorMap th, ts, tg;
-  if (!encode_rows_bf16(&ts, ds, p.n, vc, padded_cols(vc), head::kBK) ||
-      !encode_rows_bf16(&th, r.h_live, p.n, p.d, p.d, head::kBK) ||
-      !encode_rows_bf16(&tg, static_cast<uint16_t*>(grad_W) + v0 * p.d, vc, p.d, p.d, 32))
+  if (!encode_rows_bf16(&ts, ds, p.n, vc, padded_cols(vc), kBox, head::kBK) ||
+      !encode_rows_bf16(&th, r.h_live, p.n, p.d, p.d, kBox, head::kBK) ||
+      !encode_rows_bf16(&tg, static_cast<uint16_t*>(grad_W) + v0 * p.d, vc, p.d, p.d, kBox, 32))
     return cudaErrorInvalidValue;
   a.n_stages = stages_for<head::kDw>(a.bn);
   a.n_nt = static_cast<int>((p.d + a.bn - 1) / a.bn);

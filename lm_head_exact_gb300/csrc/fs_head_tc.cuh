@@ -21,7 +21,7 @@
 #include <algorithm>
 
 #include "fs_head_ptx.cuh"
-#include "fs_head_tmap.h"
+#include "fs_tmap.h"
 #include "fs_train.h"
 
 namespace fs {

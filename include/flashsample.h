@@ -341,7 +341,8 @@ FS_API fs_status fs_sample_noalloc(const void* h, const void* W, int64_t B, int6
  * a fixed block (0.6 MB) per (device, stream) that the library allocates on
  * the first call; it is part of fs_workspace_reserve(), which makes the calls
  * capturable.  A captured graph uses the block of the stream it was captured
- * on: keep its replays ordered with that stream's other calls.
+ * on: keep its replays ordered with that stream's other calls.  Several host
+ * threads may use one stream: each call enqueues its launches as a whole.
  *
  * A row t takes part ("is scored") when 0 <= ids[t] < V and its temperature
  * is valid.  T > 0 divides the logits; T == 0 scores under softmax(logits),

@@ -92,9 +92,22 @@ struct Workspace {
   size_t train_bytes = 0;
 };
 
-std::mutex g_ws_mutex;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_workspaces;
+using StreamKey = std::pair<int, cudaStream_t>;
+
+std::mutex g_ws_mutex;               // of the maps below; held only while they are read or changed
+std::map<StreamKey, Workspace> g_workspaces;
+std::map<StreamKey, std::mutex> g_call_mutexes;   // CallLock's, taken before g_ws_mutex; never erased
 std::map<int, int*> g_error_words;   // per device: kernels' bounded-wait error word
+
+std::mutex& call_mutex(const StreamKey& key) {
+  static std::mutex out_of_memory;   // stands in for the ones that cannot be made
+  std::lock_guard<std::mutex> lock(g_ws_mutex);
+  try {
+    return g_call_mutexes[key];
+  } catch (...) {
+    return out_of_memory;
+  }
+}
 
 constexpr size_t kFinishHeader = 256;
 
@@ -505,6 +518,12 @@ fs_status sample_chunk(const void* h, const void* W_chunk, int64_t B, int64_t d,
 void record_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error), "%s", msg); }
 
 // ---------------------------------------------------------------- fs_api_util.h
+CallLock::CallLock(cudaStream_t stream) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();   // the call itself reports it
+  lock_ = std::unique_lock<std::mutex>(call_mutex({dev, stream}));
+}
+
 void api_begin() { g_last_error[0] = '\0'; }
 
 fs_status api_fail(fs_status s, const char* fmt, ...) {
@@ -972,22 +991,28 @@ fs_status fs_workspace_reserve(int64_t B, int64_t V, void* stream) {
 fs_status fs_workspace_release(void) {
   int dev;
   FS_TRY(current_device(&dev));
-  std::lock_guard<std::mutex> lock(g_ws_mutex);
-  for (auto it = g_workspaces.begin(); it != g_workspaces.end();) {
-    if (it->first.first == dev) {
-      cudaStreamSynchronize(it->first.second);
-      if (it->second.finish) cudaFree(it->second.finish);
-      if (it->second.unfused) cudaFree(it->second.unfused);
-      if (it->second.host_out) cudaFreeHost(it->second.host_out);
-      if (it->second.staging) cudaFree(it->second.staging);
-      if (it->second.topk) cudaFree(it->second.topk);
-      if (it->second.train) cudaFree(it->second.train);
-      it = g_workspaces.erase(it);
-    } else {
-      ++it;
+  StreamKey key{dev, nullptr};
+  for (bool first = true;; first = false) {                 // the device's streams, in the order of their keys
+    {
+      std::lock_guard<std::mutex> lock(g_ws_mutex);
+      const auto next = first ? g_workspaces.lower_bound(key) : g_workspaces.upper_bound(key);
+      if (next == g_workspaces.end() || next->first.first != dev) return FS_OK;
+      key = next->first;
     }
+    std::lock_guard<std::mutex> call(call_mutex(key));      // no call is between its launches
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
+    const auto it = g_workspaces.find(key);
+    if (it == g_workspaces.end()) continue;
+    Workspace& ws = it->second;
+    cudaStreamSynchronize(key.second);
+    if (ws.finish) cudaFree(ws.finish);
+    if (ws.unfused) cudaFree(ws.unfused);
+    if (ws.host_out) cudaFreeHost(ws.host_out);
+    if (ws.staging) cudaFree(ws.staging);
+    if (ws.topk) cudaFree(ws.topk);
+    if (ws.train) cudaFree(ws.train);
+    g_workspaces.erase(it);
   }
-  return FS_OK;
 }
 
 fs_status fs_set_path(int path) {

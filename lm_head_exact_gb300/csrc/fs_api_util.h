@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
 #include <cuda_runtime.h>
 
 #include "flashsample.h"
@@ -11,8 +12,8 @@ namespace fs {
 
 // Per-(device, stream) scratch of the training operators, of fixed size.
 // `ticket` and `count` are zero between calls: the last block of the launch
-// that used them leaves them so.  Calls on one stream are ordered, so they
-// may share it.
+// that used them leaves them so.  A call's launches are enqueued under one
+// CallLock and run in their order, so the calls of one stream may share it.
 constexpr int kTrainMaxBlocks = 2048;
 struct alignas(256) TrainScratch {
   unsigned int ticket;
@@ -22,6 +23,18 @@ struct alignas(256) TrainScratch {
   float pad2[3];
   double sums[kTrainMaxBlocks][4];      // one row per block
   alignas(256) unsigned char small[FS_SMALL_WORKSPACE];   // workspace of calls that bring none
+};
+
+// Held by a call from its first use of the stream's workspace until its last
+// launch is enqueued.  What one launch leaves there for the next (a count, a
+// factor, parts to merge) would otherwise be overwritten by a call that
+// another host thread enqueues on the same stream in between.
+class CallLock {
+ public:
+  explicit CallLock(cudaStream_t stream);
+
+ private:
+  std::unique_lock<std::mutex> lock_;
 };
 
 void api_begin();                       // clears fs_last_error()

@@ -161,6 +161,7 @@ fs_status fs_token_logprobs(const void* h, const void* W, int64_t n, int64_t d, 
   FS_API_TRY(api_check_array(lse, 4, "lse"));
   if (kept != nullptr) FS_API_TRY(api_check_array(kept, 16, "kept"));
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const CallLock lock(stream);
   FS_API_TRY(find_workspace(&workspace, workspace_bytes, forward_workspace(nullptr, n, V).bytes, stream));
   const ForwardWorkspace w = forward_workspace(workspace, n, V);
   int* err = nullptr;
@@ -206,6 +207,7 @@ fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, in
       (grad_h != nullptr && grad_W != nullptr && overlaps(grad_h, nd, grad_W, vd)))
     return api_fail(FS_ERR_INVALID_ARG, "grad_h and grad_W must not overlap each other, h or W");
   if (grad_h == nullptr && grad_W == nullptr) return FS_OK;
+  const CallLock lock(stream);
   FS_API_TRY(find_workspace(&workspace, workspace_bytes, backward_workspace(nullptr, n, d, V).bytes, stream));
   const BackwardWorkspace w = backward_workspace(workspace, n, d, V);
   int* err = nullptr;
@@ -261,6 +263,7 @@ fs_status fs_policy_loss(const float* logp, const float* old_logp, const float* 
   if (mask != nullptr) FS_API_TRY(api_check_array(mask, 1, "mask"));
   if (seq_starts != nullptr) FS_API_TRY(api_check_array(seq_starts, 8, "seq_starts"));
   FS_API_TRY(api_check_array(grad, 4, "grad"));
+  const CallLock lock(stream);
   if (mean == FS_MEAN_SEQUENCE)
     FS_API_TRY(find_workspace(&workspace, workspace_bytes, fs_policy_loss_workspace_bytes(n_seqs), stream));
   TrainScratch* scratch = nullptr;
@@ -309,6 +312,7 @@ fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, const i
     }
   }
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const CallLock lock(stream);
   TrainScratch* scratch = nullptr;
   FS_API_TRY(api_train_scratch(stream, &scratch));
   FS_API_TRY(api_check_launch());

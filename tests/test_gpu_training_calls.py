@@ -49,3 +49,62 @@ def test_first_call_of_a_host_thread(fs, torch_cuda, what):
     torch.cuda.synchronize()
     for a, b in zip(want, out):
         assert torch.equal(a, b)
+
+
+def _run_threads(torch, jobs, rounds):
+    """Every job `rounds` times on a host thread of its own, all on one stream;
+    the results of each, in order."""
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    results = [[] for _ in jobs]
+    errors = []
+    start = threading.Barrier(len(jobs))
+
+    def work(job, out):
+        try:
+            with torch.cuda.stream(stream):
+                start.wait()
+                for _ in range(rounds):
+                    out.append(job())
+        except Exception as e:                             # noqa: BLE001  (reported by the test's thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(jobs, results)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    torch.cuda.synchronize()
+    return results
+
+
+@pytest.mark.parametrize("what", ["clip", "policy", "scores"])
+def test_threads_that_share_a_stream(fs, torch_cuda, what):
+    """What a call leaves in the stream's workspace for its next launch is not
+    another thread's: every result is the one of the call made alone."""
+    torch = torch_cuda
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    jobs = []
+    for k in range(2):
+        if what == "clip":
+            grads = [rand(3000) * (k + 1), rand(500)]
+            jobs.append(lambda g=grads, m=0.5 + 4 * k: (lambda o: [fs.clip_grad_norm(g, m, out=o)] + o)(
+                [torch.empty_like(x) for x in g]))
+        elif what == "policy":
+            old = -rand(6, 300).abs()
+            args = old + 0.2 * rand(6, 300), old, rand(6)
+            mask = torch.rand(6, 300, generator=gen, device="cuda") < 0.2 + 0.6 * k
+            jobs.append(lambda a=args, m=mask, mean=("token", "sequence")[k]: fs.policy_loss(*a, mask=m, mean=mean))
+        else:
+            h, W = rand(20 + 4 * k, 64).bfloat16(), rand(700, 64).bfloat16()
+            ids, temp = torch.arange(h.shape[0], device="cuda"), torch.full((h.shape[0],), 0.7 + k, device="cuda")
+            jobs.append(lambda a=(h, W, ids, temp): fs.token_logprobs(*a))
+    alone = [job() for job in jobs]
+    torch.cuda.synchronize()
+    for want, got in zip(alone, _run_threads(torch, jobs, 400)):
+        for r in got:
+            for a, b in zip(want, r):
+                assert torch.equal(a, b)
+    assert fs.device_error() == 0

@@ -37,7 +37,9 @@
  *    counter and one packed candidate key per batch row, through which the
  *    CTAs of the fused kernel finish the sample (the last CTA to finish writes
  *    the outputs).  It grows on demand, which is not allowed inside
- *    CUDA-graph capture: call fs_workspace_reserve() first.
+ *    CUDA-graph capture: call fs_workspace_reserve() first.  Several host
+ *    threads may use one stream: each call enqueues its launches as a whole
+ *    (the chunk calls of a chunked step are calls of their own).
  *  - Errors: argument problems return FS_ERR_INVALID_ARG / FS_ERR_UNSUPPORTED
  *    before anything is enqueued; a failed CUDA call returns FS_ERR_CUDA.
  *    fs_last_error() gives a human-readable detail of the last failure on
@@ -341,8 +343,7 @@ FS_API fs_status fs_sample_noalloc(const void* h, const void* W, int64_t B, int6
  * a fixed block (0.6 MB) per (device, stream) that the library allocates on
  * the first call; it is part of fs_workspace_reserve(), which makes the calls
  * capturable.  A captured graph uses the block of the stream it was captured
- * on: keep its replays ordered with that stream's other calls.  Several host
- * threads may use one stream: each call enqueues its launches as a whole.
+ * on: keep its replays ordered with that stream's other calls.
  *
  * A row t takes part ("is scored") when 0 <= ids[t] < V and its temperature
  * is valid.  T > 0 divides the logits; T == 0 scores under softmax(logits),

@@ -594,6 +594,7 @@ fs_status fs_sample_ex(const void* h, const void* W, int64_t B, int64_t d, int64
   f.write_out = true;
   f.out_ids = out_ids;
   f.out_max = out_max;
+  const CallLock lock(static_cast<cudaStream_t>(stream));
   return run(p, f, static_cast<cudaStream_t>(stream));
 }
 
@@ -616,6 +617,7 @@ fs_status fs_debug_fused_logits(const void* h, const void* W, int64_t B, int64_t
   f.write_out = true;
   f.out_ids = out_ids;
   f.out_max = out_max;
+  const CallLock lock(static_cast<cudaStream_t>(stream));
   return run(p, f, static_cast<cudaStream_t>(stream));
 }
 
@@ -632,6 +634,7 @@ fs_status fs_sample_chunked(const void* h, const void* W_chunk, int64_t B, int64
                             float* carry_max, int64_t* carry_ids, int flags,
                             int64_t* out_ids, float* out_max, void* stream) {
   g_last_error[0] = '\0';
+  const CallLock lock(static_cast<cudaStream_t>(stream));
   return sample_chunk(h, W_chunk, B, d, v_begin, v_end, temp, bias_chunk, bias_row_stride, seed, step, carry_max,
                       carry_ids, flags, EarlyArgs{}, out_ids, out_max, stream);
 }
@@ -655,6 +658,7 @@ fs_status fs_sample_chunked_step(const void* h, const void* W, int64_t B, int64_
   Problem whole{h, W, B, d, bounds[n_chunks], 0, temp, bias, bias_row_stride, seed, step};
   FS_TRY(check_problem(whole, true, out_ids, out_max));
   FS_TRY(check_carry(B, carry_max, carry_ids));
+  const CallLock lock(static_cast<cudaStream_t>(stream));
   for (int i = 0; i < n_chunks; ++i) {
     const int flags = (i == 0 ? FS_CHUNK_FIRST : 0) | (i == n_chunks - 1 ? FS_CHUNK_LAST : 0);
     const void* W_chunk = static_cast<const uint16_t*>(W) + bounds[i] * d;
@@ -688,6 +692,7 @@ fs_status fs_sample_chunked_early(const void* h, const void* W_chunk, int64_t B,
   early.rest_w_norm = rest_w_norm;
   early.rest_bias_max = rest_bias_max;
   early.done = done;
+  const CallLock lock(static_cast<cudaStream_t>(stream));
   return sample_chunk(h, W_chunk, B, d, v_begin, v_end, temp, bias_chunk, bias_row_stride, seed, step, carry_max,
                       carry_ids, flags, early, out_ids, out_max, stream);
 }
@@ -777,6 +782,7 @@ fs_status fs_sample_host(const void* h_host, const void* W, int64_t B, int64_t d
   const size_t off_max = off_ids + static_cast<size_t>(B) * 8;
   const size_t out_bytes = static_cast<size_t>(B) * 12;
   const size_t total = off_ids + out_bytes;
+  const CallLock call(stream);     // to the end: the results leave through the stream's landing area
   char* staging = nullptr;
   char* landing = nullptr;
   char* landing_dev = nullptr;
@@ -906,6 +912,7 @@ fs_status fs_sample_topk(const void* h, const void* W, int64_t B, int64_t d, int
                                              : tc_topk_parts(B, V, dev);
   const size_t need = std::max<size_t>(static_cast<size_t>(B) * parts * K * sizeof(Partial), 256);
   Partial* partials = nullptr;
+  const CallLock call(stream);
   {
     std::lock_guard<std::mutex> lock(g_ws_mutex);
     Workspace& ws = g_workspaces[{dev, stream}];
@@ -953,6 +960,7 @@ fs_status fs_sample_unfused(const void* h, const void* W, int64_t B, int64_t d, 
   FS_TRY(current_device(&dev));
   const size_t plane = (static_cast<size_t>(B) * static_cast<size_t>(V) * 4 + 255) & ~size_t(255);
   char* buf = nullptr;
+  const CallLock call(stream);
   {
     std::lock_guard<std::mutex> lock(g_ws_mutex);
     Workspace& ws = g_workspaces[{dev, stream}];
@@ -980,6 +988,7 @@ size_t fs_workspace_bytes(int64_t B, int64_t V) {
 fs_status fs_workspace_reserve(int64_t B, int64_t V, void* stream) {
   g_last_error[0] = '\0';
   if (B < 0 || V < 0) return fail(FS_ERR_INVALID_ARG, "need B >= 0 and V >= 0");
+  const CallLock lock(static_cast<cudaStream_t>(stream));
   int* err = nullptr;
   FS_TRY(error_word(&err, static_cast<cudaStream_t>(stream)));   // once per device, never during capture
   TrainScratch* scratch = nullptr;

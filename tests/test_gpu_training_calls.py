@@ -108,3 +108,38 @@ def test_threads_that_share_a_stream(fs, torch_cuda, what):
             for a, b in zip(want, r):
                 assert torch.equal(a, b)
     assert fs.device_error() == 0
+
+
+@pytest.mark.parametrize("what", ["topk", "unfused", "host", "growing"])
+def test_threads_that_sample_on_one_stream(fs, torch_cuda, what):
+    """Staging, logits and candidate lists of one thread's call stay its own;
+    a batch that makes the workspace grow leaves the other thread's call
+    whole."""
+    torch = torch_cuda
+    gen = torch.Generator(device="cuda").manual_seed(12)
+    jobs, alone = [], []
+    rounds = 30 if what == "growing" else 200
+    for k in range(2):
+        h = torch.randn(2000, 64, generator=gen, device="cuda").bfloat16()
+        W = torch.randn(900, 64, generator=gen, device="cuda").bfloat16()
+        temp = torch.full((2000,), 0.5 + k, device="cuda")
+        n = 12 + 8 * k
+        if what == "topk":
+            job = lambda i, h=h, W=W, t=temp, n=n: fs.sample_topk(h[:n], W, t[:n], 5, 6, 4)  # noqa: E731
+        elif what == "unfused":
+            job = lambda i, h=h, W=W, t=temp, n=n: fs.sample_unfused(h[:n], W, t[:n], 5, 6)  # noqa: E731
+        elif what == "host":
+            hh, th = h[:n].cpu(), temp[:n].cpu()
+            job = lambda i, hh=hh, W=W, th=th: [torch.from_numpy(a) for a in fs.sample_host(hh, W, th, 5, 6)]  # noqa: E731
+        else:
+            job = lambda i, h=h, W=W, t=temp, k=k: (lambda n: fs.sample(h[:n], W, t[:n], 5, 6))(  # noqa: E731
+                16 + 60 * i * k)
+        jobs.append((lambda f, at: lambda: f(next(at)))(job, iter(range(rounds))))
+        alone.append([job(i) for i in range(rounds if what == "growing" else 1)])
+    torch.cuda.synchronize()
+    for want, got in zip(alone, _run_threads(torch, jobs, rounds)):
+        assert len(got) == rounds
+        for i, r in enumerate(got):
+            for a, b in zip(want[i % len(want)], r):
+                assert torch.equal(a, b)
+    assert fs.device_error() == 0

@@ -39,7 +39,9 @@
  *    the outputs).  It grows on demand, which is not allowed inside
  *    CUDA-graph capture: call fs_workspace_reserve() first.  Several host
  *    threads may use one stream: each call enqueues its launches as a whole
- *    (the chunk calls of a chunked step are calls of their own).
+ *    (the chunk calls of a chunked step are calls of their own).  On
+ *    cudaStreamPerThread every thread has a workspace of its own, kept until
+ *    fs_workspace_release().
  *  - Errors: argument problems return FS_ERR_INVALID_ARG / FS_ERR_UNSUPPORTED
  *    before anything is enqueued; a failed CUDA call returns FS_ERR_CUDA.
  *    fs_last_error() gives a human-readable detail of the last failure on

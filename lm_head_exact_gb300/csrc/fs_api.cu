@@ -10,6 +10,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -92,7 +93,17 @@ struct Workspace {
   size_t train_bytes = 0;
 };
 
-using StreamKey = std::pair<int, cudaStream_t>;
+// The handle cudaStreamPerThread names another stream in each host thread, so
+// there the key holds the thread's number too (0 for every other stream).
+using StreamKey = std::tuple<int, cudaStream_t, uint64_t>;
+
+StreamKey stream_key(int dev, cudaStream_t stream) {
+  static std::atomic<uint64_t> threads{0};
+  thread_local uint64_t mine = 0;
+  if (stream != cudaStreamPerThread) return {dev, stream, 0};
+  if (mine == 0) mine = ++threads;
+  return {dev, stream, mine};
+}
 
 std::mutex g_ws_mutex;               // of the maps below; held only while they are read or changed
 std::map<StreamKey, Workspace> g_workspaces;
@@ -167,7 +178,7 @@ fs_status next_chunk_set(cudaStream_t stream, bool first, bool last, int* set, b
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   std::lock_guard<std::mutex> lock(g_ws_mutex);
-  Workspace& ws = g_workspaces[{dev, stream}];
+  Workspace& ws = g_workspaces[stream_key(dev, stream)];
   ws.chunk_seq = first ? 0 : ws.chunk_seq + 1;
   *set = static_cast<int>(ws.chunk_seq % kKeySets);
   *overlap_ok = first || *set != 0;
@@ -183,7 +194,7 @@ fs_status get_finish(cudaStream_t stream, int64_t B, Finish* f, int set = 0) {
   fs_status s = current_device(&dev);
   if (s != FS_OK) return s;
   std::lock_guard<std::mutex> lock(g_ws_mutex);
-  Workspace& ws = g_workspaces[{dev, stream}];
+  Workspace& ws = g_workspaces[stream_key(dev, stream)];
   const size_t need = finish_bytes_for(B);
   if (ws.finish_bytes < need) {
     s = grow(&ws.finish, &ws.finish_bytes, need, stream);
@@ -521,7 +532,7 @@ void record_error(const char* msg) { snprintf(g_last_error, sizeof(g_last_error)
 CallLock::CallLock(cudaStream_t stream) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) cudaGetLastError();   // the call itself reports it
-  lock_ = std::unique_lock<std::mutex>(call_mutex({dev, stream}));
+  lock_ = std::unique_lock<std::mutex>(call_mutex(stream_key(dev, stream)));
 }
 
 void api_begin() { g_last_error[0] = '\0'; }
@@ -555,7 +566,7 @@ fs_status api_train_scratch(cudaStream_t stream, TrainScratch** out) {
   int dev;
   FS_TRY(current_device(&dev));
   std::lock_guard<std::mutex> lock(g_ws_mutex);
-  Workspace& ws = g_workspaces[{dev, stream}];
+  Workspace& ws = g_workspaces[stream_key(dev, stream)];
   if (ws.train == nullptr) {
     FS_TRY(grow(&ws.train, &ws.train_bytes, sizeof(TrainScratch), stream));
     // on the call's stream, which the kernels that use it follow on
@@ -788,7 +799,7 @@ fs_status fs_sample_host(const void* h_host, const void* W, int64_t B, int64_t d
   char* landing_dev = nullptr;
   {
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Workspace& ws = g_workspaces[{dev, stream}];
+    Workspace& ws = g_workspaces[stream_key(dev, stream)];
     FS_TRY(grow(&ws.staging, &ws.staging_bytes, total, stream));
     staging = static_cast<char*>(ws.staging);
     if (ws.host_out_bytes < out_bytes) {
@@ -915,7 +926,7 @@ fs_status fs_sample_topk(const void* h, const void* W, int64_t B, int64_t d, int
   const CallLock call(stream);
   {
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Workspace& ws = g_workspaces[{dev, stream}];
+    Workspace& ws = g_workspaces[stream_key(dev, stream)];
     FS_TRY(grow(&ws.topk, &ws.topk_bytes, need, stream));
     partials = static_cast<Partial*>(ws.topk);
   }
@@ -963,7 +974,7 @@ fs_status fs_sample_unfused(const void* h, const void* W, int64_t B, int64_t d, 
   const CallLock call(stream);
   {
     std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Workspace& ws = g_workspaces[{dev, stream}];
+    Workspace& ws = g_workspaces[stream_key(dev, stream)];
     FS_TRY(grow(&ws.unfused, &ws.unfused_bytes, (logits_out ? plane : 2 * plane) + unfused_partial_bytes(B),
                 stream));
     buf = static_cast<char*>(ws.unfused);
@@ -1000,12 +1011,12 @@ fs_status fs_workspace_reserve(int64_t B, int64_t V, void* stream) {
 fs_status fs_workspace_release(void) {
   int dev;
   FS_TRY(current_device(&dev));
-  StreamKey key{dev, nullptr};
+  StreamKey key{dev, nullptr, 0};
   for (bool first = true;; first = false) {                 // the device's streams, in the order of their keys
     {
       std::lock_guard<std::mutex> lock(g_ws_mutex);
       const auto next = first ? g_workspaces.lower_bound(key) : g_workspaces.upper_bound(key);
-      if (next == g_workspaces.end() || next->first.first != dev) return FS_OK;
+      if (next == g_workspaces.end() || std::get<0>(next->first) != dev) return FS_OK;
       key = next->first;
     }
     std::lock_guard<std::mutex> call(call_mutex(key));      // no call is between its launches
@@ -1013,7 +1024,10 @@ fs_status fs_workspace_release(void) {
     const auto it = g_workspaces.find(key);
     if (it == g_workspaces.end()) continue;
     Workspace& ws = it->second;
-    cudaStreamSynchronize(key.second);
+    if (std::get<1>(key) == cudaStreamPerThread)
+      cudaDeviceSynchronize();                              // perhaps another thread's: not to be named here
+    else
+      cudaStreamSynchronize(std::get<1>(key));
     if (ws.finish) cudaFree(ws.finish);
     if (ws.unfused) cudaFree(ws.unfused);
     if (ws.host_out) cudaFreeHost(ws.host_out);

@@ -143,3 +143,40 @@ def test_threads_that_sample_on_one_stream(fs, torch_cuda, what):
             for a, b in zip(want[i % len(want)], r):
                 assert torch.equal(a, b)
     assert fs.device_error() == 0
+
+
+def test_the_per_thread_stream_is_each_threads_own(fs, torch_cuda):
+    """One handle, two streams: calls that run at the same time share neither
+    counts nor tickets."""
+    torch = torch_cuda
+    per_thread = torch.cuda.ExternalStream(2)              # cudaStreamPerThread
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    rounds, S, L = 100, 64, 500
+    cases, outs, alone = [], [], []
+    for k in range(2):
+        old = -torch.rand(S, L, generator=gen, device="cuda")
+        logp = old + 0.2 * torch.randn(S, L, generator=gen, device="cuda")
+        adv = torch.randn(S, generator=gen, device="cuda")
+        mask = torch.rand(S, L, generator=gen, device="cuda") < 0.2 + 0.6 * k
+        cases.append((logp, old, adv, mask))
+        outs.append([(torch.zeros(4, device="cuda"), torch.zeros(S, L, device="cuda")) for _ in range(rounds)])
+        alone.append(fs.policy_loss(logp, old, adv, mask=mask))
+    torch.cuda.synchronize()
+
+    def work(k):
+        logp, old, adv, mask = cases[k]
+        for out in outs[k]:
+            fs.policy_loss(logp, old, adv, mask=mask, out=out, stream=per_thread)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for want, got in zip(alone, outs):
+        for r in got:
+            for a, b in zip(want, r):
+                assert torch.equal(a, b)
+    fs.check(fs.library().fs_workspace_release())
+    assert fs.device_error() == 0

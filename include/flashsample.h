@@ -538,13 +538,15 @@ FS_API fs_status fs_debug_wait_timeout(uint64_t timeout_ns, void* stream);
  * FS_FAULT_ALLOC makes every workspace allocation that would happen fail with
  * FS_ERR_WORKSPACE, FS_FAULT_LAUNCH makes every fused sampling launch fail
  * with FS_ERR_CUDA -- before any CUDA call is made, so the GPU and the
- * context are untouched and later calls work once FS_FAULT_NONE is set.  The
- * initial value comes from the FS_FAULT environment variable ("alloc",
- * "launch"; anything else: none).
+ * context are untouched and later calls work once FS_FAULT_NONE is set.
+ * FS_FAULT_LATER_LAUNCH lets the counting launch of fs_policy_loss run and
+ * fails the one after it.  The initial value comes from the FS_FAULT
+ * environment variable ("alloc", "launch", "later"; anything else: none).
  */
 #define FS_FAULT_NONE 0
 #define FS_FAULT_ALLOC 1
 #define FS_FAULT_LAUNCH 2
+#define FS_FAULT_LATER_LAUNCH 3
 FS_API fs_status fs_debug_set_fault(int kind);
 
 /* Static name of a status code. */

@@ -22,7 +22,7 @@ FS_CHUNK_FIRST = 1
 FS_CHUNK_LAST = 2
 FS_CHUNK_SERIAL = 4
 FS_PATH_AUTO, FS_PATH_SIMT, FS_PATH_TC_VOCAB, FS_PATH_TC_BATCH, FS_PATH_TC_PAIR = 0, 1, 2, 3, 4
-FS_FAULT_NONE, FS_FAULT_ALLOC, FS_FAULT_LAUNCH = 0, 1, 2
+FS_FAULT_NONE, FS_FAULT_ALLOC, FS_FAULT_LAUNCH, FS_FAULT_LATER_LAUNCH = 0, 1, 2, 3
 FS_MEAN_TOKEN, FS_MEAN_SEQUENCE, FS_MEAN_NONE = 0, 1, 2
 FS_TYPE_F32, FS_TYPE_BF16, FS_TYPE_F16 = 0, 1, 2
 FS_NORM_L2, FS_NORM_MAX = 0, 1

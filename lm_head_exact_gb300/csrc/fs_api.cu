@@ -28,7 +28,7 @@ std::atomic<int> g_forced_path{kPathAuto};
 std::atomic<int> g_launch_overlap{1};
 
 // Host-side fault injection (FS_FAULT_*): read from the FS_FAULT environment
-// variable ("alloc" or "launch") on first use, or set by fs_debug_set_fault.
+// variable ("alloc", "launch" or "later") on first use, or set by fs_debug_set_fault.
 // An injected fault makes the library return the error of the failing call
 // without touching the GPU.
 std::atomic<int> g_fault{-1};
@@ -38,7 +38,10 @@ int injected_fault() {
   if (f < 0) {
     const char* env = getenv("FS_FAULT");
     f = env == nullptr ? FS_FAULT_NONE
-                       : (strcmp(env, "alloc") == 0 ? FS_FAULT_ALLOC : strcmp(env, "launch") == 0 ? FS_FAULT_LAUNCH : FS_FAULT_NONE);
+        : strcmp(env, "alloc") == 0  ? FS_FAULT_ALLOC
+        : strcmp(env, "launch") == 0 ? FS_FAULT_LAUNCH
+        : strcmp(env, "later") == 0  ? FS_FAULT_LATER_LAUNCH
+                                     : FS_FAULT_NONE;
     g_fault.store(f);
   }
   return f;
@@ -560,6 +563,8 @@ fs_status api_check_launch() {
   return FS_OK;
 }
 
+bool api_later_launch_fails() { return injected_fault() == FS_FAULT_LATER_LAUNCH; }
+
 fs_status api_error_word(int** out, cudaStream_t stream) { return error_word(out, stream); }
 
 fs_status api_train_scratch(cudaStream_t stream, TrainScratch** out) {
@@ -1046,7 +1051,7 @@ fs_status fs_set_path(int path) {
 
 fs_status fs_debug_set_fault(int kind) {
   g_last_error[0] = '\0';
-  if (kind < FS_FAULT_NONE || kind > FS_FAULT_LAUNCH) return fail(FS_ERR_INVALID_ARG, "unknown fault kind %d", kind);
+  if (kind < FS_FAULT_NONE || kind > FS_FAULT_LATER_LAUNCH) return fail(FS_ERR_INVALID_ARG, "unknown fault kind %d", kind);
   g_fault.store(kind);
   return FS_OK;
 }

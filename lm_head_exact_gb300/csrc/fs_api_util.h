@@ -46,6 +46,8 @@ fs_status api_check_array(const void* p, size_t align, const char* name);
 fs_status api_check_shapes(int64_t B, int64_t d, int64_t V);
 // The injected launch failure (FS_FAULT_LAUNCH), where one is set.
 fs_status api_check_launch();
+// Whether a call's launches after its first are to fail (FS_FAULT_LATER_LAUNCH).
+bool api_later_launch_fails();
 fs_status api_error_word(int** out, cudaStream_t stream);
 fs_status api_train_scratch(cudaStream_t stream, TrainScratch** out);
 

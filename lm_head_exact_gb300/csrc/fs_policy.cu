@@ -336,9 +336,16 @@ cudaError_t launch_policy_loss(const PolicyProblem& p, cudaStream_t stream) {
   const bool by_seq = p.adv_per_seq || p.mean == FS_MEAN_SEQUENCE;
   const auto kernel = vec ? (by_seq ? policy_loss_kernel<true, true> : policy_loss_kernel<true, false>)
                           : (by_seq ? policy_loss_kernel<false, true> : policy_loss_kernel<false, false>);
-  return launch_kernel(kernel,
-                       dim3(static_cast<unsigned>(std::max<int64_t>(blocks, 1))), dim3(kThreads), 0, stream, counted,
-                       p, counted);
+  if (counted && api_later_launch_fails())
+    e = cudaErrorLaunchOutOfResources;
+  else
+    e = launch_kernel(kernel, dim3(static_cast<unsigned>(std::max<int64_t>(blocks, 1))), dim3(kThreads), 0, stream,
+                      counted, p, counted);
+  // The loss kernel would have left the count at zero for the next call.
+  if (e != cudaSuccess && counted &&
+      cudaMemsetAsync(&p.scratch->count, 0, sizeof(p.scratch->count), stream) != cudaSuccess)
+    cudaGetLastError();
+  return e;
 }
 
 }  // namespace fs

@@ -180,3 +180,25 @@ def test_the_per_thread_stream_is_each_threads_own(fs, torch_cuda):
                 assert torch.equal(a, b)
     fs.check(fs.library().fs_workspace_release())
     assert fs.device_error() == 0
+
+
+@pytest.mark.parametrize("mean", ["token", "sequence"])
+def test_a_loss_launch_that_fails_leaves_no_count(fs, torch_cuda, mean):
+    """The counting launch has run, the one that takes the count away has not:
+    the next call counts from zero."""
+    torch = torch_cuda
+    gen = torch.Generator(device="cuda").manual_seed(14)
+    old = -torch.rand(5, 40, generator=gen, device="cuda")
+    mask = torch.rand(5, 40, generator=gen, device="cuda") < 0.5
+    args = old + 0.1, old, torch.randn(5, generator=gen, device="cuda")
+    want = fs.policy_loss(*args, mask=mask, mean=mean)
+    for _ in range(2):
+        fs.debug_set_fault(fs.FS_FAULT_LATER_LAUNCH)
+        try:
+            with pytest.raises(fs.FlashSampleError) as e:
+                fs.policy_loss(*args, mask=mask, mean=mean)
+        finally:
+            fs.debug_set_fault(fs.FS_FAULT_NONE)
+        assert e.value.status == "FS_ERR_CUDA"
+    for a, b in zip(want, fs.policy_loss(*args, mask=mask, mean=mean)):
+        assert torch.equal(a, b)

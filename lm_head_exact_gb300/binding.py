@@ -163,6 +163,21 @@ def _bias_args(bias, B, V):
     return ptr, 0
 
 
+def _made_on(stream, device, make):
+    """The tensors that make() allocates, for a call that writes them on
+    ``stream``: from that stream's memory, for what the current stream frees
+    may still be in use there.  They are marked as used on the current stream,
+    where the caller reads them once it has waited for ``stream``."""
+    torch = _torch()
+    if stream is None or stream == (current := torch.cuda.current_stream(device)):
+        return make()
+    with torch.cuda.stream(stream):
+        made = make()
+    for t in made:
+        t.record_stream(current)
+    return made
+
+
 def _outs(B, device, out):
     torch = _torch()
     if out is not None:
@@ -495,10 +510,12 @@ def _workspace(nbytes, device, stream):
     return t, t.data_ptr()
 
 
-def logprob_buffer(n, V, device="cuda"):
+def logprob_buffer(n, V, device="cuda", stream=None):
     """The fp32 buffer in which ``token_logprobs`` leaves the logits of n rows
-    for ``token_logprobs_backward``."""
-    return _torch().empty(_kept_elems(n, V), dtype=_torch().float32, device=device)
+    for ``token_logprobs_backward``; ``stream``: the one that those calls are
+    given, if not the current one."""
+    torch = _torch()
+    return _made_on(stream, device, lambda: (torch.empty(_kept_elems(n, V), dtype=torch.float32, device=device),))[0]
 
 
 def _kept_arg(kept, n, V):
@@ -523,7 +540,7 @@ def token_logprobs(h, W, ids, temp, bias=None, kept=None, out=None, stream=None)
     args = _head_args(h, W, ids, temp, bias)
     n, d, V = args[2:5]
     if out is None:
-        out = (torch.empty_like(temp), torch.empty_like(temp))
+        out = _made_on(stream, temp.device, lambda: (torch.empty_like(temp), torch.empty_like(temp)))
     logp, lse = out
     nbytes = _forward_bytes(n, d, V)
     work, where = _workspace(nbytes, h.device, stream)
@@ -545,9 +562,9 @@ def token_logprobs_backward(h, W, ids, temp, logp, lse, grad_logp, bias=None, ke
     n, d, V = args[2:5]
     grad_h, grad_W = out if out is not None else (None, None)
     if need_h and grad_h is None:
-        grad_h = torch.empty_like(h)
+        grad_h, = _made_on(stream, h.device, lambda: (torch.empty_like(h),))
     if need_W and grad_W is None:
-        grad_W = torch.empty_like(W)
+        grad_W, = _made_on(stream, h.device, lambda: (torch.empty_like(W),))
     nbytes = _backward_bytes(n, d, V)
     work, where = _workspace(nbytes, h.device, stream)
     check(library().fs_token_logprobs_backward(
@@ -598,7 +615,8 @@ def policy_loss(logp, old_logp, advantages, seq_starts=None, mask=None, ref_logp
         adv_per_seq = advantages.shape != shape
     adv = _arg(advantages, "advantages", f32, (S,) if adv_per_seq else shape)
     if out is None:
-        out = torch.empty(4, dtype=f32, device=logp.device), torch.empty_like(logp)
+        out = _made_on(stream, logp.device,
+                       lambda: (torch.empty(4, dtype=f32, device=logp.device), torch.empty_like(logp)))
     stats, grad = out
     lib = library()
     work, where, nbytes = None, None, 0
@@ -651,7 +669,8 @@ def clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, stream=None):
             raise FlashSampleError("FS_ERR_INVALID_ARG", "an output must be a contiguous CUDA tensor of its "
                                    "gradient's type and shape")
         outs = array("Q", map(tensor.data_ptr, out))
-    norm = torch.empty((), dtype=torch.float32, device=grads[0].device if n else "cuda")
+    device = grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    norm, = _made_on(stream, device, lambda: (torch.empty((), dtype=torch.float32, device=device),))
     check(library().fs_clip_grad_norm(pointers.buffer_info()[0], outs.buffer_info()[0], sizes.buffer_info()[0],
                                       types.buffer_info()[0], n, max_norm,
                                       FS_NORM_L2 if norm_type == 2 else FS_NORM_MAX, norm.data_ptr(),

@@ -202,3 +202,59 @@ def test_a_loss_launch_that_fails_leaves_no_count(fs, torch_cuda, mean):
         assert e.value.status == "FS_ERR_CUDA"
     for a, b in zip(want, fs.policy_loss(*args, mask=mask, mean=mean)):
         assert torch.equal(a, b)
+
+
+def _on_another_stream(torch, shapes, call, use):
+    """call(stream)'s results, made while the current stream has yet to read
+    tensors of these shapes and types that the program has dropped: none of
+    the results may lie in their memory."""
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    dropped = [torch.full(s, 3.0, device="cuda").to(t) for s, t in shapes for _ in range(3)]
+    addresses = {t.data_ptr() for t in dropped}
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)                          # some 10 ms of the current stream
+    read = [t.clone() for t in dropped]
+    dropped.clear()
+    results = call(side)
+    assert not addresses & {t.data_ptr() for t in results}
+    torch.cuda.current_stream().wait_stream(side)
+    got = [t.clone() for t in results]
+    del results
+    torch.cuda.synchronize()
+    assert all(bool((t == 3).all()) for t in read)
+    for a, b in zip(use, got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("what", ["scores", "gradients", "policy", "clip"])
+def test_results_on_a_given_stream(fs, torch_cuda, what):
+    """With stream=, the results' memory is not still in use on the current
+    stream, and the results are the same."""
+    torch = torch_cuda
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    n, d, V = 200, 64, 3000
+    h, W = (torch.randn(m, d, generator=gen, device="cuda").bfloat16() for m in (n, V))
+    ids, temp = torch.randint(0, V, (n,), generator=gen, device="cuda"), torch.ones(n, device="cuda")
+    logp, lse = fs.token_logprobs(h, W, ids, temp)
+    old = logp - 0.1                                       # (every input is there before the current stream is held up)
+    f32, bf16 = torch.float32, torch.bfloat16
+    if what == "scores":
+        shapes = [((n,), f32)]
+        call = lambda s=None: list(fs.token_logprobs(h, W, ids, temp, stream=s))  # noqa: E731
+    elif what == "gradients":
+        shapes = [((n, d), bf16), ((V, d), bf16), ((fs.logprob_buffer(n, V).numel(),), f32)]
+
+        def call(s=None):
+            kept = fs.logprob_buffer(n, V, stream=s)
+            a, b = fs.token_logprobs(h, W, ids, temp, kept=kept, stream=s)
+            return [*fs.token_logprobs_backward(h, W, ids, temp, a, b, temp, kept=kept, stream=s)]
+    elif what == "policy":
+        shapes = [((4,), f32), ((n,), f32)]
+        call = lambda s=None: list(fs.policy_loss(logp, old, lse, stream=s))  # noqa: E731
+    else:
+        shapes = [((), f32)]
+        call = lambda s=None: [fs.clip_grad_norm([logp], float("inf"), stream=s)]  # noqa: E731
+    want = call()
+    _on_another_stream(torch, shapes, call, want)

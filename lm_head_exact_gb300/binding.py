@@ -169,7 +169,10 @@ def _made_on(stream, device, make):
     may still be in use there.  They are marked as used on the current stream,
     where the caller reads them once it has waited for ``stream``."""
     torch = _torch()
-    if stream is None or stream == (current := torch.cuda.current_stream(device)):
+    if stream is None or torch.device(device).type != "cuda":  # (tensors elsewhere are refused by the call's checks)
+        return make()
+    current = torch.cuda.current_stream(device)
+    if stream == current:
         return make()
     with torch.cuda.stream(stream):
         made = make()
@@ -178,12 +181,12 @@ def _made_on(stream, device, make):
     return made
 
 
-def _outs(B, device, out):
+def _outs(B, device, out, stream):
     torch = _torch()
     if out is not None:
         return out
-    return (torch.empty(B, dtype=torch.int64, device=device),
-            torch.empty(B, dtype=torch.float32, device=device))
+    return _made_on(stream, device, lambda: (torch.empty(B, dtype=torch.int64, device=device),
+                                             torch.empty(B, dtype=torch.float32, device=device)))
 
 
 def sample(h, W, temp, seed, step, bias=None, out=None, stream=None):
@@ -196,7 +199,7 @@ def sample(h, W, temp, seed, step, bias=None, out=None, stream=None):
     torch = _torch()
     B, d = h.shape
     V = W.shape[0]
-    ids, mx = _outs(B, h.device, out)
+    ids, mx = _outs(B, h.device, out, stream)
     bptr, bstride = _bias_args(bias, B, V)
     check(library().fs_sample_ex(_dev(h, "h", torch.bfloat16, 2), _dev(W, "W", torch.bfloat16, 2),
                                  B, d, V, _dev(temp, "temp", torch.float32, 1), bptr, bstride,
@@ -213,8 +216,9 @@ def debug_fused_logits(h, W, temp, seed, step, bias=None, stream=None):
     torch = _torch()
     B, d = h.shape
     V = W.shape[0]
-    ids, mx = _outs(B, h.device, None)
-    logits = torch.full((B, V), float("nan"), dtype=torch.float32, device=h.device)
+    ids, mx = _outs(B, h.device, None, stream)
+    logits, = _made_on(stream, h.device, lambda: (torch.full((B, V), float("nan"), dtype=torch.float32,
+                                                             device=h.device),))
     bptr, bstride = _bias_args(bias, B, V)
     check(library().fs_debug_fused_logits(_dev(h, "h", torch.bfloat16, 2), _dev(W, "W", torch.bfloat16, 2),
                                           B, d, V, _dev(temp, "temp", torch.float32, 1), bptr, bstride,
@@ -231,7 +235,7 @@ def sample_unfused(h, W, temp, seed, step, bias=None, logits_out=None, out=None,
     torch = _torch()
     B, d = h.shape
     V = W.shape[0]
-    ids, mx = _outs(B, h.device, out)
+    ids, mx = _outs(B, h.device, out, stream)
     bptr, bstride = _bias_args(bias, B, V)
     lptr = _dev(logits_out, "logits_out", torch.float32) if logits_out is not None else ctypes.c_void_p(0)
     check(library().fs_sample_unfused(_dev(h, "h", torch.bfloat16, 2), _dev(W, "W", torch.bfloat16, 2),
@@ -252,7 +256,7 @@ def combine_shards(shard_max, shard_ids, out=None, stream=None):
     Returns (ids int64 [B], max fp32 [B])."""
     torch = _torch()
     R, B = shard_max.shape
-    ids, mx = _outs(B, shard_max.device, out)
+    ids, mx = _outs(B, shard_max.device, out, stream)
     check(library().fs_combine_shards(
         _dev(shard_max, "shard_max", torch.float32, 2), _dev(shard_ids, "shard_ids", torch.int64, 2), R, B,
         _dev(ids, "out_ids"), _dev(mx, "out_max"), _stream_ptr(stream)))
@@ -284,12 +288,13 @@ def sample_tp(h, W_shard, v_begin, temp, seed, step, group=None, bias_shard=None
     the whole vocabulary."""
     torch = _torch()
     B = h.shape[0]
-    cm = torch.empty(B, dtype=torch.float32, device=h.device)
-    ci = torch.empty(B, dtype=torch.int64, device=h.device)
-    local = sample_chunked(h, W_shard, v_begin, temp, seed, step, cm, ci, True, True, bias_chunk=bias_shard,
-                           stream=stream)
-    all_max, all_ids = tp_exchange(local[1], local[0], group=group)
-    return combine_shards(all_max, all_ids, stream=stream)
+    out = _outs(B, h.device, None, stream)
+    with torch.cuda.stream(stream):                        # (None: the current one) the exchange follows the sample
+        cm = torch.empty(B, dtype=torch.float32, device=h.device)
+        ci = torch.empty(B, dtype=torch.int64, device=h.device)
+        local = sample_chunked(h, W_shard, v_begin, temp, seed, step, cm, ci, True, True, bias_chunk=bias_shard)
+        all_max, all_ids = tp_exchange(local[1], local[0], group=group)
+        return combine_shards(all_max, all_ids, out=out)
 
 
 def sample_topk(h, W, temp, seed, step, k, bias=None, out=None, stream=None):
@@ -301,8 +306,8 @@ def sample_topk(h, W, temp, seed, step, k, bias=None, out=None, stream=None):
     B, d = h.shape
     V = W.shape[0]
     if out is None:
-        out = (torch.empty((B, k), dtype=torch.int64, device=h.device),
-               torch.empty((B, k), dtype=torch.float32, device=h.device))
+        out = _made_on(stream, h.device, lambda: (torch.empty((B, k), dtype=torch.int64, device=h.device),
+                                                  torch.empty((B, k), dtype=torch.float32, device=h.device)))
     ids, z = out
     bptr, bstride = _bias_args(bias, B, V)
     check(library().fs_sample_topk(
@@ -323,7 +328,7 @@ def sample_chunked(h, W_chunk, v_begin, temp, seed, step, carry_max, carry_ids, 
     flags = (FS_CHUNK_FIRST if first else 0) | (FS_CHUNK_LAST if last else 0) | (FS_CHUNK_SERIAL if serial else 0)
     ids = mx = None
     if last:
-        ids, mx = _outs(B, h.device, out)
+        ids, mx = _outs(B, h.device, out, stream)
     bptr, bstride = _bias_args(bias_chunk, B, W_chunk.shape[0])
     check(library().fs_sample_chunked(
         _dev(h, "h", torch.bfloat16, 2), _dev(W_chunk, "W_chunk", torch.bfloat16, 2), B, d,
@@ -346,7 +351,7 @@ def sample_chunked_step(h, W, bounds, temp, seed, step, carry_max, carry_ids, bi
     n = len(b) - 1
     if n < 1 or b[-1] != W.shape[0]:
         raise FlashSampleError("FS_ERR_INVALID_ARG", "bounds must have >= 2 entries ending at W.shape[0]")
-    ids, mx = _outs(B, h.device, out)
+    ids, mx = _outs(B, h.device, out, stream)
     bptr, bstride = _bias_args(bias, B, W.shape[0])
     check(library().fs_sample_chunked_step(
         _dev(h, "h", torch.bfloat16, 2), _dev(W, "W", torch.bfloat16, 2), B, d, ctypes.c_void_p(b.ctypes.data), n,
@@ -371,7 +376,7 @@ def sample_chunked_early(h, W_chunk, v_begin, temp, seed, step, carry_max, carry
     flags = (FS_CHUNK_FIRST if first else 0) | (FS_CHUNK_LAST if last else 0) | (FS_CHUNK_SERIAL if serial else 0)
     ids = mx = None
     if last:
-        ids, mx = _outs(B, h.device, out)
+        ids, mx = _outs(B, h.device, out, stream)
     bptr, bstride = _bias_args(bias_chunk, B, W_chunk.shape[0])
     check(library().fs_sample_chunked_early(
         _dev(h, "h", torch.bfloat16, 2), _dev(W_chunk, "W_chunk", torch.bfloat16, 2), B, d,
@@ -388,7 +393,7 @@ def row_norms(X, out=None, stream=None):
     torch = _torch()
     n, d = X.shape
     if out is None:
-        out = torch.empty(n, dtype=torch.float32, device=X.device)
+        out, = _made_on(stream, X.device, lambda: (torch.empty(n, dtype=torch.float32, device=X.device),))
     check(library().fs_row_norms(_dev(X, "X", torch.bfloat16, 2), n, d, _dev(out, "out", torch.float32, 1),
                                  _stream_ptr(stream)))
     return out

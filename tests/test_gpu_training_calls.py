@@ -8,6 +8,14 @@ import pytest
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def _streams_left_as_new(fs):
+    """PyTorch hands its streams out in turn: what these tests leave on them is
+    given back."""
+    yield
+    fs.check(fs.library().fs_workspace_release())
+
+
 def _in_a_thread(work):
     """What work() returns on a new host thread; its exception is raised here."""
     out = []
@@ -256,5 +264,26 @@ def test_results_on_a_given_stream(fs, torch_cuda, what):
     else:
         shapes = [((), f32)]
         call = lambda s=None: [fs.clip_grad_norm([logp], float("inf"), stream=s)]  # noqa: E731
+    want = call()
+    _on_another_stream(torch, shapes, call, want)
+
+
+@pytest.mark.parametrize("what", ["sample", "logits", "topk", "combine", "norms"])
+def test_samples_on_a_given_stream(fs, torch_cuda, what):
+    torch = torch_cuda
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    n, d, V = 40, 64, 700
+    h, W = (torch.randn(m, d, generator=gen, device="cuda").bfloat16() for m in (n, V))
+    temp = torch.ones(n, device="cuda")
+    ids, mx = fs.sample(h, W, temp, 1, 2)
+    ids, mx = torch.stack((ids, ids)), torch.stack((mx, mx - 1))
+    i64, f32 = torch.int64, torch.float32
+    shapes, call = {
+        "sample": ([((n,), i64), ((n,), f32)], lambda s=None: [*fs.sample(h, W, temp, 1, 2, stream=s)]),
+        "logits": ([((n,), i64), ((n,), f32), ((n, V), f32)],
+                   lambda s=None: [*fs.debug_fused_logits(h, W, temp, 1, 2, stream=s)]),
+        "topk": ([((n, 3), i64), ((n, 3), f32)], lambda s=None: [*fs.sample_topk(h, W, temp, 1, 2, 3, stream=s)]),
+        "combine": ([((n,), i64), ((n,), f32)], lambda s=None: [*fs.combine_shards(mx, ids, stream=s)]),
+        "norms": ([((V,), f32)], lambda s=None: [fs.row_norms(W, stream=s)])}[what]
     want = call()
     _on_another_stream(torch, shapes, call, want)

@@ -76,7 +76,9 @@ __global__ void __launch_bounds__(kThreads) head_merge_kernel(const HeadProblem 
   float lp = 0.0f;
   if (valid && id >= 0 && id < p.V) {
     const float x = own_x[t];
-    lp = x == -INFINITY ? -INFINITY : x - z;
+    // not x - z: z is rounded to its own size, which for a token that is nearly
+    // certain is all that x - z would hold (lse = 200: 8e-6); logf(s) is small
+    lp = x == -INFINITY ? -INFINITY : (x - part.m) - logf(part.s);
   }
   logp[t] = lp;
 }
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(256) head_ds_kept_kernel(const HeadProblem p, 
       if (id >= v && id < v + 8) {                       // the token's own entry is one of these
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (v + j == id) o[j] = head::own_ds_of(x[j], z, c, r.rest[t]);
+          if (v + j == id) o[j] = head::own_ds_of(r.logp[t], c, r.rest[t]);
       }
     }
     *reinterpret_cast<uint4*>(dst + v) = *reinterpret_cast<uint4*>(o);
@@ -344,6 +346,7 @@ cudaError_t launch_head_ds(const HeadProblem& p, const HeadRows& r, const float*
   }
   Args a{};
   a.p = p;
+  a.logp = r.logp;
   a.lse = r.lse;
   a.coef = r.coef;
   a.ds = out;

@@ -103,6 +103,7 @@ struct Args {
   float* kept;               // nullable [n, kept_pitch]
   int64_t kept_pitch;
   // kDs
+  const float* logp;
   const float* lse;
   const float* coef;
   __nv_bfloat16* ds;
@@ -203,12 +204,15 @@ __device__ __forceinline__ LsePart lse_join(LsePart a, LsePart b) {
   return LsePart{m, a.s * __expf(a.m - m) + b.s * __expf(b.m - m)};
 }
 
-// A token's own entry of ds, c (1 - p), is by far the largest of its row, so
-// its rounding to bf16 alone would make the gradients' error half again as
-// large as rounding the results does.  What the rounding leaves over is kept
-// and added in fp32: rest W[id] to grad_h, rest h to row id of grad_W.
-__device__ __forceinline__ __nv_bfloat16 own_ds_of(float x, float lse, float coef, float& rest) {
-  const float v = coef * (1.0f - __expf(x - lse));
+// A token's own entry of ds, c (1 - p), is the largest of its row, by far
+// where the rest is spread over many entries, and its rounding to bf16 alone
+// would then make the gradients' error half again as large as rounding the
+// results does.  What the rounding leaves over is kept and added in fp32: rest
+// W[id] to grad_h, rest h to row id of grad_W.  1 - p comes from logp: for a
+// token that is nearly certain, 1 - exp(x - lse) would consist of the
+// rounding of lse (at lse = 200 and p = 1 - 1e-4 it is off by 7%).
+__device__ __forceinline__ __nv_bfloat16 own_ds_of(float logp, float coef, float& rest) {
+  const float v = -coef * expm1f(logp);
   const __nv_bfloat16 r = __float2bfloat16_rn(v);
   rest = v - __bfloat162float(r);
   return r;
@@ -554,13 +558,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ 
             hits &= hits - 1;
             const int own = __shfl_sync(0xffffffffu, id[k], c & 31) - static_cast<int>(m_warp);
             float mine = 0.0f;
+            if constexpr (kKind == kLse) {
 #pragma unroll
-            for (int j = k * 32; j < k * 32 + 32; ++j) mine = j == c ? x[j] : mine;
+              for (int j = k * 32; j < k * 32 + 32; ++j) mine = j == c ? x[j] : mine;
+            }
             if (lane == own) {
               if constexpr (kKind == kLse) {
                 a.own_x[t_first + c] = mine;
               } else if (third[c] != 0.0f) {
-                a.ds[(t_first + c) * a.ds_pitch + m] = own_ds_of(mine, second[c], third[c], a.rest[t_first + c]);
+                a.ds[(t_first + c) * a.ds_pitch + m] =
+                    own_ds_of(a.logp[t_first + c], third[c], a.rest[t_first + c]);
               }
             }
           }

@@ -1,0 +1,103 @@
+"""The training operators where their values are extreme, against fp64.
+
+u = 2^-24 is the half step of fp32, 2^-8 that of bf16.  Logits are put in
+through the bias alone (h or W is zero), so they are exact, and what is left
+is the error of the operators themselves.
+"""
+
+import math
+
+import numpy as np
+import pytest
+
+from lm_head_exact_gb300 import synthetic
+from oracle import training as tr
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF_BF16 = 2.0 ** -8
+
+
+def _bf16(torch, x):
+    bits = synthetic.bf16_bits(np.asarray(x, np.float32))
+    return torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16), synthetic.bf16_bits_to_f32(bits)
+
+
+def _host(t):
+    return t.detach().double().cpu().numpy()
+
+
+class NearCertain:
+    """n rows whose own token has probability 1 - delta at logits around level;
+    the rest is spread over 1 to 40 other tokens."""
+
+    V = 1000
+
+    def __init__(self, n, seed=0):
+        rng = np.random.default_rng(seed)
+        self.bias = np.full((n, self.V), -np.inf, np.float32)
+        self.ids = np.arange(n) % 500
+        self.delta = np.array([1e-3, 1e-4, 1e-5])[np.arange(n) % 3]
+        for t in range(n):
+            level = np.float32([20.0, 200.0, -150.0, 3000.0][t // 3 % 4] + rng.random())
+            others = rng.choice(np.arange(500, self.V), rng.integers(1, 41), replace=False)
+            w = rng.uniform(0.5, 1.5, len(others))
+            self.bias[t, self.ids[t]] = level
+            self.bias[t, others] = level + np.log(w / w.sum() * self.delta[t])
+        self.temp = np.array([1.0, 0.5], np.float32)[rng.integers(0, 2, n)]
+        self.bias *= self.temp[:, None]                    # exact: powers of two
+        self.g = rng.uniform(0.5, 2.0, n).astype(np.float32) * rng.choice([-1, 1], n).astype(np.float32)
+
+    def device(self, torch):
+        return tuple(torch.from_numpy(a).cuda() for a in (self.ids, self.temp, self.bias, self.g))
+
+
+# 1 - p = sum of the others' exp over s.  An exponential is within 2^-22, its argument (at most 16, after
+# the scaling to base 2) within half a step twice: 2^-19 of the sum.  The largest term, 1, is in at most
+# 22 additions (5 within a warp's rows, 1 with the tile before, 16 in the merge), each off by u.
+REL, ABS = 2.0 ** -19, 24 * U
+
+
+@pytest.mark.parametrize("n", [12, 300])
+def test_scores_of_near_certain_tokens(fs, torch_cuda, n):
+    torch = torch_cuda
+    c = NearCertain(n)
+    ids, temp, bias, _ = c.device(torch)
+    h, W = torch.zeros(n, 8, device="cuda").bfloat16(), torch.ones(c.V, 8, device="cuda").bfloat16()
+    logp, lse = fs.token_logprobs(h, W, ids, temp, bias=bias)
+    s = tr.scores(np.zeros((n, 8)), np.ones((c.V, 8)), c.ids, c.temp, c.bias)
+    assert np.all(np.abs(s.logp + c.delta) < 0.01 * c.delta)
+    assert np.all(np.abs(_host(logp) - s.logp) <= REL * np.abs(s.logp) + ABS)
+    assert np.all(np.abs(_host(lse) - s.lse) <= 2 * U * np.abs(s.lse) + ABS)
+    assert np.all(_host(logp) <= 0)
+
+
+@pytest.mark.parametrize("kept", [True, False])
+@pytest.mark.parametrize("n", [12, 300])
+def test_gradients_of_near_certain_tokens(fs, torch_cuda, n, kept):
+    """Their own entries of ds to what (1 - p) is known to; the others to the
+    half step of bf16 in which the products take them."""
+    torch = torch_cuda
+    c = NearCertain(n, seed=1)
+    ids, temp, bias, g = c.device(torch)
+    rng = np.random.default_rng(2)
+    for zero in ("h", "W"):
+        h, h64 = _bf16(torch, np.zeros((n, 16)) if zero == "h" else rng.standard_normal((n, 16)))
+        W, W64 = _bf16(torch, np.zeros((c.V, 16)) if zero == "W" else rng.standard_normal((c.V, 16)))
+        keep = fs.logprob_buffer(n, c.V) if kept else None
+        logp, lse = fs.token_logprobs(h, W, ids, temp, bias=bias, kept=keep)
+        gh, gW = fs.token_logprobs_backward(h, W, ids, temp, logp, lse, g, bias=bias, kept=keep)
+        s = tr.scores(h64, W64, c.ids, c.temp, c.bias)
+        ds, live, want_h, want_W = tr.score_gradients(h64, W64, c.ids, s, c.g)
+        assert live.all()
+        coef = np.abs(c.g * s.inv_t)
+        rows = np.arange(n)
+        # the own entry: 1 - p as above, its remainder added in fp32
+        t_ds = np.abs(ds) * (HALF_BF16 + REL + 2 * U * np.abs(s.lse)[:, None])
+        t_ds[rows, c.ids] = np.abs(ds[rows, c.ids]) * (REL + 8 * U) + coef * ABS
+        for got, want, tol in ((gh, want_h, t_ds @ np.abs(W64) + 64 * U * (np.abs(ds) @ np.abs(W64))),
+                               (gW, want_W, t_ds.T @ np.abs(h64) + 64 * U * (np.abs(ds).T @ np.abs(h64)))):
+            tol = 1.01 * tol + HALF_BF16 * np.abs(want) + 1e-37
+            over = np.abs(_host(got) - want) / tol
+            assert over.max() <= 1, (zero, over.max(), np.unravel_index(over.argmax(), over.shape))

@@ -364,7 +364,7 @@ FS_API fs_status fs_sample_noalloc(const void* h, const void* W, int64_t B, int6
  * A row that is not scored gets logp 0 (its lse is still written; -inf where
  * the temperature is invalid).  A row whose every x is -inf has lse -inf; a
  * token at x = -inf has logp -inf.  A logit that is NaN or +inf gives NaN for
- * its row, and for no other.
+ * its row's lse and logp, whatever the token's own logit is, and for no other.
  *   kept (nullable): fp32 [fs_logprob_buffer_elems(n, V)] where the call
  *     leaves the logits for fs_token_logprobs_backward, 16-byte aligned.
  *     Without it the n x V logits never reach device memory.

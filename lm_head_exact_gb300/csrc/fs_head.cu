@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kThreads) head_merge_kernel(const HeadProblem 
     const float x = own_x[t];
     // not x - z: z is rounded to its own size, which for a token that is nearly
     // certain is all that x - z would hold (lse = 200: 8e-6); logf(s) is small
-    lp = x == -INFINITY ? -INFINITY : (x - part.m) - logf(part.s);
+    lp = z != z ? NAN : x == -INFINITY ? -INFINITY : (x - part.m) - logf(part.s);
   }
   logp[t] = lp;
 }

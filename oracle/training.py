@@ -39,7 +39,7 @@ def scores(h, W, ids, temp, bias=None):
             lse = np.where(np.isnan(x).any(1) | (x == np.inf).any(1), np.nan, lse)
         lse = np.where(valid, lse, -np.inf)
         own = x[np.arange(len(ids)), np.where(scored, ids, 0)] if V else np.zeros(len(ids))
-        logp = np.where(scored, np.where(own == -np.inf, -np.inf, own - lse), 0.0)
+        logp = np.where(scored, np.where((own == -np.inf) & ~np.isnan(lse), -np.inf, own - lse), 0.0)
     return Scores(x, lse, logp, scored, inv_t)
 
 

@@ -101,3 +101,28 @@ def test_gradients_of_near_certain_tokens(fs, torch_cuda, n, kept):
             tol = 1.01 * tol + HALF_BF16 * np.abs(want) + 1e-37
             over = np.abs(_host(got) - want) / tol
             assert over.max() <= 1, (zero, over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+@pytest.mark.parametrize("kept", [True, False])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("n", [3, 300])
+def test_a_masked_token_in_a_row_that_is_not_finite(fs, torch_cuda, n, bad, kept):
+    """logp is NaN like lse, not -inf, and the row's gradient is NaN, not
+    zero; the other rows' scores and grad_h are as without it."""
+    torch = torch_cuda
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    h, W = (torch.randn(m, 64, generator=gen, device="cuda").bfloat16() for m in (n, 500))
+    ids, temp, g = torch.arange(n, device="cuda"), torch.ones(n, device="cuda"), torch.ones(n, device="cuda")
+    results = []
+    for x in (0.0, bad):
+        bias = torch.zeros(n, 500, device="cuda")
+        bias[1, 1] = -math.inf if x else 0.0               # the token of row 1
+        bias[1, 400] = x
+        keep = fs.logprob_buffer(n, 500) if kept else None
+        logp, lse = fs.token_logprobs(h, W, ids, temp, bias=bias, kept=keep)
+        gh, _ = fs.token_logprobs_backward(h, W, ids, temp, logp, lse, g, bias=bias, kept=keep)
+        results.append((logp, lse, gh))
+    rest = torch.arange(n, device="cuda") != 1
+    for clean, got in zip(*results):
+        assert bool(got[1].isnan().all())
+        assert torch.equal(clean[rest], got[rest])

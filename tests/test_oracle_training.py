@@ -99,3 +99,18 @@ def test_norm_and_factor():
     assert tr.grad_norm(a) == 5.0 and tr.grad_norm(a, float("inf")) == 4.0 and tr.grad_norm([]) == 0.0
     assert tr.clip_factor(5.0, 10.0) == 1.0 and abs(tr.clip_factor(5.0, 1.0) - 0.2) < 1e-6
     assert tr.clip_factor(np.inf, 1.0) == 1.0 and tr.clip_factor(5.0, 0.0) == 0.0
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_scores_of_a_masked_token_in_a_row_that_is_not_finite(bad):
+    """A row without a log-sum has no log-probability of any token, of one at
+    -inf neither, and such a row's gradient does not vanish unseen."""
+    h, W, ids, temp = _head()
+    bias = np.zeros((5, 11))
+    bias[2, ids[2]] = -np.inf
+    bias[2, (ids[2] + 1) % 11] = bad
+    with np.errstate(all="ignore"):
+        s = tr.scores(h, W, ids, temp, bias)
+        ds, live, _, _ = tr.score_gradients(h, W, ids, s, np.ones(5))
+    assert np.isnan(s.lse[2]) and np.isnan(s.logp[2]) and live[2] and np.isnan(ds[2]).all()
+    assert np.isfinite(s.logp[[0, 1, 3, 4]]).all()

@@ -9,12 +9,13 @@ logits in a framework's graph:
 2. the present policy scores them again, keeping its logits;
 3. ``policy_loss`` gives the clipped loss with its KL term and dloss/dlogp;
 4. ``token_logprobs_backward`` turns that into gradients of the hidden states
-   and of the LM head;
-5. ``clip_grad_norm`` scales them by their global norm.
+   and of the LM head.
 
 grad_h goes on into the model's own backward pass
-(``hidden.backward(grad_h)`` in PyTorch); here, where the body is a fixed set
-of hidden states, only the head is updated.
+(``hidden.backward(grad_h)`` in PyTorch), and ``clip_grad_norm`` follows it,
+over the gradients of all parameters: grad_W and the body's, not grad_h, which
+is the gradient of activations.  Here, where the body is a fixed set of hidden
+states, the head is all there is to update and to clip.
 
 Usage: ``python -m lm_head_exact_gb300.policy_step [steps]`` on a GPU.
 """
@@ -50,17 +51,23 @@ def roll_out(h, W, temp, seq_starts, reward, seed, step):
 @dataclass
 class StepResult:
     stats: object           # fp32 [4]: loss, policy term, KL term, share of clipped tokens
-    grad_norm: object       # fp32 scalar, before clipping
+    grad_norm: object       # fp32 scalar, the norm that max_norm bounds (before scaling); None without max_norm
     grad_h: object          # bf16 [N, d]
     grad_W: object          # bf16 [V, d]
     logp: object            # fp32 [N]
 
 
-def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef=0.0, mean="token", max_norm=1.0,
+def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef=0.0, mean="token", max_norm=None,
                 keep_logits=True):
-    """Loss and clipped gradients of one step on ``rollout`` under the head W.
+    """Loss and gradients of one step on ``rollout`` under the head W.
     ``keep_logits`` spends 4 bytes per token and vocabulary row to form the
-    logits once instead of twice."""
+    logits once instead of twice.
+
+    The gradients are not clipped here: the norm of the model's gradient is
+    known after the body's backward pass only (clip_grad_norm over all
+    parameters' gradients).  ``max_norm`` is for something else: it bounds the
+    norm of grad_h and grad_W taken as one vector, that is of the step's whole
+    signal into head and body, and scales both by one factor."""
     r = rollout
     n, V = r.h.shape[0], W.shape[0]
     kept = fs.logprob_buffer(n, V, device=r.h.device) if keep_logits else None
@@ -69,7 +76,7 @@ def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef
                                       ref_logp=ref_logp, clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef,
                                       mean=mean, adv_per_seq=True)
     grad_h, grad_W = fs.token_logprobs_backward(r.h, W, r.ids, r.temp, logp, lse, grad_logp, kept=kept)
-    norm = fs.clip_grad_norm([grad_h, grad_W], max_norm)
+    norm = None if max_norm is None else fs.clip_grad_norm([grad_h, grad_W], max_norm)
     return StepResult(stats, norm, grad_h, grad_W, logp)
 
 
@@ -95,6 +102,7 @@ def train_toy(steps=20, V=48, d=64, sequences=256, length=4, lr=6.0, seed=1234, 
         ref_logp, _ = fs.token_logprobs(h, first, r.ids, temp)
         for _ in range(2):                                   # two steps on the same tokens: the second may clip
             out = policy_step(r, master.bfloat16(), ref_logp=ref_logp, kl_coef=0.01)
+            fs.clip_grad_norm([out.grad_W], 1.0)
             master -= lr * out.grad_W.float()
     return torch.stack(rewards).tolist()
 

@@ -40,11 +40,13 @@ class Rollout:
 def roll_out(h, W, temp, seq_starts, reward, seed, step):
     """Sample a token for every hidden state and score it under W; ``reward``
     maps the ids to one value per sequence, which become advantages by
-    subtracting their mean and dividing by their spread."""
+    subtracting their mean and dividing by their spread (one sequence alone
+    has neither: advantage 0)."""
     ids, _ = fs.sample(h, W, temp, seed, step)
     old_logp, _ = fs.token_logprobs(h, W, ids, temp)
     r = reward(ids)
-    advantages = ((r - r.mean()) / (r.std() + 1e-6)).contiguous()
+    spread = r.std() if r.numel() > 1 else 0.0
+    advantages = ((r - r.mean()) / (spread + 1e-6)).contiguous()
     return Rollout(h, ids, temp, seq_starts, advantages, old_logp)
 
 

@@ -95,3 +95,9 @@ def test_the_toy_clips_the_head_alone(world, monkeypatch):
     ps.train_toy(steps=1, V=12, d=16, sequences=4, length=2, device="cpu")
     assert len(made) == 2
     assert [c[1] for c in plain.calls if c[0] == "clip_grad_norm"] == [[m.grad_W.data_ptr()] for m in made]
+
+
+def test_one_sequence_alone_has_no_advantage(world):
+    plain, h, W, temp, _, _ = world
+    r = ps.roll_out(h, W, temp, torch.tensor([0, 12]), lambda ids: ids.float().mean()[None], 1, 2)
+    assert torch.equal(r.advantages, torch.zeros(1))

@@ -35,19 +35,21 @@ class Rollout:
     advantages: object      # fp32 [S]
     old_logp: object        # fp32 [N] under the policy that drew them
     mask: object = None     # bool [N], False: not trained on
+    bias: object = None     # fp32 [N, V] or [V], the sampler's, under which the tokens are scored too
 
 
-def roll_out(h, W, temp, seq_starts, reward, seed, step):
-    """Sample a token for every hidden state and score it under W; ``reward``
+def roll_out(h, W, temp, seq_starts, reward, seed, step, bias=None):
+    """Sample a token for every hidden state and score it under W (and the
+    sampler's ``bias``, for instance -inf at forbidden tokens); ``reward``
     maps the ids to one value per sequence, which become advantages by
     subtracting their mean and dividing by their spread (one sequence alone
     has neither: advantage 0)."""
-    ids, _ = fs.sample(h, W, temp, seed, step)
-    old_logp, _ = fs.token_logprobs(h, W, ids, temp)
+    ids, _ = fs.sample(h, W, temp, seed, step, bias=bias)
+    old_logp, _ = fs.token_logprobs(h, W, ids, temp, bias=bias)
     r = reward(ids)
     spread = r.std() if r.numel() > 1 else 0.0
     advantages = ((r - r.mean()) / (spread + 1e-6)).contiguous()
-    return Rollout(h, ids, temp, seq_starts, advantages, old_logp)
+    return Rollout(h, ids, temp, seq_starts, advantages, old_logp, bias=bias)
 
 
 @dataclass
@@ -73,11 +75,11 @@ def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef
     r = rollout
     n, V = r.h.shape[0], W.shape[0]
     kept = fs.logprob_buffer(n, V, device=r.h.device) if keep_logits else None
-    logp, lse = fs.token_logprobs(r.h, W, r.ids, r.temp, kept=kept)
+    logp, lse = fs.token_logprobs(r.h, W, r.ids, r.temp, bias=r.bias, kept=kept)
     stats, grad_logp = fs.policy_loss(logp, r.old_logp, r.advantages, seq_starts=r.seq_starts, mask=r.mask,
                                       ref_logp=ref_logp, clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef,
                                       mean=mean, adv_per_seq=True)
-    grad_h, grad_W = fs.token_logprobs_backward(r.h, W, r.ids, r.temp, logp, lse, grad_logp, kept=kept)
+    grad_h, grad_W = fs.token_logprobs_backward(r.h, W, r.ids, r.temp, logp, lse, grad_logp, bias=r.bias, kept=kept)
     norm = None if max_norm is None else fs.clip_grad_norm([grad_h, grad_W], max_norm)
     return StepResult(stats, norm, grad_h, grad_W, logp)
 

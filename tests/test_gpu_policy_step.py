@@ -49,3 +49,22 @@ def test_a_head_learns(fs, torch_cuda):
     rewards = ps.train_toy(steps=20)
     assert np.isfinite(rewards).all()
     assert np.mean(rewards[-3:]) > np.mean(rewards[:2]) + 0.1
+
+
+def test_policy_step_under_the_samplers_bias(fs, torch_cuda):
+    """An unchanged policy has ratio 1 everywhere: the loss is minus the mean
+    advantage, and forbidden tokens have no gradient."""
+    torch = torch_cuda
+    from lm_head_exact_gb300 import policy_step as ps
+    g = torch.Generator(device="cuda").manual_seed(6)
+    h = torch.randn(64, 128, generator=g, device="cuda").bfloat16()
+    W = torch.randn(900, 128, generator=g, device="cuda").bfloat16()
+    bias = torch.where(torch.arange(900, device="cuda") % 3 == 0, -float("inf"), 0.0)
+    starts = torch.arange(0, 65, 8, device="cuda")
+    r = ps.roll_out(h, W, torch.ones(64, device="cuda"), starts, lambda ids: (ids.view(8, 8) % 5).float().mean(1), 7, 8,
+                    bias=bias)
+    assert bool((r.ids % 3 != 0).all())
+    out = ps.policy_step(r, W)
+    assert torch.equal(out.logp, r.old_logp) or float((out.logp - r.old_logp).abs().max()) < 1e-5
+    assert abs(float(out.stats[0]) + float(r.advantages.mean())) < 1e-4
+    assert not bool(out.grad_W[::3].any()) and bool(out.grad_W[1::3].any())

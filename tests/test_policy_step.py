@@ -101,3 +101,19 @@ def test_one_sequence_alone_has_no_advantage(world):
     plain, h, W, temp, _, _ = world
     r = ps.roll_out(h, W, temp, torch.tensor([0, 12]), lambda ids: ids.float().mean()[None], 1, 2)
     assert torch.equal(r.advantages, torch.zeros(1))
+
+
+def test_the_samplers_bias_reaches_every_score(world):
+    """Tokens drawn under a bias are scored, and differentiated, under it: the
+    ratio of an unchanged policy is 1."""
+    plain, h, W, temp, starts, reward = world
+    bias = torch.where(torch.arange(30) % 4 == 0, -float("inf"), 0.0)
+    plain.sampled = plain.sampled // 4 * 4 + 1
+    plain.sampled.clamp_(max=29)
+    r = ps.roll_out(h, W, temp, starts, reward, 1, 2, bias=bias)
+    out = ps.policy_step(r, W)
+    torch.testing.assert_close(out.logp, r.old_logp)
+    torch.testing.assert_close(r.old_logp, plain.token_logprobs(h, W, r.ids, temp, bias)[0])
+    assert not out.grad_W[::4].any()                       # forbidden tokens learn nothing
+    names = [name for name, b in plain.calls if b is bias]
+    assert names.count("sample") == 1 and names.count("token_logprobs") == 3 and "token_logprobs_backward" in names

@@ -65,7 +65,8 @@ def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef
                 keep_logits=True):
     """Loss and gradients of one step on ``rollout`` under the head W.
     ``keep_logits`` spends 4 bytes per token and vocabulary row to form the
-    logits once instead of twice.
+    logits once instead of twice.  Rows without a token (the sampler's -1, an
+    invalid temperature) take no part, whatever the rollout's mask says.
 
     The gradients are not clipped here: the norm of the model's gradient is
     known after the body's backward pass only (clip_grad_norm over all
@@ -76,7 +77,10 @@ def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef
     n, V = r.h.shape[0], W.shape[0]
     kept = fs.logprob_buffer(n, V, device=r.h.device) if keep_logits else None
     logp, lse = fs.token_logprobs(r.h, W, r.ids, r.temp, bias=r.bias, kept=kept)
-    stats, grad_logp = fs.policy_loss(logp, r.old_logp, r.advantages, seq_starts=r.seq_starts, mask=r.mask,
+    # (unscored rows have logp 0 on both sides: a ratio of 1, and a part in the means)
+    scored = (r.ids >= 0) & (r.ids < V) & (r.temp >= 0)
+    mask = scored if r.mask is None else r.mask & scored
+    stats, grad_logp = fs.policy_loss(logp, r.old_logp, r.advantages, seq_starts=r.seq_starts, mask=mask,
                                       ref_logp=ref_logp, clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef,
                                       mean=mean, adv_per_seq=True)
     grad_h, grad_W = fs.token_logprobs_backward(r.h, W, r.ids, r.temp, logp, lse, grad_logp, bias=r.bias, kept=kept)

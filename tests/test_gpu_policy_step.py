@@ -68,3 +68,25 @@ def test_policy_step_under_the_samplers_bias(fs, torch_cuda):
     assert torch.equal(out.logp, r.old_logp) or float((out.logp - r.old_logp).abs().max()) < 1e-5
     assert abs(float(out.stats[0]) + float(r.advantages.mean())) < 1e-4
     assert not bool(out.grad_W[::3].any()) and bool(out.grad_W[1::3].any())
+
+
+def test_policy_step_with_rows_that_have_no_token(fs, torch_cuda):
+    """Rows that the sampler left out: the step is that of the other rows."""
+    torch = torch_cuda
+    from lm_head_exact_gb300 import policy_step as ps
+    g = torch.Generator(device="cuda").manual_seed(9)
+    h = torch.randn(40, 64, generator=g, device="cuda").bfloat16()
+    W = torch.randn(300, 64, generator=g, device="cuda").bfloat16()
+    temp = torch.ones(40, device="cuda")
+    temp[5:9] = -1.0
+    starts = torch.tensor([0, 10, 40], device="cuda")
+    r = ps.roll_out(h, W, temp, starts, lambda ids: torch.stack([ids[:10].float().mean(), ids[10:].float().mean()]), 1, 2)
+    assert bool((r.ids[5:9] == -1).all())
+    out = ps.policy_step(r, W)
+    live = torch.cat([torch.arange(5), torch.arange(9, 40)]).cuda()
+    alone = ps.policy_step(ps.Rollout(h[live], r.ids[live], temp[live], torch.tensor([0, 6, 36], device="cuda"),
+                                      r.advantages, r.old_logp[live]), W)
+    # the same 36 tokens, added in another order
+    assert torch.allclose(out.stats, alone.stats, rtol=1e-5, atol=1e-6)
+    assert torch.allclose(out.grad_h[live].float(), alone.grad_h.float(), rtol=2.0 ** -7, atol=1e-4)
+    assert not bool(out.grad_h[5:9].any())

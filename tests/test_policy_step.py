@@ -117,3 +117,22 @@ def test_the_samplers_bias_reaches_every_score(world):
     assert not out.grad_W[::4].any()                       # forbidden tokens learn nothing
     names = [name for name, b in plain.calls if b is bias]
     assert names.count("sample") == 1 and names.count("token_logprobs") == 3 and "token_logprobs_backward" in names
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_rows_without_a_token_take_no_part(world, masked):
+    """Neither the loss nor its means see the sampler's -1 or rows whose
+    temperature is invalid."""
+    plain, h, W, temp, starts, reward = world
+    temp = temp.clone()
+    plain.sampled[3] = -1
+    temp[7] = -1.0
+    temp[8] = float("nan")
+    r = ps.roll_out(h, W, temp, starts, reward, 1, 2)
+    if masked:
+        r.mask = torch.arange(12) != 5
+    out = ps.policy_step(r, W)
+    took = [m for name, m in plain.calls if name == "policy_loss"][0]
+    assert [i for i in range(12) if not took[i]] == ([3, 5, 7, 8] if masked else [3, 7, 8])
+    A = r.advantages.repeat_interleave(starts.diff())
+    assert torch.allclose(out.stats[0], -A[took].mean(), atol=1e-6)

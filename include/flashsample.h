@@ -457,10 +457,11 @@ FS_API size_t fs_policy_loss_workspace_bytes(int64_t n_seqs);
  *   max_norm >= 0; +inf never scales.  norm (device fp32 [1]): the norm
  *     before scaling.
  * The scaled values are formed in fp32 and rounded once.  A norm that is not
- * finite (a NaN or an infinity among the gradients, or a square above the
- * fp32 range) is reported and scales nothing.  Squares are summed in fp32
- * over some 64 elements, then in fp64, in an order that does not depend on the
- * run.
+ * finite (a NaN or an infinity among the gradients) is reported and scales
+ * nothing; finite gradients are always scaled, also where their norm passes
+ * fp32's range and is reported as +inf.  Squares are summed in fp32 over some
+ * 64 elements (scaled where they leave fp32's range; magnitudes below 2^-75
+ * may count as zero), then in fp64, in an order that does not depend on the run.
  */
 FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes,
                                    const int* types, int n_tensors, double max_norm, int norm_type, float* norm,

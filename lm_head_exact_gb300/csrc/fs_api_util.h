@@ -19,8 +19,8 @@ struct alignas(256) TrainScratch {
   unsigned int ticket;
   unsigned int pad;
   unsigned long long count;             // tokens (or sequences) that take part
-  float coef;                           // clip_grad_norm: the factor of the scaling launch
-  float pad2[3];
+  float coef, first_coef;               // clip_grad_norm: the scaling launch multiplies by both
+  float pad2[2];
   double sums[kTrainMaxBlocks][4];      // one row per block
   alignas(256) unsigned char small[FS_SMALL_WORKSPACE];   // workspace of calls that bring none
 };

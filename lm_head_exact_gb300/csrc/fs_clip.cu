@@ -42,7 +42,6 @@ struct NormArgs {
   TrainScratch* scratch;
   float* norm;
   double max_norm;
-  int norm_type;
   bool first, last;                      // of the launches that share one norm
 };
 
@@ -147,9 +146,35 @@ __device__ double block_join(double v) {
   return v;                              // valid in thread 0
 }
 
+// Squares pass fp32's range for values above 1.8e19 and lose their last bits
+// below 2^-126: a block whose sum shows either goes over its chunks once more,
+// with the values scaled by a power of two (an infinity among them stays one).
+// Rare, so in as little code as it takes: what this adds to the kernel's
+// registers would slow the loop that every call runs.
+template <int kEntries>
+__device__ __forceinline__ double squares_scaled(const Table<kEntries>& t, float scale) {
+  double total = 0.0;
+  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const Entry& e = entry_of(t, c);
+    const int64_t at = static_cast<int64_t>(c - e.first_chunk) * kChunk;
+    const int64_t end = min(at + kChunk, e.n);
+    float acc = 0.0f;
+#pragma unroll 1
+    for (int64_t i = at + threadIdx.x; i < end; i += kThreads) {
+      const float v = e.type == FS_TYPE_F32    ? static_cast<const float*>(e.g)[i]
+                      : e.type == FS_TYPE_BF16 ? to_float(static_cast<const __nv_bfloat16*>(e.g)[i])
+                                               : to_float(static_cast<const __half*>(e.g)[i]);
+      accumulate<false>(acc, v * scale);
+    }
+    total += static_cast<double>(acc);
+  }
+  return total;
+}
+
 template <int kEntries, bool kMax>
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<kEntries> t, const NormArgs a) {
   __shared__ bool last;
+  __shared__ float rescale;
   pdl_launch_dependents();
   double total = 0.0;
   for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
@@ -166,6 +191,12 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     total = join<kMax>(total, static_cast<double>(v));
   }
   total = block_join<kMax>(total);
+  if constexpr (!kMax) {
+    if (threadIdx.x == 0) rescale = total == INFINITY ? 0x1p-100f : total > 0.0 && total < 0x1p-90 ? 0x1p100f : 0.0f;
+    __syncthreads();
+    if (rescale != 0.0f)
+      total = block_join<false>(squares_scaled(t, rescale)) * (rescale < 1.0f ? 0x1p200 : 0x1p-200);
+  }
   if (threadIdx.x == 0) {
     double* mine = &a.scratch->sums[blockIdx.x][0];
     *mine = a.first ? total : join<kMax>(*mine, total);
@@ -182,8 +213,11 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     const double norm = kMax ? v : sqrt(v);
     const double coef = a.max_norm / (norm + 1e-6);
     *a.norm = static_cast<float>(norm);
-    // a norm that is not finite scales nothing
-    a.scratch->coef = isfinite(norm) && coef < 1.0 ? static_cast<float>(coef) : 1.0f;
+    // a norm that is not finite scales nothing; one that fp32 cannot hold is
+    // finite here, and a factor below fp32's normal range is applied in two steps
+    const bool scales = isfinite(norm) && coef < 1.0, small = scales && coef < 0x1p-126;
+    a.scratch->first_coef = small ? 0x1p-64f : 1.0f;
+    a.scratch->coef = scales ? static_cast<float>(small ? coef * 0x1p64 : coef) : 1.0f;
     a.scratch->ticket = 0;
   }
 }
@@ -223,22 +257,39 @@ __device__ __forceinline__ void chunk_scale(const T* g, T* o, int len, float coe
   }
 }
 
+// The same by two factors, where their product is below fp32's normal range.
+template <typename T>
+__device__ __noinline__ void chunk_scale_twice(const T* g, T* o, int len, float first, float coef) {
+  for (int i = threadIdx.x; i < len; i += kThreads) o[i] = from_float<T>(to_float(g[i]) * first * coef);
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale_by(const Entry& e, int64_t at, int len, float first, float coef) {
+  const T* g = static_cast<const T*>(e.g) + at;
+  T* o = static_cast<T*>(e.o) + at;
+  if (first == 1.0f)
+    chunk_scale(g, o, len, coef);
+  else
+    chunk_scale_twice(g, o, len, first, coef);
+}
+
 template <int kEntries>
 __global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<kEntries> t,
                                                          const TrainScratch* scratch) {
   pdl_wait();
   const float coef = *reinterpret_cast<const volatile float*>(&scratch->coef);
+  const float first = *reinterpret_cast<const volatile float*>(&scratch->first_coef);
   for (int c = t.chunks - 1 - static_cast<int>(blockIdx.x); c >= 0; c -= gridDim.x) {
     const Entry& e = entry_of(t, c);
     if (coef == 1.0f && e.o == e.g) continue;          // in place and unchanged
     const int64_t at = static_cast<int64_t>(c - e.first_chunk) * kChunk;
     const int len = static_cast<int>(min(static_cast<int64_t>(kChunk), e.n - at));
     if (e.type == FS_TYPE_F32)
-      chunk_scale(static_cast<const float*>(e.g) + at, static_cast<float*>(e.o) + at, len, coef);
+      chunk_scale_by<float>(e, at, len, first, coef);
     else if (e.type == FS_TYPE_BF16)
-      chunk_scale(static_cast<const __nv_bfloat16*>(e.g) + at, static_cast<__nv_bfloat16*>(e.o) + at, len, coef);
+      chunk_scale_by<__nv_bfloat16>(e, at, len, first, coef);
     else
-      chunk_scale(static_cast<const __half*>(e.g) + at, static_cast<__half*>(e.o) + at, len, coef);
+      chunk_scale_by<__half>(e, at, len, first, coef);
   }
 }
 
@@ -274,7 +325,7 @@ cudaError_t run(const void* const* grads, void* const* outs, const int64_t* size
     const bool last = from == n_tensors;
     single = first && last;
     const int grid = single ? std::max(1, std::min(t.chunks, full_grid)) : full_grid;
-    const NormArgs a{scratch, norm, max_norm, 0, first, last};
+    const NormArgs a{scratch, norm, max_norm, first, last};
     const cudaError_t e =
         launch_kernel(use_max ? norm_kernel<kEntries, true> : norm_kernel<kEntries, false>, dim3(grid),
                       dim3(kThreads), 0, stream, false, t, a);

@@ -126,3 +126,55 @@ def test_a_masked_token_in_a_row_that_is_not_finite(fs, torch_cuda, n, bad, kept
     for clean, got in zip(*results):
         assert bool(got[1].isnan().all())
         assert torch.equal(clean[rest], got[rest])
+
+
+def _clip_case(torch, name):
+    """Gradients by name: finite, but beyond where fp32 holds their squares."""
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal(40000)
+    return {
+        "large": [torch.tensor(x * 1e25).float(), torch.tensor(x[:77] * 1e20).bfloat16()],
+        "one_large": [torch.tensor(np.where(np.arange(40000) == 20001, 1e30, x)).float()],
+        "norm_past_fp32": [torch.full((20000,), 3e38), torch.full((501,), -3e38).bfloat16()],
+        "small": [torch.tensor(x * 1e-21).float(), torch.tensor(x[:300] * 1e-22).bfloat16()],
+        "small_and_zero": [torch.zeros(50000), torch.tensor(x[:20000] * 1e-20).float()],
+        "odd": [torch.tensor(x[:16391] * 1e22).float()],
+    }[name]
+
+
+@pytest.mark.parametrize("name", ["large", "one_large", "norm_past_fp32", "small", "small_and_zero", "odd"])
+def test_clip_grad_norm_of_finite_extremes(fs, torch_cuda, name):
+    """Finite gradients have the norm that fp64 gives them and are scaled by
+    it, in place and not."""
+    torch = torch_cuda
+    grads = [g.cuda() for g in _clip_case(torch, name)]
+    host = [_host(g) for g in grads]
+    want = tr.grad_norm(host)
+    t_norm = 40 * U                          # squares of 64 in fp32, 64 half steps of their sum, halved by the root
+    for max_norm in (1.0, 0.25 * want):
+        outs = [torch.empty_like(g) for g in grads]
+        norm = float(fs.clip_grad_norm(grads, max_norm, out=outs))
+        if want < 3.4e38:
+            assert abs(norm - want) <= t_norm * want
+        else:
+            assert norm == math.inf
+        f = tr.clip_factor(want, max_norm)
+        for g, o, x in zip(grads, outs, host):
+            half = {torch.float32: U, torch.bfloat16: HALF_BF16}[g.dtype]
+            # (2^-149: a step of fp32 below its normal range; the first of two factors may leave one, times the other)
+            assert np.all(np.abs(_host(o) - x * f) <= np.abs(x * f) * (half * 1.01 + t_norm + 4 * U) + 2.0 ** -149)
+        same = [g.clone() for g in grads]
+        fs.clip_grad_norm(same, max_norm)
+        for a, b in zip(same, outs):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_clip_grad_norm_of_an_infinity_among_large_values(fs, torch_cuda, bad):
+    torch = torch_cuda
+    g = torch.full((40000,), 1e30, device="cuda")
+    g[333] = bad
+    old = g.clone()
+    norm = float(fs.clip_grad_norm([g], 1.0))
+    assert math.isnan(norm) if math.isnan(bad) else norm == math.inf
+    assert torch.equal(g.view(torch.int32), old.view(torch.int32))

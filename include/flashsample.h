@@ -467,14 +467,17 @@ FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, 
                                    const int* types, int n_tensors, double max_norm, int norm_type, float* norm,
                                    void* stream);
 
-/* Workspace bytes one call with (B, V) needs on the current device. */
+/* Workspace bytes one sampling call with (B, V) needs on the current device
+ * (the training calls' fixed block is not among them). */
 FS_API size_t fs_workspace_bytes(int64_t B, int64_t V);
 
 /*
  * Grow the workspace of (current device, stream) to serve calls up to
- * (B, V) without allocating, and create the device error word; required
- * before capturing fs_sample / fs_sample_ex / fs_sample_chunked calls in a
- * CUDA graph on that stream (the seed and step are then fixed in the graph).
+ * (B, V) without allocating, and create the device error word and the
+ * training calls' block (0.6 MB); required before capturing fs_sample /
+ * fs_sample_ex / fs_sample_chunked or training calls in a CUDA graph on that
+ * stream (the seed and step are then fixed in the graph).  Called within a
+ * capture it succeeds where the sampling workspace is large enough already.
  */
 FS_API fs_status fs_workspace_reserve(int64_t B, int64_t V, void* stream);
 

@@ -1007,8 +1007,12 @@ fs_status fs_workspace_reserve(int64_t B, int64_t V, void* stream) {
   const CallLock lock(static_cast<cudaStream_t>(stream));
   int* err = nullptr;
   FS_TRY(error_word(&err, static_cast<cudaStream_t>(stream)));   // once per device, never during capture
-  TrainScratch* scratch = nullptr;
-  FS_TRY(api_train_scratch(static_cast<cudaStream_t>(stream), &scratch));
+  // Within a capture nothing can be allocated, and sampling needs no more than
+  // the finish area; a training call that misses its block there says so.
+  if (!capturing(static_cast<cudaStream_t>(stream))) {
+    TrainScratch* scratch = nullptr;
+    FS_TRY(api_train_scratch(static_cast<cudaStream_t>(stream), &scratch));
+  }
   Finish f{};
   return get_finish(static_cast<cudaStream_t>(stream), B, &f);
 }

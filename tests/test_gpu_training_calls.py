@@ -287,3 +287,27 @@ def test_samples_on_a_given_stream(fs, torch_cuda, what):
         "norms": ([((V,), f32)], lambda s=None: [fs.row_norms(W, stream=s)])}[what]
     want = call()
     _on_another_stream(torch, shapes, call, want)
+
+
+def test_reserve_within_a_capture(fs, torch_cuda):
+    """On a stream that has sampled before there is nothing left to grow for
+    sampling: reserving within a capture succeeds, and the graph samples."""
+    torch = torch_cuda
+    h, W = torch.ones(8, 64, device="cuda").bfloat16(), torch.ones(300, 64, device="cuda").bfloat16()
+    temp = torch.ones(8, device="cuda")
+    torch.cuda.synchronize()
+    fs.check(fs.library().fs_workspace_release())
+    stream = torch.cuda.Stream()
+    want = fs.sample(h, W, temp, 1, 2, stream=stream)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        fs.workspace_reserve(8, 300)
+        got = fs.sample(h, W, temp, 1, 2)
+        with pytest.raises(fs.FlashSampleError) as e:      # the block of the training calls is not there
+            fs.clip_grad_norm([temp], 1.0)
+        assert e.value.status == "FS_ERR_WORKSPACE"
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)

@@ -483,14 +483,15 @@ def _head_args(h, W, ids, temp, bias):
             _arg(ids, "ids", torch.int64, (n,)), _arg(temp, "temp", torch.float32, (n,)), bptr, bstride)
 
 
-# bytes of workspace by sizes alone
+# Bytes of workspace by sizes and the current device: the library lays it out
+# for the pairs of SMs that the device holds at a time.
 @lru_cache(maxsize=256)
-def _forward_bytes(n, d, V):
+def _forward_bytes(n, d, V, device):
     return library().fs_token_logprobs_workspace_bytes(n, d, V)
 
 
 @lru_cache(maxsize=256)
-def _backward_bytes(n, d, V):
+def _backward_bytes(n, d, V, device):
     return library().fs_token_logprobs_backward_workspace_bytes(n, d, V)
 
 
@@ -547,7 +548,7 @@ def token_logprobs(h, W, ids, temp, bias=None, kept=None, out=None, stream=None)
     if out is None:
         out = _made_on(stream, temp.device, lambda: (torch.empty_like(temp), torch.empty_like(temp)))
     logp, lse = out
-    nbytes = _forward_bytes(n, d, V)
+    nbytes = _forward_bytes(n, d, V, torch.cuda.current_device())
     work, where = _workspace(nbytes, h.device, stream)
     check(library().fs_token_logprobs(
         *args, _arg(logp, "logp", torch.float32, (n,)), _arg(lse, "lse", torch.float32, (n,)), _kept_arg(kept, n, V),
@@ -570,7 +571,7 @@ def token_logprobs_backward(h, W, ids, temp, logp, lse, grad_logp, bias=None, ke
         grad_h, = _made_on(stream, h.device, lambda: (torch.empty_like(h),))
     if need_W and grad_W is None:
         grad_W, = _made_on(stream, h.device, lambda: (torch.empty_like(W),))
-    nbytes = _backward_bytes(n, d, V)
+    nbytes = _backward_bytes(n, d, V, torch.cuda.current_device())
     work, where = _workspace(nbytes, h.device, stream)
     check(library().fs_token_logprobs_backward(
         *args, _arg(logp, "logp", torch.float32, (n,)), _arg(lse, "lse", torch.float32, (n,)),

@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kCountThreads) policy_count_kernel(const Polic
                               ? hi - lo
                               : block_sum<kCountThreads>(count_range(p.mask, lo, hi, threadIdx.x, kCountThreads));
       if (threadIdx.x == 0) {
-        p.counts[s] = static_cast<int>(min(c, static_cast<long long>(0x7fffffff)));
+        p.counts[s] = static_cast<float>(c);              // (a sequence may pass 2^31 tokens)
         if (c > 0) atomicAdd(&p.scratch->count, 1ull);
       }
     }
@@ -186,7 +186,7 @@ __device__ __forceinline__ void tokens(const PolicyProblem& p, const Weights& w,
   float seq_adv = 0.0f, weight = w.token;
   auto enter = [&]() {
     if (p.adv_per_seq) seq_adv = p.adv[s];
-    if (p.mean == FS_MEAN_SEQUENCE) weight = 1.0f / (static_cast<float>(p.counts[s]) * w.seqs);
+    if (p.mean == FS_MEAN_SEQUENCE) weight = 1.0f / (p.counts[s] * w.seqs);
   };
   if (kBySeq) enter();
   float policy = 0.0f, kl = 0.0f, clipped = 0.0f, g[kVec];

@@ -80,7 +80,7 @@ struct PolicyProblem {
   int mean;
   float* stats;
   float* grad;
-  int* counts;                  // [n_seqs] workspace
+  float* counts;                // [n_seqs] workspace: tokens that take part, as the weights take them
   TrainScratch* scratch;
 };
 cudaError_t launch_policy_loss(const PolicyProblem& p, cudaStream_t stream);

@@ -230,7 +230,7 @@ fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, in
 }
 
 size_t fs_policy_loss_workspace_bytes(int64_t n_seqs) {
-  return n_seqs <= 0 ? 0 : aligned(static_cast<size_t>(n_seqs) * sizeof(int));
+  return n_seqs <= 0 ? 0 : aligned(static_cast<size_t>(n_seqs) * sizeof(float));
 }
 
 fs_status fs_policy_loss(const float* logp, const float* old_logp, const float* ref_logp, const float* advantages,
@@ -278,7 +278,7 @@ fs_status fs_policy_loss(const float* logp, const float* old_logp, const float* 
   p.mean = mean;
   p.stats = stats;
   p.grad = grad;
-  p.counts = static_cast<int*>(workspace);
+  p.counts = static_cast<float*>(workspace);
   p.scratch = scratch;
   return api_launched(launch_policy_loss(p, stream), "policy loss launch");
   });

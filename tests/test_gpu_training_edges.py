@@ -178,3 +178,16 @@ def test_clip_grad_norm_of_an_infinity_among_large_values(fs, torch_cuda, bad):
     norm = float(fs.clip_grad_norm([g], 1.0))
     assert math.isnan(norm) if math.isnan(bad) else norm == math.inf
     assert torch.equal(g.view(torch.int32), old.view(torch.int32))
+
+
+def test_policy_loss_of_a_sequence_of_more_than_2_to_the_31_tokens(fs, torch_cuda):
+    """One sequence of 2^32 + 5 tokens, weighted by its own length."""
+    torch = torch_cuda
+    N = (1 << 32) + 5
+    x = torch.zeros(N, device="cuda")
+    starts = torch.tensor([0, N], device="cuda")
+    stats, grad = fs.policy_loss(x, x, torch.ones(1, device="cuda"), seq_starts=starts, mean="sequence", adv_per_seq=True)
+    # every term is the weight, 1 / N: two conversions, a product and a division, half a step each
+    for at in (slice(0, 1000), slice((1 << 31) - 500, (1 << 31) + 500), slice(N - 1000, N)):
+        assert float((grad[at].double() * N + 1).abs().max()) <= 4 * U
+    assert abs(float(stats[1]) + 1) <= 20 * U               # (16 rounds of fp32 sums on top)

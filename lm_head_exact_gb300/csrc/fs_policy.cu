@@ -200,7 +200,11 @@ __device__ __forceinline__ void tokens(const PolicyProblem& p, const Weights& w,
     const float A = kBySeq && p.adv_per_seq ? seq_adv : x.adv[j];
     const float d = x.lp[j] - x.old[j];
     const bool cut = is_clipped(A, d, x.lp[j], x.old[j], p.log_hi, p.log_lo);
-    const float rA = expf(d) * A;
+    float rA = expf(d) * A;
+    if (d > 88.0f) {                             // where e^d may pass fp32's range and r A does not
+      const float half = expf(0.5f * d);
+      rA = A == 0.0f && d < INFINITY ? 0.0f : A * half * half;
+    }
     const float term = cut ? (A > 0.0f ? p.hi : p.lo) * A : rA;
     policy = x.on[j] ? fmaf(-term, weight, policy) : policy;
     float grad = cut ? 0.0f : -rA;

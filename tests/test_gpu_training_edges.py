@@ -191,3 +191,22 @@ def test_policy_loss_of_a_sequence_of_more_than_2_to_the_31_tokens(fs, torch_cud
     for at in (slice(0, 1000), slice((1 << 31) - 500, (1 << 31) + 500), slice(N - 1000, N)):
         assert float((grad[at].double() * N + 1).abs().max()) <= 4 * U
     assert abs(float(stats[1]) + 1) <= 20 * U               # (16 rounds of fp32 sums on top)
+
+
+@pytest.mark.parametrize("mean", ["token", "none"])
+def test_policy_loss_of_ratios_past_fp32(fs, torch_cuda, mean):
+    """exp(logp - old) above fp32's range: no advantage, no term; a small
+    negative one, a finite term."""
+    torch = torch_cuda
+    logp = np.float32([-0.5, -0.25, -1.0, -0.5, -2.0, -0.125, -0.75])
+    old = np.float32([-100.5, -300.0, -91.0, -89.0, -2.5, -120.0, -95.75])
+    adv = np.float32([0.0, 0.0, -1e-6, 0.0, 0.5, 1.0, -1e-4])
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    stats, grad = fs.policy_loss(dev(logp), dev(old), dev(adv), mean=mean)
+    want = tr.policy(logp, old, adv, [7], mean=mean)
+    # exp of half the difference within 2 steps, twice; the products and the weight: 16 half steps
+    assert np.all(np.abs(_host(grad) - want.grad) <= 16 * U * np.abs(want.grad))
+    for got, x in zip(_host(stats), (want.loss, want.policy, 0.0, want.clipped)):
+        assert abs(got - x) <= 20 * U * abs(x)
+    inf = torch.full((1,), -math.inf, device="cuda")       # 0 times an infinite ratio is none of these
+    assert math.isnan(float(fs.policy_loss(torch.zeros(1, device="cuda"), inf, torch.zeros(1, device="cuda"))[0][0]))

@@ -426,7 +426,9 @@ FS_API size_t fs_token_logprobs_backward_workspace_bytes(int64_t n, int64_t d, i
  *   stats [4] fp32: loss, its policy term, its KL term (before kl_coef) and
  *     the weighted share of clipped tokens; grad [N] fp32.  All zero when no
  *     token takes part.
- *   0 <= clip_low < 1, clip_high >= 0, kl_coef finite (0 without ref_logp).
+ *   0 <= clip_low < 1, clip_high >= 0, kl_coef finite (0 without ref_logp;
+ *     with it, 0 measures the KL term only, and one that passes fp32's range
+ *     reaches neither loss nor gradient).
  *   workspace: fs_policy_loss_workspace_bytes(n_seqs) bytes, for
  *     FS_MEAN_SEQUENCE only (NULL otherwise).
  * Sums are held in fp64; the results do not depend on the run.

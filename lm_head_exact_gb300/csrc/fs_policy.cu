@@ -213,7 +213,7 @@ __device__ __forceinline__ void tokens(const PolicyProblem& p, const Weights& w,
       float estimate, em1;
       kl_terms(x.ref[j] - x.lp[j], estimate, em1);
       kl = x.on[j] ? fmaf(estimate, weight, kl) : kl;
-      grad = fmaf(-p.kl_coef, em1, grad);
+      grad = p.kl_coef != 0.0f ? fmaf(-p.kl_coef, em1, grad) : grad;      // (em1 may be infinite)
     }
     g[j] = x.on[j] ? grad * weight : 0.0f;
   }
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const PolicyProbl
     block_sums(v, t);
   }
   if (threadIdx.x == 0) {
-    p.stats[0] = static_cast<float>(t[0] + static_cast<double>(p.kl_coef) * t[1]);
+    p.stats[0] = static_cast<float>(p.kl_coef != 0.0f ? t[0] + static_cast<double>(p.kl_coef) * t[1] : t[0]);
     p.stats[1] = static_cast<float>(t[0]);
     p.stats[2] = static_cast<float>(t[1]);
     p.stats[3] = static_cast<float>(t[2]);

@@ -210,3 +210,21 @@ def test_policy_loss_of_ratios_past_fp32(fs, torch_cuda, mean):
         assert abs(got - x) <= 20 * U * abs(x)
     inf = torch.full((1,), -math.inf, device="cuda")       # 0 times an infinite ratio is none of these
     assert math.isnan(float(fs.policy_loss(torch.zeros(1, device="cuda"), inf, torch.zeros(1, device="cuda"))[0][0]))
+
+
+def test_policy_loss_that_only_measures_the_kl(fs, torch_cuda):
+    """kl_coef 0: an estimate past fp32's range is reported, and neither loss
+    nor gradient holds a NaN from 0 times infinity."""
+    torch = torch_cuda
+    logp = np.float32([-100.0, -0.5, -1.0])
+    old = np.float32([-99.5, -0.5, -1.25])
+    adv = np.float32([-0.5, 1.0, -1.0])
+    ref = np.float32([-0.5, -0.75, -1.0])
+    dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    stats, grad = fs.policy_loss(dev(logp), dev(old), dev(adv), ref_logp=dev(ref))
+    want = tr.policy(logp, old, adv, [3], ref=ref)
+    assert np.all(np.abs(_host(grad) - want.grad) <= 16 * U * np.abs(want.grad))
+    got = _host(stats)
+    assert abs(got[0] - want.policy) <= 20 * U and abs(got[1] - want.policy) <= 20 * U and got[2] == math.inf
+    plain, grad2 = fs.policy_loss(dev(logp), dev(old), dev(adv))
+    assert torch.equal(grad, grad2) and torch.equal(plain[:2], stats[:2])

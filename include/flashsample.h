@@ -455,7 +455,8 @@ FS_API size_t fs_policy_loss_workspace_bytes(int64_t n_seqs);
  *     counts and FS_TYPE_*; types may differ, sizes may be 0.
  *   outs: host array of device pointers for the scaled gradients (each its
  *     gradient's own pointer, or memory that overlaps no gradient), or NULL
- *     for the norm alone.
+ *     for the norm alone.  Written memory is no other tensor's: a gradient that
+ *     is listed twice cannot be scaled in place (FS_ERR_INVALID_ARG).
  *   max_norm >= 0; +inf never scales.  norm (device fp32 [1]): the norm
  *     before scaling.
  * The scaled values are formed in fp32 and rounded once.  A norm that is not

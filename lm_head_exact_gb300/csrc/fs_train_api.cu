@@ -3,6 +3,7 @@
 // include/flashsample.h.
 #include <algorithm>
 #include <cmath>
+#include <vector>
 
 #include "flashsample.h"
 #include "fs_api_util.h"
@@ -133,6 +134,33 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const char* x = static_cast<const char*>(a);
   const char* y = static_cast<const char*>(b);
   return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
+// Whether a tensor that fs_clip_grad_norm writes shares memory with another
+// one: blocks scale in any order, so it would be scaled once or twice.
+bool written_twice(const void* const* grads, void* const* outs, const int64_t* sizes, const int* types, int n,
+                   bool scales) {
+  struct Span {
+    uintptr_t at, end;
+    bool written;
+  };
+  std::vector<Span> spans;
+  spans.reserve(2 * static_cast<size_t>(n));
+  for (int i = 0; i < n; ++i) {
+    const uintptr_t bytes = static_cast<uintptr_t>(sizes[i]) * (types[i] == FS_TYPE_F32 ? 4 : 2);
+    const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(outs[i]);
+    if (bytes == 0) continue;
+    spans.push_back({g, g + bytes, scales && o == g});
+    if (o != g) spans.push_back({o, o + bytes, true});
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.at < b.at; });
+  uintptr_t end = 0, written = 0;         // of the spans so far, and of the written ones
+  for (const Span& s : spans) {
+    if (s.at < (s.written ? end : written)) return true;
+    end = std::max(end, s.end);
+    if (s.written) written = std::max(written, s.end);
+  }
+  return false;
 }
 
 }  // namespace
@@ -300,16 +328,14 @@ fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, const i
     if (types[i] < FS_TYPE_F32 || types[i] > FS_TYPE_F16)
       return api_fail(FS_ERR_INVALID_ARG, "unknown type %d of tensor %d", types[i], i);
   }
+  if (outs != nullptr && written_twice(grads, outs, sizes, types, n_tensors, !std::isinf(max_norm)))
+    return api_fail(FS_ERR_INVALID_ARG, "an output overlaps another tensor, or its gradient without being it");
   FS_API_TRY(api_check_array(norm, 4, "norm"));
   for (int i = 0; i < n_tensors; ++i) {
     if (sizes[i] == 0) continue;
     const size_t width = types[i] == FS_TYPE_F32 ? 4 : 2;
     FS_API_TRY(api_check_array(grads[i], width, "a gradient"));
-    if (outs != nullptr && outs[i] != grads[i]) {
-      FS_API_TRY(api_check_array(outs[i], width, "an output"));
-      if (overlaps(outs[i], sizes[i] * width, grads[i], sizes[i] * width))
-        return api_fail(FS_ERR_INVALID_ARG, "outs[%d] overlaps its gradient without being it", i);
-    }
+    if (outs != nullptr && outs[i] != grads[i]) FS_API_TRY(api_check_array(outs[i], width, "an output"));
   }
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const CallLock lock(stream);

@@ -97,3 +97,24 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(built_library):
         fs.token_logprobs(h, W, ids, t, bias=torch.zeros(3, 4))
     with pytest.raises(fs.FlashSampleError, match="norm_type"):
         fs.clip_grad_norm([g], 1.0, norm_type=1.0)
+
+
+@pytest.mark.parametrize("what,grads,outs,sizes,types,max_norm,refused", [
+    ("listed twice", [4096, 4096], [4096, 4096], [8, 8], [0, 0], 1.0, True),
+    ("listed twice, only measured", [4096, 4096], [4096, 4096], [8, 8], [0, 0], float("inf"), False),
+    ("listed twice, written elsewhere", [4096, 4096], [8192, 8224], [8, 8], [0, 0], 1.0, False),
+    ("one output for two", [4096, 5000], [8192, 8192], [8, 8], [0, 0], 1.0, True),
+    ("one output for two, unscaled", [4096, 5000], [8192, 8192], [8, 8], [0, 0], float("inf"), True),
+    ("overlapping views in place", [4096, 4112], [4096, 4112], [8, 8], [0, 1], 1.0, True),
+    ("neighbours in place", [4096, 4112], [4096, 4112], [8, 8], [1, 1], 1.0, False),
+    ("an output on another gradient", [4096, 8192], [8200, 6000], [8, 8], [0, 0], 1.0, True),
+    ("an output on its gradient's rest", [4096], [4100], [8], [0], 1.0, True),
+    ("a large one around a small one", [4096, 4200], [4096, 4200], [1000, 2], [0, 2], 1.0, True),
+    ("empty ones anywhere", [4096, 4096, 4100], [4096, 4096, 4100], [8, 0, 0], [0, 0, 0], 1.0, False),
+])
+def test_clip_refuses_memory_that_would_be_scaled_twice(lib, what, grads, outs, sizes, types, max_norm, refused):
+    n = len(grads)
+    status = lib.fs_clip_grad_norm((ctypes.c_void_p * n)(*grads), (ctypes.c_void_p * n)(*outs),
+                                   (ctypes.c_int64 * n)(*sizes), (ctypes.c_int * n)(*types), n, max_norm, 0, Z, Z)
+    assert status == 1
+    assert ("overlaps" in _last(lib)) == refused and ("norm is NULL" in _last(lib)) != refused

@@ -51,13 +51,6 @@ __device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
       : "r"(taddr));
 }
 
-// 32 TMEM lanes x 1 32-bit column.
-__device__ __forceinline__ uint32_t tmem_ld_1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-  return r;
-}
-
 // Shared-memory matrix descriptor of a bf16 operand stored along its M or N axis
 // (MN-major) with the 128-byte swizzle: boxes of 64 MN elements (128 bytes) by 64 k rows, 8192 bytes each, one after another
 // along MN.  Leading byte offset: from one 64-element block to the next;

@@ -228,3 +228,104 @@ def test_policy_loss_that_only_measures_the_kl(fs, torch_cuda):
     assert abs(got[0] - want.policy) <= 20 * U and abs(got[1] - want.policy) <= 20 * U and got[2] == math.inf
     plain, grad2 = fs.policy_loss(dev(logp), dev(old), dev(adv))
     assert torch.equal(grad, grad2) and torch.equal(plain[:2], stats[:2])
+
+
+def _peaked_tolerances(hp, s, grads):
+    """As Head.tolerances, with an own entry whose remainder is added in fp32
+    and which is known to what 1 - p is."""
+    ds, live, gh, gW = grads
+    n, V, d = len(hp.ids), hp.W.shape[0], hp.h.shape[1]
+    rows = np.nonzero(live)[0]
+    h64 = np.where(live[:, None], np.abs(hp.h.astype(np.float64)), 0.0)
+    W64 = np.abs(hp.W.astype(np.float64))
+    size = np.abs(hp.h.astype(np.float64)) @ W64.T
+    tx = (d + 4) * 2 * U * size * s.inv_t[:, None]
+    t_lse = tx.max(1) + (V / 8 + 32) * U + 4 * U * np.abs(s.lse)
+    p = np.where(live[:, None], np.exp(s.x - s.lse[:, None]), 0.0)
+    c = np.abs(hp.g.astype(np.float64) * s.inv_t)[:, None] * live[:, None]
+    t_ds = c * p * (tx + t_lse[:, None] + 2.0 ** -20 + 8 * U * np.abs(s.lse)[:, None]) + np.abs(ds) * (HALF_BF16 + 4 * U)
+    t_ds[rows, hp.ids[rows]] = (c * (tx + t_lse[:, None]))[rows, hp.ids[rows]] + 8 * U * np.abs(ds[rows, hp.ids[rows]])
+    tol = [t_ds @ W64 + (V + 32) * 2 * U * (np.abs(ds) @ W64) + HALF_BF16 * np.abs(gh),
+           t_ds.T @ h64 + (n + 32) * 2 * U * (np.abs(ds).T @ h64) + HALF_BF16 * np.abs(gW)]
+    return [1.01 * t + 1e-37 for t in tol]
+
+
+@pytest.mark.parametrize("kept", [True, False])
+@pytest.mark.parametrize("n,d,V", [(20, 64, 3000), (100, 256, 1000), (300, 72, 1700)])
+def test_gradients_of_peaked_rows(fs, torch_cuda, n, d, V, kept):
+    """Most of a row's probability on one to three tokens, its own among them
+    for half the rows."""
+    torch = torch_cuda
+    from test_gpu_training import Head
+    hp = Head(n, d, V, "none", seed=21, scale=12.0)
+    top = np.argmax(hp.h.astype(np.float64) @ hp.W.astype(np.float64).T, 1)
+    hp.ids = np.where((np.arange(n) % 2 == 0) & (hp.ids >= 0), top, hp.ids)
+    h, W, ids, temp, _, g = hp.device(torch)
+    keep = fs.logprob_buffer(n, V) if kept else None
+    logp, lse = fs.token_logprobs(h, W, ids, temp, kept=keep)
+    got = fs.token_logprobs_backward(h, W, ids, temp, logp, lse, g, kept=keep)
+    s, grads = hp.reference()
+    for x, want, tol, what in zip(got, grads[2:], _peaked_tolerances(hp, s, grads), ("grad_h", "grad_W")):
+        over = np.abs(_host(x) - want) / tol
+        assert over.max() <= 1, (what, over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+# Rounding a result to bf16 is off by 2^-8 / m / sqrt(3) (m the mantissa in [1, 2), spread evenly over its
+# logarithm) in the mean square: 0.00166 of it.  In flat rows the own entry is nearly all of ds; rounding
+# it too would make that 0.0023.  The bound lies between, 20% above the first.
+FLAT_ERROR = 0.0020
+
+
+def _error(got, want):
+    return float(np.linalg.norm(got - want) / np.linalg.norm(want))
+
+
+@pytest.mark.parametrize("kept", [True, False])
+@pytest.mark.parametrize("n,d,V", [(100, 256, 1000), (300, 520, 1700)])
+def test_own_entries_are_not_rounded_to_bf16(fs, torch_cuda, n, d, V, kept):
+    torch = torch_cuda
+    from test_gpu_training import Head
+    hp = Head(n, d, V, "none", seed=21)
+    h, W, ids, temp, _, g = hp.device(torch)
+    keep = fs.logprob_buffer(n, V) if kept else None
+    logp, lse = fs.token_logprobs(h, W, ids, temp, kept=keep)
+    got = fs.token_logprobs_backward(h, W, ids, temp, logp, lse, g, kept=keep)
+    _, (ds, live, want_h, want_W) = hp.reference()
+    assert _error(_host(got[0]), want_h) < FLAT_ERROR and _error(_host(got[1]), want_W) < FLAT_ERROR
+    # with every entry of ds rounded, the reference itself is further off
+    round_bf16 = lambda a: synthetic.bf16_bits_to_f32(synthetic.bf16_bits(a.astype(np.float32))).astype(np.float64)  # noqa: E731
+    ds = round_bf16(ds)
+    h64 = np.where(live[:, None], hp.h.astype(np.float64), 0.0)
+    assert _error(round_bf16(ds @ hp.W), want_h) > FLAT_ERROR and _error(round_bf16(ds.T @ h64), want_W) > FLAT_ERROR
+
+
+def test_own_entries_when_the_vocabulary_comes_in_pieces(fs, torch_cuda):
+    """So many tokens that ds is formed for a part of the vocabulary at a time:
+    the remainder belongs to the piece that holds the token."""
+    torch = torch_cuda
+    n, d, V = 70000, 64, 33000
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    h = torch.randn(n, d, generator=gen, device="cuda").bfloat16()
+    W = (torch.randn(V, d, generator=gen, device="cuda") / 8).bfloat16()
+    ids = torch.randint(0, V, (n,), generator=gen, device="cuda")
+    temp, g = torch.ones(n, device="cuda"), torch.randn(n, generator=gen, device="cuda")
+    logp, lse = fs.token_logprobs(h, W, ids, temp)
+    got = [fs.token_logprobs_backward(h, W, ids, temp, logp, lse, g)]
+    keep = fs.logprob_buffer(n, V)
+    logp, lse = fs.token_logprobs(h, W, ids, temp, kept=keep)
+    got.append(fs.token_logprobs_backward(h, W, ids, temp, logp, lse, g, kept=keep))
+    del keep
+    W64 = W.double()
+    want_h, want_W = torch.empty(n, d, dtype=torch.float64, device="cuda"), torch.zeros_like(W64)
+    for i in range(0, n, 5000):
+        at = slice(i, i + 5000)
+        h64 = h[at].double()
+        ds = -(h64 @ W64.T).softmax(1)
+        ds[torch.arange(ds.shape[0], device="cuda"), ids[at]] += 1
+        ds *= g[at].double()[:, None]
+        want_h[at] = ds @ W64
+        want_W += ds.T @ h64
+    for gh, gW in got:
+        for x, want in ((gh, want_h), (gW, want_W)):
+            for half in (slice(0, len(x) // 2), slice(len(x) // 2, None)):     # (both pieces of grad_W)
+                assert float((x[half].double() - want[half]).norm() / want[half].norm()) < FLAT_ERROR

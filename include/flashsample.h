@@ -365,6 +365,9 @@ FS_API fs_status fs_sample_noalloc(const void* h, const void* W, int64_t B, int6
  * the temperature is invalid).  A row whose every x is -inf has lse -inf; a
  * token at x = -inf has logp -inf.  A logit that is NaN or +inf gives NaN for
  * its row's lse and logp, whatever the token's own logit is, and for no other.
+ * The fp32 sums of a logit are cut into pieces of 1024 products for n <= 256
+ * and of 2048 beyond, and reduced in an order that depends on n: a token's
+ * scores in two calls of different n differ by up to some 1e-6 of |lse|.
  *   kept (nullable): fp32 [fs_logprob_buffer_elems(n, V)] where the call
  *     leaves the logits for fs_token_logprobs_backward, 16-byte aligned.
  *     Without it the n x V logits never reach device memory.
@@ -390,9 +393,11 @@ FS_API int64_t fs_logprob_buffer_elems(int64_t n, int64_t V);
  * its buffer, or NULL to form the logits again from h, W and bias.
  * Rows that are not scored, have g == 0, lse == -inf or logp == -inf carry no
  * gradient: their grad_h is zero and their h may hold anything.
- * Products take ds rounded to bf16 and accumulate in fp32; what the rounding
- * leaves over of each token's own entry, the largest of its row, is added in
- * fp32.
+ * Products take ds rounded to bf16 and accumulate in fp32 (in the tensor
+ * cores, which cut and do not round); what the rounding leaves over of each
+ * token's own entry, the largest of its row, is added in fp32.  Where few
+ * other entries hold as much as the own one, their rounding (2^-8 of each) is
+ * in the gradients besides the rounding of the results.
  *   workspace: fs_token_logprobs_backward_workspace_bytes(n, d, V) bytes.
  */
 FS_API fs_status fs_token_logprobs_backward(const void* h, const void* W, int64_t n, int64_t d, int64_t V,

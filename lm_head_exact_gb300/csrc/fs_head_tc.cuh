@@ -166,6 +166,10 @@ struct Units {
 };
 
 // ---------------------------------------------------------------- logit epilogues
+// Exponentials are __expf's, within some 2^-21 of their value where the result
+// matters: a term of a row's sum, or an entry of ds that is rounded to 2^-8
+// right after.  expf's further bits would be lost in the logits' own error, and
+// its instructions are on every element.
 constexpr float kLowest = -3.402823466e38f;  // the lowest finite value
 
 // value(i) of 16 columns joined over the warp's lanes: lanes 2 i and 2 i + 1
@@ -226,7 +230,9 @@ __device__ __forceinline__ __nv_bfloat16 ds_of(float x, float lse, float coef) {
 
 // The tokens t whose own rows are among the 32 rows from m_warp on, in order,
 // with the row's number; the whole warp looks at 128 tokens at a time and
-// visits each one found together.
+// visits each one found together.  Tokens that share a row are visited one
+// after another, 0.9 us each: where most of some ten thousand tokens have one
+// id, or the vocabulary has fewer rows than that, this is what grad_W takes.
 template <typename Visit>
 __device__ __forceinline__ void each_own(const Args& a, int m_warp, Visit visit) {
   const int lane = threadIdx.x & 31;
@@ -252,6 +258,10 @@ __device__ __forceinline__ void each_own(const Args& a, int m_warp, Visit visit)
   }
 }
 
+// 576 threads leave 96 registers each.  The epilogues of kLse and kDs hold 64
+// logits and 8 part values and spill (kLse 232 bytes, with a bias 196; kDs 92 and
+// 268; kDh 76, kDw 24), which is part of what bounds narrow heads, where an
+// epilogue is longer than a tile's products.
 template <Kind kKind, bool kBias>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,

@@ -5,8 +5,8 @@
 //   loss += w (-min(r A, clip(r) A) + kl (e^q - 1 - q)),
 //   grad  = w (-r A [not clipped] + kl (1 - e^q)).
 //
-// Each token is read once and its gradient written once (12 to 17 bytes in, 4
-// out).  The weights need the number of tokens that take part: with a mask or
+// Each token is read once and its gradient written once (8 bytes in, up to 17
+// with reference, advantage and mask by token, and 4 out).  The weights need the number of tokens that take part: with a mask or
 // a mean over sequences a counting launch goes first, which reads the mask
 // only (one byte a token).
 #include <algorithm>

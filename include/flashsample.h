@@ -475,6 +475,111 @@ FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, 
                                    const int* types, int n_tensors, double max_norm, int norm_type, float* norm,
                                    void* stream);
 
+/* ------------------------------------------------------------------------
+ * An 8-bit LM head, and the norm ahead of it.  A matrix in 8 bits [rows, k]
+ * is a pair: q, one byte an element (FS_TYPE_E4M3 or FS_TYPE_E5M2, rows
+ * q_row_stride bytes apart: a multiple of 16, 16-byte aligned; what lies
+ * between k and the stride is neither read nor written), and fp32 scales, one
+ * for each block of 128 elements of a row, the last one possibly short.  Block
+ * (i, j) has its scale at scale[i * scale_row_stride + j * scale_col_stride];
+ * a row i is one row of q (block_rows 1) or 128 (block_rows 128).  q times its
+ * scale is the value.  Rows of scales side by side (scale_row_stride 1) are
+ * read fastest where block_rows is 1.  None of these calls needs a workspace,
+ * but for fs_layer_norm_backward's, which comes from the caller as the training
+ * calls' does.  Widths need not be multiples of anything.
+ * ------------------------------------------------------------------------ */
+
+/* 8-bit element types, beside FS_TYPE_F32, _BF16 and _F16. */
+#define FS_TYPE_E4M3 3
+#define FS_TYPE_E5M2 4
+
+/*
+ * Quantising: for every block of block_rows (1 or 128) x 128 elements of the
+ * matrix [R, C], which is x [rows, cols] or, with transpose 1, its transpose,
+ *   scale = max(amax / largest, 2^-100),  q = x * (1 / scale)  to nearest even,
+ * largest being 448 (FS_TYPE_E4M3) or 57344 (FS_TYPE_E5M2); amax / largest,
+ * the reciprocal and the product are each rounded to fp32.  A NaN stays one and
+ * does not count into amax; an infinity makes its whole block NaN.
+ *   x: fp32, bf16 or fp16 (x_type), rows x_row_stride >= cols elements apart.
+ *   q [R, C], scale [ceil(R / block_rows), ceil(C / 128)]: outputs.  Scale
+ *     strides >= 0 that keep the scales apart (not checked).
+ *   rows, cols < 2^31.
+ */
+FS_API fs_status fs_quantize_fp8(const void* x, int x_type, int64_t rows, int64_t cols, int64_t x_row_stride,
+                                 int transpose, int block_rows, int q_type, void* q, int64_t q_row_stride,
+                                 float* scale, int64_t scale_row_stride, int64_t scale_col_stride, void* stream);
+
+/*
+ * The product of two 8-bit matrices a [m, k] (block_rows 1) and b [n, k]
+ * (block_rows 1 or 128):
+ *   out[i, j] = sum over blocks of a_scale b_scale (sum within the block of a[i, :] b[j, :])
+ * The products of a block are summed by the tensor cores, the blocks in fp32
+ * registers, in an order that the sizes fix; a_scale b_scale is formed first, in fp32 (its overflow
+ * is an infinity).  out: fp32, bf16 or fp16, rows out_row_stride >= n elements
+ * apart, rounded once.  Types of a and b may differ.  m, n, k < 2^31 - 1024; k == 0
+ * gives zeros.  out overlaps neither a nor b.
+ * For a linear layer in training: y = x8 W8^T, grad_x = g8 (W^T)8^T with
+ * W^T from a transposing fs_quantize_fp8 (of 128 x 128 blocks: the same
+ * values as W's), grad_W = (g^T)8 (x^T)8^T, both quantised along the tokens.
+ */
+FS_API fs_status fs_fp8_matmul(const void* a, int a_type, int64_t a_row_stride, const float* a_scale,
+                               int64_t a_scale_row_stride, int64_t a_scale_col_stride, const void* b, int b_type,
+                               int64_t b_row_stride, const float* b_scale, int64_t b_scale_row_stride,
+                               int64_t b_scale_col_stride, int b_block_rows, int64_t m, int64_t n, int64_t k,
+                               void* out, int out_type, int64_t out_row_stride, void* stream);
+
+/*
+ * fs_sample_ex with h [B, d] and the head W [V, d] in 8 bits, both
+ * FS_TYPE_E4M3: h quantised by rows (block_rows 1; fs_quantize_fp8 or
+ * fs_layer_norm), W by rows or in blocks of 128 x 128 (W_block_rows).  The
+ * same noise, temperatures, bias, ties and outputs as fs_sample_ex, over the
+ * logits that fs_fp8_matmul forms; reads half the bytes of a bf16 head.
+ * d < 2^31 - 1024, B and V < 2^31.  Uses the sampling workspace of
+ * (device, stream): fs_workspace_reserve() before a capture.
+ */
+FS_API fs_status fs_sample_fp8(const void* h, int64_t h_row_stride, const float* h_scale, int64_t h_scale_row_stride,
+                               int64_t h_scale_col_stride, const void* W, int64_t W_row_stride, const float* W_scale,
+                               int64_t W_scale_row_stride, int64_t W_scale_col_stride, int W_block_rows, int64_t B,
+                               int64_t d, int64_t V, const float* temp, const float* bias, int64_t bias_row_stride,
+                               uint64_t seed, uint64_t step, int64_t* out_ids, float* out_max, void* stream);
+
+/*
+ * Layer norm of the rows of x [n, d], and its form without the mean (rms 1):
+ *   y = (x - mean) rstd weight + bias,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   x: fp32, bf16 or fp16 (x_type), rows x_row_stride >= d elements apart.
+ *   weight, bias (nullable: 1 and 0) [d] of w_type: fp32 or x_type.
+ *   y [n, d] of x_type, rows y_row_stride apart (it may be x itself), or NULL
+ *     with q: y quantised from its fp32 values as fs_quantize_fp8 does with
+ *     block_rows 1, into q (q_type) and scale.  One of y and q.
+ *   mean, rstd (nullable) [n] fp32, for the backward pass; mean is not written
+ *     with rms.
+ *   1 <= d <= 32768, n < 2^31, eps >= 0.
+ */
+FS_API fs_status fs_layer_norm(const void* x, int x_type, int64_t n, int64_t d, int64_t x_row_stride,
+                               const void* weight, const void* bias, int w_type, int rms, double eps, void* y,
+                               int64_t y_row_stride, float* mean, float* rstd, void* q, int q_type,
+                               int64_t q_row_stride, float* scale, int64_t scale_row_stride,
+                               int64_t scale_col_stride, void* stream);
+
+/*
+ * Backward pass of fs_layer_norm: given g = dL/dy [n, d] of x_type, with
+ * xh = (x - mean) rstd and a = g weight,
+ *   grad_x = rstd (a - mean(a) - xh mean(a xh))     (rms: without mean(a))
+ *   grad_weight = sum over rows of g xh,  grad_bias = sum over rows of g
+ * each nullable; grad_x [n, d] of x_type (it may be g itself), grad_weight and
+ * grad_bias [d] of w_type.  mean and rstd are the forward call's (mean NULL
+ * with rms).  Sums are held in fp32 and do not depend on the run.
+ *   workspace: fs_layer_norm_backward_workspace_bytes(n, d) bytes, or NULL
+ *     where FS_SMALL_WORKSPACE suffices or no sums are wanted.
+ */
+FS_API fs_status fs_layer_norm_backward(const void* g, int64_t g_row_stride, const void* x, int x_type, int64_t n,
+                                        int64_t d, int64_t x_row_stride, const void* weight, int w_type, int rms,
+                                        const float* mean, const float* rstd, void* grad_x, int64_t grad_x_row_stride,
+                                        void* grad_weight, void* grad_bias, void* workspace, size_t workspace_bytes,
+                                        void* stream);
+
+FS_API size_t fs_layer_norm_backward_workspace_bytes(int64_t n, int64_t d);
+
 /* Workspace bytes one sampling call with (B, V) needs on the current device
  * (the training calls' fixed block is not among them). */
 FS_API size_t fs_workspace_bytes(int64_t B, int64_t V);

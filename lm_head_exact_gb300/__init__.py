@@ -9,6 +9,7 @@ is no CPU fallback.
 
 __all__ = ["sample", "sample_ex", "sample_chunked", "sample_unfused", "sample_host",
            "token_logprobs", "token_logprobs_backward", "logprob_buffer", "policy_loss", "clip_grad_norm",
+           "quantize_fp8", "fp8_matmul", "sample_fp8", "layer_norm", "layer_norm_fp8", "layer_norm_backward",
            "FlashSampleError", "library"]
 
 

@@ -567,6 +567,8 @@ bool api_later_launch_fails() { return injected_fault() == FS_FAULT_LATER_LAUNCH
 
 fs_status api_error_word(int** out, cudaStream_t stream) { return error_word(out, stream); }
 
+fs_status api_finish(cudaStream_t stream, int64_t B, Finish* f) { return get_finish(stream, B, f); }
+
 fs_status api_train_scratch(cudaStream_t stream, TrainScratch** out) {
   int dev;
   FS_TRY(current_device(&dev));

@@ -50,6 +50,9 @@ fs_status api_check_launch();
 bool api_later_launch_fails();
 fs_status api_error_word(int** out, cudaStream_t stream);
 fs_status api_train_scratch(cudaStream_t stream, TrainScratch** out);
+struct Finish;
+// The keys and the ticket that a sampling launch of up to B rows finishes through.
+fs_status api_finish(cudaStream_t stream, int64_t B, Finish* f);
 
 #define FS_API_TRY(expr)              \
   do {                                \

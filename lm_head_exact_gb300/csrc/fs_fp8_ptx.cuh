@@ -1,0 +1,83 @@
+// What the 8-bit products use of the tensor cores beyond the layers of the
+// 16-bit kernels (fs_sm100.cuh, fs_head_ptx.cuh): tcgen05.mma kind::f8f6f4, its
+// instruction descriptor, issue by an elected lane within one CTA, and loads
+// from the shared memory of another CTA of the cluster.
+#pragma once
+
+#include "fs_head_ptx.cuh"
+
+namespace fs {
+namespace sm100 {
+
+// Instruction descriptor of kind::f8f6f4 with fp32 D, both operands K-major;
+// the 8-bit formats are 0 (E4M3) and 1 (E5M2), each operand its own.
+__host__ __device__ constexpr uint32_t idesc_fp8_f32(uint32_t a_e5m2, uint32_t b_e5m2, uint32_t M, uint32_t N) {
+  return (1u << 4)            // D format: f32
+         | (a_e5m2 << 7)      // A format
+         | (b_e5m2 << 10)     // B format
+         | ((N >> 3) << 17)   // N / 8
+         | ((M >> 4) << 24);  // M / 16
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T over 32 elements of k.
+__device__ __forceinline__ void mma_fp8_if(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+
+// The same over a pair of CTAs (see mma_bf16_pair).
+__device__ __forceinline__ void mma_fp8_pair_if(uint32_t elected, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_if(uint32_t elected, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(elected)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d_if(uint32_t elected, uint32_t smem_dst, const void* tmap, uint32_t bar,
+                                               int32_t x, int32_t y, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;\n\t}" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "l"(policy), "r"(elected)
+      : "memory");
+}
+
+// Waits for the TMEM loads issued so far.  The registers that they write are
+// operands, so that no use of them is moved ahead of the wait.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+}  // namespace sm100
+}  // namespace fs

@@ -20,4 +20,9 @@ bool encode_rows_bf16(CUtensorMap* tm, const void* base, int64_t rows, int64_t c
 // The same over a matrix without gaps, d elements a row.
 bool encode_kmajor_bf16(CUtensorMap* tm, const void* base, int64_t rows, int64_t d, int box_cols, int box_rows);
 
+// The same over a matrix of bytes [rows, cols] whose rows lie `pitch` bytes
+// apart (a multiple of 16); cols need not be a multiple of anything.
+bool encode_rows_u8(CUtensorMap* tm, const void* base, int64_t rows, int64_t cols, int64_t pitch, int box_cols,
+                    int box_rows);
+
 }  // namespace fs

@@ -27,6 +27,9 @@ pytestmark = pytest.mark.gpu
 
 S = 45 * U
 EPS = 1e-5
+# Half the least step of a type: below 2^-14 fp16's values lie 2^-24 apart, whatever
+# the value, so a rounding there is off by up to 2^-25 (bf16 and fp32: 2^-134, 2^-150).
+LEAST = {"fp32": 2.0 ** -150, "bf16": 2.0 ** -134, "fp16": 2.0 ** -25}
 
 
 class Case:
@@ -99,7 +102,7 @@ def test_layer_norm_and_gradients(fs, torch_cuda, n, d, kind, w_kind, rms):
             assert mean is None
         else:
             near(mean, r.mean, e_mean, what + " mean")
-        near(y, r.y, e_y + HALF[kind] * np.abs(r.y) + 2.0 ** -25, what + " y")
+        near(y, r.y, e_y + HALF[kind] * np.abs(r.y) + LEAST[kind], what + " y")
         check_gradients(c, r, e_rstd, e_xh, fs.layer_norm_backward(g, x, w, mean, rstd), what)
 
 
@@ -116,12 +119,12 @@ def check_gradients(c, r, e_rstd, e_xh, got, what):
     e_max = (S + 3 * U) * (a * xh).mean(1) + (a * e_xh).mean(1)
     terms = a + m_a[:, None] + xh * m_ax[:, None]
     e = U * a + e_ma[:, None] + e_xh * m_ax[:, None] + xh * e_max[:, None] + 4 * U * terms
-    tol = r.rstd[:, None] * (e * 1.01 + terms * (e_rstd[:, None] + U)) + HALF[c.kind] * np.abs(want[0]) + 2.0 ** -25
+    tol = r.rstd[:, None] * (e * 1.01 + terms * (e_rstd[:, None] + U)) + HALF[c.kind] * np.abs(want[0]) + LEAST[c.kind]
     near(gx, want[0], tol, what + " grad_x")
     steps = (c.n / 1 + 304 / 16 + 24) * U
-    near(gw, want[1], steps * (np.abs(g) * xh).sum(0) + (np.abs(g) * e_xh).sum(0) * 1.01 + HALF[c.w_kind] * np.abs(want[1]) + 1e-30,
+    near(gw, want[1], steps * (np.abs(g) * xh).sum(0) + (np.abs(g) * e_xh).sum(0) * 1.01 + HALF[c.w_kind] * np.abs(want[1]) + LEAST[c.w_kind],
          what + " grad_weight")
-    near(gb, want[2], steps * np.abs(g).sum(0) + HALF[c.w_kind] * np.abs(want[2]) + 1e-30, what + " grad_bias")
+    near(gb, want[2], steps * np.abs(g).sum(0) + HALF[c.w_kind] * np.abs(want[2]) + LEAST[c.w_kind], what + " grad_bias")
 
 
 def test_without_weight_and_bias(fs, torch_cuda):
@@ -147,7 +150,7 @@ def test_many_rows(fs, torch_cuda):
         x, g, w, b = c.tensors(torch)
         y, mean, rstd = fs.layer_norm(x, w, b, eps=EPS)
         r, _, e_rstd, e_xh, e_y = c.reference()
-        near(y, r.y, e_y + HALF[kind] * np.abs(r.y) + 2.0 ** -25, f"{n} x {d} y")
+        near(y, r.y, e_y + HALF[kind] * np.abs(r.y) + LEAST[kind], f"{n} x {d} y")
         check_gradients(c, r, e_rstd, e_xh, fs.layer_norm_backward(g, x, w, mean, rstd), f"{n} x {d}")
 
 

@@ -496,9 +496,9 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
         if (!ok) break;
         turn_phase ^= 1;
       }
-      float acc[kLoads * kRegs];
+      f32x2 sum[kLoads * kRegs / 2];                       // columns by twos
 #pragma unroll
-      for (int c = 0; c < kLoads * kRegs; ++c) acc[c] = 0.0f;
+      for (int c = 0; c < kLoads * kRegs / 2; ++c) sum[c] = 0ull;
       uint32_t use = static_cast<uint32_t>(tile) * n_use, fill = static_cast<uint32_t>(tile) * n_fill;
 #pragma unroll 1
       for (int kb = k0; kb < k1; ++kb) {
@@ -552,29 +552,31 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
           ++use;
         }
         if (live) {
-          float2 w[kColScales ? kCols / 8 : 1];
+          f32x2 w[kColScales ? kCols / 8 : 1];
 #pragma unroll
           for (int q = 0; q < kLoads; ++q) {
             if constexpr (kColScales) {
               if (q % 2 == 0) {
 #pragma unroll
                 for (int g = 0; g < kCols / 8; ++g) {
-                  w[g] = *reinterpret_cast<const float2*>(col_scales + part * kPart + kCols * (q >> 1) + 8 * g + 2 * (lane & 3));
-                  if constexpr (!kLaneScales) {
-                    w[g].x *= f[0];
-                    w[g].y *= f[0];
-                  }
+                  w[g] = *reinterpret_cast<const f32x2*>(col_scales + part * kPart + kCols * (q >> 1) + 8 * g + 2 * (lane & 3));
+                  if constexpr (!kLaneScales) w[g] = mul2(w[g], pack2(f[0], f[0]));
                 }
               }
             }
 #pragma unroll
-            for (int i = 0; i < kRegs; ++i) {
-              float by = f[0];
-              if constexpr (kColScales) {
-                by = i & 1 ? w[i >> 2].y : w[i >> 2].x;
-                if constexpr (kLaneScales) by *= f[2 * (q & 1) + (i >> 1 & 1)];
+            for (int i = 0; i < kRegs; i += 2) {
+              f32x2 by;
+              if constexpr (!kColScales) {
+                by = pack2(f[0], f[0]);
+              } else if constexpr (kLaneScales) {
+                const float row = f[2 * (q & 1) + (i >> 1 & 1)];
+                by = mul2(w[i >> 2], pack2(row, row));
+              } else {
+                by = w[i >> 2];
               }
-              acc[q * kRegs + i] = fmaf(__uint_as_float(r[q][i]), by, acc[q * kRegs + i]);
+              f32x2& s = sum[(q * kRegs + i) / 2];
+              s = fma2(pack2(__uint_as_float(r[q][i]), __uint_as_float(r[q][i + 1])), by, s);
             }
           }
         }
@@ -587,6 +589,13 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
       if (!ok) break;
       __syncwarp();
       if (kGroups > 1 && lane == 0) mbar_arrive(&turn_bar[(group + 1) % kGroups]);
+      float acc[kLoads * kRegs];
+#pragma unroll
+      for (int c = 0; c < kLoads * kRegs / 2; ++c) {
+        const float2 v = unpack2(sum[c]);
+        acc[2 * c] = v.x;
+        acc[2 * c + 1] = v.y;
+      }
       if constexpr (kSplit) {
         // every load has landed and been multiplied: the stages hold the partial tile now
         float* red = reinterpret_cast<float*>(smem);

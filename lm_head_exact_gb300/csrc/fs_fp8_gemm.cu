@@ -31,7 +31,7 @@ Plan plan(int64_t m, int64_t n, int n_kb, int sms) {
   if (m <= kThinMaxRows) return Plan{kThin, thin_columns(m), split_of((n + kLanes - 1) / kLanes, 1)};
   Plan best{kWide, 192, 1};
   double best_time = 1e300;
-  const struct { Form form; int bn, ctas; double clocks; } forms[] = {{kPair, 192, 2, 520}, {kWide, 192, 1, 640}};
+  const struct { Form form; int bn, ctas; double clocks; } forms[] = {{kPair, 192, 2, 1000}, {kWide, 192, 1, 1000}};
   for (const auto& f : forms) {
     const int64_t tile_m = kLanes * f.ctas;
     const int64_t tiles = (m + tile_m - 1) / tile_m * ((n + f.bn - 1) / f.bn);

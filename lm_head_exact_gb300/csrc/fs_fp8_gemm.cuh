@@ -12,8 +12,8 @@
 //   kPair  256 rows of a over a pair of CTAs (tcgen05 cta_group::2), 192 rows of b, of
 //          which each CTA loads a half
 //
-// A stage of the TMA ring is one block of 128 elements of k: 128 bytes a row, one
-// swizzle row, four tcgen05.mma kind::f8f6f4 of 32.  The tensor cores' sum of a
+// A stage of the TMA ring is one or two blocks of 128 elements of k: 128 bytes a
+// row, one swizzle row, four tcgen05.mma kind::f8f6f4 of 32 each.  The tensor cores' sum of a
 // block, in fp32, is one of several TMEM buffers in turn; epilogue warps multiply
 // it by the block's scales and add it to registers while the next block is
 // multiplied.  (Scales are any fp32 numbers, so the hardware's power-of-two block
@@ -21,12 +21,16 @@
 // and not rounded, is short enough to lose nothing visible: the blocks are added
 // in registers, to nearest.)
 //
-// Twelve epilogue warps, a lane quarter and up to 64 columns each, so that a thread
-// holds a block's sums of all its columns beside the running ones: loads from TMEM
-// can only be waited for together, at some 200 clocks a time (two halves of 128
-// columns in turn: twice as long).  Where a tile has fewer columns, groups of
-// four warps take the tiles in turn, so that one tile's scan or stores overlap the
-// next tile's sums.  A warp of its own brings the scales to shared memory ahead.
+// What bounds it beyond few rows is the way of the sums through the epilogue, not
+// the MMAs: of a lane quarter's port and of its scheduler, loading a column's sums
+// from TMEM takes 2 clocks and adding them up 2 more, and what hands a buffer over
+// (barriers take 100 clocks to look at) some 300 a block.  kWide and kPair
+// therefore take 192 columns, by twelve warps of a lane quarter and 64 columns (1000
+// clocks a block; 256 columns by eight warps 1400, 128 by eight 800); kThin eight warps,
+// with registers for two blocks' sums, so that one is loaded while the other is
+// added up.  Where a tile has 64 columns or fewer, two groups of four warps take
+// the tiles in turn, so that one tile's scan or stores overlap the next tile's
+// sums.  A warp of its own brings the scales to shared memory ahead.
 //
 // With few tiles the k axis is split over the CTAs of a cluster; each leaves its
 // partial tile in its own shared memory, and every CTA adds a part of it
@@ -60,16 +64,8 @@ constexpr int kBarBytes = 1024;
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxSplits = 8;
 
-constexpr int kEpiWarps = 12;
-constexpr int kProducerWarp = 12, kMmaWarp = 13, kScaleWarp = 14;
-constexpr int kThreads = 16 * 32;
 constexpr int kAhead = 4;                      // blocks whose scales are brought at a time
 constexpr int kSlots = 2;                      // times that many
-
-// Registers of a thread at launch, and what the epilogue's three warpgroups and
-// the fourth one go on with.
-constexpr int kLaunchRegs = 128, kEpiRegs = 160, kOtherRegs = 32;
-static_assert(3 * kEpiRegs + kOtherRegs <= 4 * kLaunchRegs, "no more than the block was launched with");
 
 template <Form kForm, int kBN, bool kColScales>
 struct Shape {
@@ -77,14 +73,25 @@ struct Shape {
   static constexpr int kCtas = kForm == kPair ? 2 : 1;
   static constexpr int kTileL = kLanes * kCtas;
   static constexpr int kCLoad = kBN / kCtas;              // rows of the columns' operand a CTA loads
-  static constexpr int kStageBytes = kLTile + kCLoad * kBK;
+  static constexpr int kEpiWarps = kSwap ? 8 : 12;
+  static constexpr int kThreads = (kEpiWarps + 4) * 32;
+  // Registers of a thread at launch, and what the epilogue's warpgroups and the
+  // last one (producer, MMA, scales) go on with.
+  static constexpr int kLaunchRegs = kSwap ? 168 : 128, kEpiRegs = kSwap ? 232 : 160, kOtherRegs = kSwap ? 40 : 32;
+  static_assert(kEpiWarps / 4 * kEpiRegs + kOtherRegs <= (kEpiWarps / 4 + 1) * kLaunchRegs,
+                "no more than the block was launched with");
+  static constexpr int kPairK = kSwap ? 2 : 1;            // blocks of k in a stage
+  static constexpr bool kTwoBlocks = kSwap;               // registers for two blocks' sums
+  static constexpr int kBlockBytes = kLTile + kCLoad * kBK;       // of a block of k in a stage
+  static constexpr int kStageBytes = kPairK * kBlockBytes;
   static constexpr int kPart = kBN < 64 ? kBN : 64;       // columns of an epilogue warp
   static constexpr int kColParts = kBN / kPart;
   static constexpr int kGroups = kEpiWarps / 4 / kColParts;
   // Blocks of k that a TMEM buffer takes side by side: what hands a buffer over
   // is then done for several of them.
-  static constexpr int kPer = kSwap ? (kBN <= 32 ? 4 : 2) : 1;
-  static constexpr int kBufs = kBN == 192 ? 2 : 512 / (kBN * kPer) < 8 ? 512 / (kBN * kPer) : 8;
+  static constexpr int kPer = !kSwap ? 1 : kBN <= 32 ? 4 : 2;
+  static_assert(kPer % kPairK == 0, "a stage's blocks go into one buffer");
+  static constexpr int kBufs = 512 / (kBN * kPer) < 8 ? 512 / (kBN * kPer) : 8;
   static constexpr int kTmemCols = 512;
   // Scales of a block: the lanes' (or one, of their tile), then the columns' (or
   // one for each part).
@@ -206,13 +213,14 @@ __device__ __forceinline__ Best scan_staged(const float* at, int64_t v0, int64_t
 // whole lanes, where every thread needs them all, reading them took as much
 // of shared memory's bandwidth as the operands do.
 template <Form kForm, int kBN, bool kSample, bool kLaneScales, bool kColScales, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<kForm, kBN, kColScales>::kThreads, 1)
 kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUtensorMap tmap_c, const Args a) {
   using S = Shape<kForm, kBN, kColScales>;
   constexpr bool kSwap = S::kSwap, kPairs = kForm == kPair;
   static_assert(kColScales || kLaneScales, "scales of a tile of lanes are folded into those of the columns");
   constexpr int kStages = S::kStages, kBufs = S::kBufs, kPart = S::kPart, kGroups = S::kGroups;
-  constexpr int kPer = S::kPer;
+  constexpr int kPer = S::kPer, kPairK = S::kPairK, kEpiWarps = S::kEpiWarps;
+  constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1, kScaleWarp = kEpiWarps + 2;
   constexpr int kGroupWarps = 4 * S::kColParts;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -299,7 +307,7 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
   // (the registers move within the roles' branches: code that both reach would
   // have to do with the fewer)
   if (warp >= kEpiWarps) {
-    give_registers<kOtherRegs>();
+    give_registers<S::kOtherRegs>();
     if (warp == kProducerWarp) {
       // ------------------------------------------------------------ TMA producer (both CTAs of a pair)
       pdl_wait();
@@ -321,17 +329,22 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
         place(t, &lt, &ct);
         const int l0 = lt * S::kTileL + half * kLanes, c0 = ct * kBN + half * S::kCLoad;
 #pragma unroll 1
-        for (int kb = k0; kb < k1; ++kb) {
+        for (int kb = k0; kb < k1; kb += kPairK) {
           ok = mbar_wait_warp(empty0 + stage * 8, phase ^ 1, a.err, abort_flag);
           if (!ok) break;
-          const uint32_t dst = smem0 + stage * S::kStageBytes;
-          if (half == 0) mbar_arrive_expect_tx_if(elected, full0 + stage * 8, bytes);
-          if constexpr (kPairs) {
-            tma_load_2d_pair_if(elected, dst, &tmap_l, leader0 + stage * 8, kb * kBK, l0, pol_l);
-            tma_load_2d_pair_if(elected, dst + kLTile, &tmap_c, leader0 + stage * 8, kb * kBK, c0, pol_c);
-          } else {
-            tma_load_2d_if(elected, dst, &tmap_l, full0 + stage * 8, kb * kBK, l0, pol_l);
-            tma_load_2d_if(elected, dst + kLTile, &tmap_c, full0 + stage * 8, kb * kBK, c0, pol_c);
+          const int blocks = min(kPairK, k1 - kb);
+          if (half == 0) mbar_arrive_expect_tx_if(elected, full0 + stage * 8, blocks * bytes);
+          uint32_t dst = smem0 + stage * S::kStageBytes;
+#pragma unroll
+          for (int i = 0; i < kPairK; ++i, dst += S::kBlockBytes) {
+            if (i >= blocks) break;
+            if constexpr (kPairs) {
+              tma_load_2d_pair_if(elected, dst, &tmap_l, leader0 + stage * 8, (kb + i) * kBK, l0, pol_l);
+              tma_load_2d_pair_if(elected, dst + kLTile, &tmap_c, leader0 + stage * 8, (kb + i) * kBK, c0, pol_c);
+            } else {
+              tma_load_2d_if(elected, dst, &tmap_l, full0 + stage * 8, (kb + i) * kBK, l0, pol_l);
+              tma_load_2d_if(elected, dst + kLTile, &tmap_c, full0 + stage * 8, (kb + i) * kBK, c0, pol_c);
+            }
           }
           ++n_issued;
           if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -352,37 +365,52 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
       const uint32_t full0 = smem_u32(full_bar), empty0 = smem_u32(empty_bar);
       const uint32_t tfull0 = smem_u32(tfull_bar), tempty0 = smem_u32(tempty_bar);
       int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
+      uint32_t phase = 0, buf_phase = 0, stage_seen = 0, buf_seen = 0;
       bool ok = true;
 #pragma unroll 1
       for (int t = first; ok && t < a.n_tiles; t += step) {
 #pragma unroll 1
-        for (int kb = k0; kb < k1; ++kb) {
+        for (int kb = k0; kb < k1; kb += kPairK) {
           const int pos = (kb - k0) % kPer;                // within the buffer
-          ok = (pos > 0 || mbar_wait_warp(tempty0 + buf * 8, buf_phase ^ 1, a.err, abort_flag)) &&
-               mbar_wait_warp(full0 + stage * 8, phase, a.err, abort_flag);
+          // (a barrier takes 100 clocks and more to look at: kThin looks at the next
+          // ones before this stage's MMAs are issued, in the other forms the epilogue
+          // waits for these MMAs)
+          ok = (pos > 0 || (kSwap && __all_sync(0xffffffffu, buf_seen)) ||
+                mbar_wait_warp(tempty0 + buf * 8, buf_phase ^ 1, a.err, abort_flag)) &&
+               ((kSwap && __all_sync(0xffffffffu, stage_seen)) || mbar_wait_warp(full0 + stage * 8, phase, a.err, abort_flag));
           if (!ok) break;
           tc_fence_after();
+          const int blocks = min(kPairK, k1 - kb);
+          const bool last = pos + kPairK >= kPer || kb + kPairK >= k1;
           const uint64_t l_desc = l_desc0 + stage * (S::kStageBytes >> 4);
           const uint64_t c_desc = c_desc0 + stage * (S::kStageBytes >> 4);
           const uint32_t d_tmem = tmem_base + (buf * kPer + pos) * kBN;
-#pragma unroll
-          for (int k = 0; k < kBK / 32; ++k) {
-            if constexpr (kPairs)
-              mma_fp8_pair_if(elected, d_tmem, l_desc + k * 2, c_desc + k * 2, idesc, k > 0);
-            else
-              mma_fp8_if(elected, d_tmem, l_desc + k * 2, c_desc + k * 2, idesc, k > 0);
-          }
-          const bool last = pos == kPer - 1 || kb + 1 == k1;
-          if constexpr (kPairs) {
-            mma_commit_pair_multicast_if(elected, empty0 + stage * 8, both);
-            if (last) mma_commit_pair_multicast_if(elected, tfull0 + buf * 8, both);
-          } else {
-            mma_commit_if(elected, empty0 + stage * 8);
-            if (last) mma_commit_if(elected, tfull0 + buf * 8);
-          }
+          const uint32_t empty = empty0 + stage * 8, tfull = tfull0 + buf * 8;
           if (++stage == kStages) { stage = 0; phase ^= 1; }
           if (last && ++buf == kBufs) { buf = 0; buf_phase ^= 1; }
+          if constexpr (kSwap) {
+            stage_seen = mbar_test(full0 + stage * 8, phase);
+            if (last) buf_seen = mbar_test(tempty0 + buf * 8, buf_phase ^ 1);
+          }
+#pragma unroll
+          for (int i = 0; i < kPairK; ++i) {
+            if (i >= blocks) break;
+#pragma unroll
+            for (int k = 0; k < kBK / 32; ++k) {
+              constexpr int kNext = S::kBlockBytes >> 4;
+              if constexpr (kPairs)
+                mma_fp8_pair_if(elected, d_tmem + i * kBN, l_desc + i * kNext + k * 2, c_desc + i * kNext + k * 2, idesc, k > 0);
+              else
+                mma_fp8_if(elected, d_tmem + i * kBN, l_desc + i * kNext + k * 2, c_desc + i * kNext + k * 2, idesc, k > 0);
+            }
+          }
+          if constexpr (kPairs) {
+            mma_commit_pair_multicast_if(elected, empty, both);
+            if (last) mma_commit_pair_multicast_if(elected, tfull, both);
+          } else {
+            mma_commit_if(elected, empty);
+            if (last) mma_commit_if(elected, tfull);
+          }
         }
       }
       if (!ok) {
@@ -441,7 +469,7 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    take_registers<kEpiRegs>();
+    take_registers<S::kEpiRegs>();
     const int quad = warp & 3;                             // TMEM lane quarter
     const int part = (warp >> 2) % S::kColParts;           // columns
     const int group = (warp >> 2) / S::kColParts;          // every kGroups-th tile
@@ -500,22 +528,21 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
 #pragma unroll
       for (int c = 0; c < kLoads * kRegs / 2; ++c) sum[c] = 0ull;
       uint32_t use = static_cast<uint32_t>(tile) * n_use, fill = static_cast<uint32_t>(tile) * n_fill;
-#pragma unroll 1
-      for (int kb = k0; kb < k1; ++kb) {
-        const int pos = (kb - k0) % kPer, at = (kb - k0) % kAhead;
-        if (at == 0) {
-          ok = mbar_wait(&sfull_bar[fill % kSlots], (fill / kSlots) & 1, a.err, abort_flag);
-          if (!ok) break;
+      uint32_t sums[S::kTwoBlocks ? 2 : 1][kLoads][kRegs];     // of two blocks, in turn, or of one
+      // Waits for block kb's sums and scales and begins to load the sums.
+      auto begin = [&](int kb, uint32_t (&r)[kLoads][kRegs]) {
+        const int pos = (kb - k0) % kPer;
+        if ((kb - k0) % kAhead == 0) {
+          const uint32_t n = static_cast<uint32_t>(tile) * n_fill + (kb - k0) / kAhead;
+          if (!mbar_wait(&sfull_bar[n % kSlots], (n / kSlots) & 1, a.err, abort_flag)) return false;
         }
         if (pos == 0) {
-          ok = mbar_wait(&tfull_bar[use % kBufs], (use / kBufs) & 1, a.err, abort_flag);
-          if (!ok) break;
+          if (!mbar_wait(&tfull_bar[use % kBufs], (use / kBufs) & 1, a.err, abort_flag)) return false;
           __syncwarp();
           tc_fence_after();
         }
-        uint32_t r[kLoads][kRegs];
-        const uint32_t from = lane_addr + (use % kBufs * kPer + pos) * kBN;
         if (live) {
+          const uint32_t from = lane_addr + (use % kBufs * kPer + pos) * kBN;
 #pragma unroll
           for (int q = 0; q < kLoads; ++q) {
             if constexpr (kColScales)
@@ -524,18 +551,11 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
               tmem_ld_32(from + kCols * q, r[q]);
           }
         }
-        // the factors of this block: of the thread's rows and columns
-        const float* lane_scales = scales + (fill % kSlots * kAhead + at) * S::kScaleWords;
-        const float* col_scales = lane_scales + kLanes;
-        float f[kLaneScales && kColScales ? 4 : 1];
-        if constexpr (kLaneScales && kColScales) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] = lane_scales[quad * 32 + 8 * i + (lane >> 2)];
-        } else if constexpr (kLaneScales) {
-          f[0] = lane_scales[quad * 32 + lane] * col_scales[part];
-        } else {
-          f[0] = lane_scales[0];
-        }
+        return true;
+      };
+      // Adds block kb's sums, while the next block's are loaded where there are registers for them.
+      auto finish = [&](int kb, uint32_t (&r)[kLoads][kRegs], uint32_t (&r_next)[kLoads][kRegs]) {
+        const int pos = (kb - k0) % kPer, at = (kb - k0) % kAhead;
         if (live) {
 #pragma unroll
           for (int q = 0; q < kLoads; ++q) tmem_ld_wait_for(r[q]);
@@ -551,7 +571,21 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
           }
           ++use;
         }
+        bool there = true;
+        if (S::kTwoBlocks && kb + 1 < k1) there = begin(kb + 1, r_next);
         if (live) {
+          // the factors of this block: of the thread's rows and columns
+          const float* lane_scales = scales + (fill % kSlots * kAhead + at) * S::kScaleWords;
+          const float* col_scales = lane_scales + kLanes;
+          float f[kLaneScales && kColScales ? 4 : 1];
+          if constexpr (kLaneScales && kColScales) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = lane_scales[quad * 32 + 8 * i + (lane >> 2)];
+          } else if constexpr (kLaneScales) {
+            f[0] = lane_scales[quad * 32 + lane] * col_scales[part];
+          } else {
+            f[0] = lane_scales[0];
+          }
           f32x2 w[kColScales ? kCols / 8 : 1];
 #pragma unroll
           for (int q = 0; q < kLoads; ++q) {
@@ -585,6 +619,14 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
           if (lane == 0) mbar_arrive(&sempty_bar[fill % kSlots]);
           ++fill;
         }
+        if (!S::kTwoBlocks && kb + 1 < k1) there = begin(kb + 1, r_next);
+        return there;
+      };
+      ok = begin(k0, sums[0]);
+#pragma unroll 1
+      for (int kb = k0; ok && kb < k1; kb += S::kTwoBlocks ? 2 : 1) {
+        ok = finish(kb, sums[0], sums[S::kTwoBlocks ? 1 : 0]);
+        if (S::kTwoBlocks && ok && kb + 1 < k1) ok = finish(kb + 1, sums[S::kTwoBlocks ? 1 : 0], sums[0]);
       }
       if (!ok) break;
       __syncwarp();
@@ -752,13 +794,13 @@ cudaError_t launch(Args a, const Fp8Matrix& ma, const Fp8Matrix& mb, int64_t m, 
       cudaFuncAttributes attr = {};
       return cudaFuncGetAttributes(&attr, fn) == cudaSuccess ? attr.numRegs : 0;
     }();
-    if (regs != kLaunchRegs) return cudaErrorInvalidDeviceFunction;
+    if (regs != S::kLaunchRegs) return cudaErrorInvalidDeviceFunction;
   }
   if (e != cudaSuccess) return e;
   const int cluster = S::kCtas * (kSplit ? a.splits : 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas * cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

@@ -63,6 +63,20 @@ __device__ __forceinline__ void tma_load_2d_if(uint32_t elected, uint32_t smem_d
       : "memory");
 }
 
+// Whether the phase with this parity has completed, without waiting: a look ahead
+// at a barrier that is needed next.
+__device__ __forceinline__ uint32_t mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+
 // Waits for the TMEM loads issued so far.  The registers that they write are
 // operands, so that no use of them is moved ahead of the wait.
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16]) {

@@ -702,29 +702,34 @@ def clip_grad_norm(grads, max_norm, out=None, norm_type=2.0, stream=None):
 _TYPES = {}
 
 
-def _type_of(dtype):
-    """FS_TYPE_* of a torch type, or None."""
+def _types():
+    """FS_TYPE_* by torch type."""
     if not _TYPES:
         torch = _torch()
         _TYPES.update({torch.float32: FS_TYPE_F32, torch.bfloat16: FS_TYPE_BF16, torch.float16: FS_TYPE_F16,
                        torch.float8_e4m3fn: FS_TYPE_E4M3, torch.float8_e5m2: FS_TYPE_E5M2})
-    return _TYPES.get(dtype)
+    return _TYPES
+
+
+_WIDE = (FS_TYPE_F32, FS_TYPE_BF16, FS_TYPE_F16)
+_FP8 = (FS_TYPE_E4M3, FS_TYPE_E5M2)
 
 
 def _rows(t, name, types, shape=None):
-    """(address, FS_TYPE_*, row stride) of a CUDA matrix of one of these types
-    whose rows are contiguous."""
+    """(address, FS_TYPE_*, rows, columns, row stride) of a CUDA matrix of one
+    of these types whose rows are contiguous."""
     try:
-        kind = _type_of(t.dtype)
-        if t.is_cuda and kind in types and t.dim() == 2 and (shape is None or t.shape == shape):
+        kind = (_TYPES or _types()).get(t.dtype)
+        rows, cols = t.shape
+        if kind in types and t.is_cuda and (shape is None or (rows, cols) == shape):
             rs, cs = t.stride()
-            if cs == 1 or t.shape[1] <= 1:
-                return t.data_ptr(), kind, (rs if t.shape[0] > 1 else max(rs, t.shape[1]))
-    except AttributeError:
+            if cs == 1 or cols <= 1:
+                return t.data_ptr(), kind, rows, cols, rs if rows > 1 else max(rs, cols)
+    except (AttributeError, ValueError):
         pass
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be a CUDA tensor (no CPU fallback)")
-    if _type_of(t.dtype) not in types:
+    if _types().get(t.dtype) not in types:
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must not be {t.dtype}")
     if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be {'a matrix' if shape is None else tuple(shape)}, "
@@ -732,43 +737,67 @@ def _rows(t, name, types, shape=None):
     raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must have contiguous rows")
 
 
-_WIDE = (FS_TYPE_F32, FS_TYPE_BF16, FS_TYPE_F16)
-_FP8 = (FS_TYPE_E4M3, FS_TYPE_E5M2)
-
-
 def _fp8_rows(q, name, types, shape=None):
     """``_rows`` of an 8-bit matrix: the library wants rows that lie a multiple
     of 16 bytes apart, and a single row is as good as one."""
-    at, kind, stride = _rows(q, name, types, shape)
-    return at, kind, stride if q.shape[0] > 1 else (stride + 15) // 16 * 16
+    at, kind, rows, cols, stride = _rows(q, name, types, shape)
+    return at, kind, rows, cols, stride if rows > 1 else (stride + 15) // 16 * 16
 
 
 def _scale_args(scale, name, rows, cols):
     """(address, row stride, column stride, rows of a block) of the scales of
     an 8-bit [rows, cols]."""
+    cb = (cols + 127) // 128
+    try:
+        if scale.is_cuda and scale.dtype is _torch().float32:
+            shape = scale.shape
+            if shape == (rows, cb):
+                return scale.data_ptr(), *scale.stride(), 1
+            if shape == ((rows + 127) // 128, cb):
+                return scale.data_ptr(), *scale.stride(), 128
+    except AttributeError:
+        pass
     torch = _torch()
     if not isinstance(scale, torch.Tensor) or not scale.is_cuda or scale.dtype != torch.float32:
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be a float32 CUDA tensor (no CPU fallback)")
-    cb = -(-cols // 128)
-    if scale.shape == (rows, cb):
-        block = 1
-    elif scale.shape == (-(-rows // 128), cb):
-        block = 128
-    else:
-        raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be [{rows}, {cb}] or [{-(-rows // 128)}, {cb}], "
-                               f"got {tuple(scale.shape)}")
-    return scale.data_ptr(), scale.stride(0), scale.stride(1), block
+    raise FlashSampleError("FS_ERR_INVALID_ARG", f"{name} must be [{rows}, {cb}] or [{-(-rows // 128)}, {cb}], "
+                           f"got {tuple(scale.shape)}")
 
 
-def _fp8_empty(rows, cols, block_rows, dtype, device, stream):
-    """q [rows, cols] in rows of whole 16 bytes, and its scales: those of single
-    rows side by side for a block, as the products read them fastest."""
+def _fp8_out(rows, cols, block_rows, dtype, device, out, stream):
+    """(q, scale, address, FS_TYPE_*, row stride, the scales' address and
+    strides): ``out``, or new ones: rows of whole 16 bytes, and the scales of
+    single rows side by side for a block, as the products read them fastest."""
+    kind = (_TYPES or _types()).get(dtype)
+    if kind not in _FP8:
+        raise FlashSampleError("FS_ERR_INVALID_ARG", f"dtype must be float8_e4m3fn or float8_e5m2, got {dtype}")
+    rb, cb = (rows if block_rows == 1 else (rows + 127) // 128), (cols + 127) // 128
+    if out is not None:
+        q, scale = out
+        at, kind, _, _, stride = _fp8_rows(q, "q", _FP8, (rows, cols))
+        s_at, s_row, s_col, _ = _scale_args(scale, "scale", rows, cols)
+        if scale.shape[0] != rb:
+            raise FlashSampleError("FS_ERR_INVALID_ARG", f"scale must have {rb} rows")
+        return q, scale, at, kind, stride, s_at, s_row, s_col
     torch = _torch()
-    rb, cb, pitch = -(-rows // block_rows), -(-cols // 128), (cols + 15) // 16 * 16
-    q, scale = _made_on(stream, device, lambda: (
-        torch.empty((rows, pitch), dtype=dtype, device=device),
-        torch.empty((cb, rb) if block_rows == 1 else (rb, cb), dtype=torch.float32, device=device)))
-    return (q[:, :cols] if pitch != cols else q), (scale.t() if block_rows == 1 else scale)
+    stride = (cols + 15) // 16 * 16
+    s_row, s_col = (1, rb) if block_rows == 1 else (cb, 1)
+    if stream is None:
+        q = torch.empty_strided((rows, cols), (stride, 1), dtype=dtype, device=device)
+        scale = torch.empty_strided((rb, cb), (s_row, s_col), dtype=torch.float32, device=device)
+    else:
+        q, scale = _made_on(stream, device, lambda: (
+            torch.empty_strided((rows, cols), (stride, 1), dtype=dtype, device=device),
+            torch.empty_strided((rb, cb), (s_row, s_col), dtype=torch.float32, device=device)))
+    return q, scale, q.data_ptr(), kind, stride, scale.data_ptr(), s_row, s_col
+
+
+def _new(shape, dtype, device, stream):
+    """A tensor for a call that writes it on ``stream``."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _made_on(stream, device, lambda: (torch.empty(shape, dtype=dtype, device=device),))[0]
 
 
 def quantize_fp8(x, block_rows=1, dtype=None, transpose=False, out=None, stream=None):
@@ -782,20 +811,12 @@ def quantize_fp8(x, block_rows=1, dtype=None, transpose=False, out=None, stream=
     contiguous where C is one; the scales of single rows are a transposed
     view.  Hidden states are quantised by rows, weights in blocks of 128 x
     128 (``block_rows=128``), once."""
-    torch = _torch()
-    dtype = torch.float8_e4m3fn if dtype is None else dtype
-    ptr, kind, stride = _rows(x, "x", _WIDE)
-    rows, cols = x.shape
-    R, C = (cols, rows) if transpose else (rows, cols)
+    ptr, kind, rows, cols, stride = _rows(x, "x", _WIDE)
     if block_rows not in (1, 128):
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"block_rows must be 1 or 128, got {block_rows}")
-    if _type_of(dtype) not in _FP8:
-        raise FlashSampleError("FS_ERR_INVALID_ARG", f"dtype must be float8_e4m3fn or float8_e5m2, got {dtype}")
-    q, scale = out if out is not None else _fp8_empty(R, C, block_rows, dtype, x.device, stream)
-    q_ptr, q_kind, q_stride = _fp8_rows(q, "q", _FP8, (R, C))
-    s_ptr, s_row, s_col, _ = _scale_args(scale, "scale", R, C)
-    if scale.shape[0] != -(-R // block_rows):
-        raise FlashSampleError("FS_ERR_INVALID_ARG", f"scale must have {-(-R // block_rows)} rows")
+    R, C = (cols, rows) if transpose else (rows, cols)
+    q, scale, *to = _fp8_out(R, C, block_rows, _torch().float8_e4m3fn if dtype is None else dtype, x.device, out, stream)
+    q_ptr, q_kind, q_stride, s_ptr, s_row, s_col = to
     check(library().fs_quantize_fp8(ptr, kind, rows, cols, stride, 1 if transpose else 0, block_rows, q_kind, q_ptr, q_stride,
                                     s_ptr, s_row, s_col, _stream_of(x, stream)))
     return q, scale
@@ -805,10 +826,8 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
     """a bᵀ of two 8-bit matrices: a [m, k] quantised by rows, b [n, k] by rows
     or in blocks of 128 x 128 (told by the shape of its scales).  Returns
     [m, n] of ``out_dtype`` (bf16 by default; fp32 or fp16), or writes ``out``."""
-    torch = _torch()
-    a_ptr, a_kind, a_stride = _fp8_rows(a, "a", _FP8)
-    b_ptr, b_kind, b_stride = _fp8_rows(b, "b", _FP8)
-    (m, k), (n, k2) = a.shape, b.shape
+    a_ptr, a_kind, m, k, a_stride = _fp8_rows(a, "a", _FP8)
+    b_ptr, b_kind, n, k2, b_stride = _fp8_rows(b, "b", _FP8)
     if k != k2:
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"a must be [m, k] and b [n, k], got {tuple(a.shape)} and {tuple(b.shape)}")
     as_ptr, as_row, as_col, _ = _scale_args(a_scale, "a_scale", m, k)
@@ -816,10 +835,10 @@ def fp8_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"a_scale must have a row for each of a's {m}")
     bs_ptr, bs_row, bs_col, block = _scale_args(b_scale, "b_scale", n, k)
     if out is None:
-        out, = _made_on(stream, a.device, lambda: (torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=a.device),))
+        out = _new((m, n), out_dtype or _torch().bfloat16, a.device, stream)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise FlashSampleError("FS_ERR_INVALID_ARG", f"out must be {out_dtype}, got {out.dtype}")
-    o_ptr, o_kind, o_stride = _rows(out, "out", _WIDE, (m, n))
+    o_ptr, o_kind, _, _, o_stride = _rows(out, "out", _WIDE, (m, n))
     check(library().fs_fp8_matmul(a_ptr, a_kind, a_stride, as_ptr, as_row, as_col, b_ptr, b_kind, b_stride, bs_ptr, bs_row,
                                   bs_col, block, m, n, k, o_ptr, o_kind, o_stride, _stream_of(a, stream)))
     return out
@@ -831,9 +850,8 @@ def sample_fp8(h, h_scale, W, W_scale, temp, seed, step, bias=None, out=None, st
     or in blocks of 128 x 128 (``quantize_fp8(W, block_rows=128)``, once).
     Reads half the bytes of a bf16 head.  Returns (ids int64 [B], max fp32 [B])."""
     torch = _torch()
-    h_ptr, _, h_stride = _fp8_rows(h, "h", (FS_TYPE_E4M3,))
-    W_ptr, _, W_stride = _fp8_rows(W, "W", (FS_TYPE_E4M3,))
-    (B, d), (V, d2) = h.shape, W.shape
+    h_ptr, _, B, d, h_stride = _fp8_rows(h, "h", (FS_TYPE_E4M3,))
+    W_ptr, _, V, d2, W_stride = _fp8_rows(W, "W", (FS_TYPE_E4M3,))
     if d != d2:
         raise FlashSampleError("FS_ERR_INVALID_ARG", "h must be [B, d] and W [V, d]")
     hs_ptr, hs_row, hs_col, _ = _scale_args(h_scale, "h_scale", B, d)
@@ -853,22 +871,23 @@ def sample_fp8(h, h_scale, W, W_scale, temp, seed, step, bias=None, out=None, st
     return ids, mx
 
 
-def _vector(t, name, d, dtype):
-    """Address of a weight or bias: None, or [d] in fp32 or in x's type."""
-    if t is None:
-        return None
-    torch = _torch()
-    return _arg(t, name, torch.float32 if getattr(t, "dtype", None) == torch.float32 else dtype, (d,))
-
-
 def _norm_args(x, weight, bias):
-    ptr, kind, stride = _rows(x, "x", _WIDE)
-    d = x.shape[1]
-    w, b = _vector(weight, "weight", d, x.dtype), _vector(bias, "bias", d, x.dtype)
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise FlashSampleError("FS_ERR_INVALID_ARG", f"weight and bias must have one type, got {weight.dtype} and {bias.dtype}")
-    w_kind = FS_TYPE_F32 if weight is None and bias is None else _type_of((bias if weight is None else weight).dtype)
-    return ptr, kind, x.shape[0], d, stride, w, b, w_kind
+    """x's ``_rows``, then the addresses and FS_TYPE_* of weight and bias:
+    None, or [d] in one type, fp32 or x's."""
+    ptr, kind, n, d, stride = _rows(x, "x", _WIDE)
+    w = b = None
+    w_kind = FS_TYPE_F32
+    torch = _torch()
+    if weight is not None:
+        dtype = torch.float32 if getattr(weight, "dtype", None) is torch.float32 else x.dtype
+        w, w_kind = _arg(weight, "weight", dtype, (d,)), _TYPES[dtype]
+    if bias is not None:
+        dtype = torch.float32 if getattr(bias, "dtype", None) is torch.float32 else x.dtype
+        b = _arg(bias, "bias", dtype, (d,))
+        if weight is not None and _TYPES[dtype] != w_kind:
+            raise FlashSampleError("FS_ERR_INVALID_ARG", f"weight and bias must have one type, got {weight.dtype} and {bias.dtype}")
+        w_kind = _TYPES[dtype]
+    return ptr, kind, n, d, stride, w, b, w_kind
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=None):
@@ -880,12 +899,14 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=
     included.  d <= 32768."""
     torch = _torch()
     ptr, kind, n, d, stride, w, b, w_kind = _norm_args(x, weight, bias)
-    stats = _made_on(stream, x.device, lambda: tuple(torch.empty(n, dtype=torch.float32, device=x.device)
-                                                     for _ in range(1 if rms else 2)))
+    device = x.device
+    mean = None if rms else _new(n, torch.float32, device, stream)
+    rstd = _new(n, torch.float32, device, stream)
     if out is None:
-        out, = _made_on(stream, x.device, lambda: (torch.empty((n, d), dtype=x.dtype, device=x.device),))
-    y_ptr, y_kind, y_stride = _rows(out, "out", (kind,), (n, d))
-    mean, rstd = (None, stats[0]) if rms else stats
+        out = _new((n, d), x.dtype, device, stream)
+        y_ptr, y_stride = out.data_ptr(), d
+    else:
+        y_ptr, _, _, _, y_stride = _rows(out, "out", (kind,), (n, d))
     check(library().fs_layer_norm(ptr, kind, n, d, stride, w, b, w_kind, 1 if rms else 0, eps, y_ptr, y_stride,
                                   None if rms else mean.data_ptr(), rstd.data_ptr(), None, 0, 0, None, 0, 0,
                                   _stream_of(x, stream)))
@@ -896,16 +917,9 @@ def layer_norm_fp8(x, weight=None, bias=None, eps=1e-5, rms=False, dtype=None, o
     """``layer_norm`` whose result is quantised by rows from its fp32 values, in
     the same pass: returns (q [n, d], scale [n, ceil(d / 128)]) as
     ``quantize_fp8`` does, for ``fp8_matmul`` and ``sample_fp8``."""
-    torch = _torch()
-    dtype = torch.float8_e4m3fn if dtype is None else dtype
     ptr, kind, n, d, stride, w, b, w_kind = _norm_args(x, weight, bias)
-    if _type_of(dtype) not in _FP8:
-        raise FlashSampleError("FS_ERR_INVALID_ARG", f"dtype must be float8_e4m3fn or float8_e5m2, got {dtype}")
-    q, scale = out if out is not None else _fp8_empty(n, d, 1, dtype, x.device, stream)
-    q_ptr, q_kind, q_stride = _fp8_rows(q, "q", _FP8, (n, d))
-    s_ptr, s_row, s_col, _ = _scale_args(scale, "scale", n, d)
-    if scale.shape[0] != n:
-        raise FlashSampleError("FS_ERR_INVALID_ARG", f"scale must have {n} rows")
+    q, scale, *to = _fp8_out(n, d, 1, _torch().float8_e4m3fn if dtype is None else dtype, x.device, out, stream)
+    q_ptr, q_kind, q_stride, s_ptr, s_row, s_col = to
     check(library().fs_layer_norm(ptr, kind, n, d, stride, w, b, w_kind, 1 if rms else 0, eps, None, 0, None, None, q_ptr,
                                   q_kind, q_stride, s_ptr, s_row, s_col, _stream_of(x, stream)))
     return q, scale
@@ -925,27 +939,28 @@ def layer_norm_backward(grad, x, weight, mean, rstd, need_x=True, need_weight=Tr
     ``weight_dtype``: the type of the two sums where weight is None (fp32).
     ``out``: the tensor for grad_x, ``grad`` itself included."""
     torch = _torch()
-    x_ptr, kind, x_stride = _rows(x, "x", _WIDE)
-    n, d = x.shape
-    g_ptr, _, g_stride = _rows(grad, "grad", (kind,), (n, d))
-    w = _vector(weight, "weight", d, x.dtype)
-    w_dtype = weight.dtype if weight is not None else weight_dtype or torch.float32
-    if w_dtype not in (torch.float32, x.dtype):
-        raise FlashSampleError("FS_ERR_INVALID_ARG", f"weight_dtype must be float32 or {x.dtype}, got {w_dtype}")
+    x_ptr, kind, n, d, x_stride, w, _, w_kind = _norm_args(x, weight, None)
+    g_ptr, _, _, _, g_stride = _rows(grad, "grad", (kind,), (n, d))
+    if weight is None and weight_dtype is not None:
+        w_kind = _TYPES.get(weight_dtype)
+        if weight_dtype not in (torch.float32, x.dtype):
+            raise FlashSampleError("FS_ERR_INVALID_ARG", f"weight_dtype must be float32 or {x.dtype}, got {weight_dtype}")
+    w_dtype = torch.float32 if w_kind == FS_TYPE_F32 else x.dtype
+    device, f32 = x.device, torch.float32
     gx_ptr, gx_stride, gx = None, 0, None
     if need_x:
-        gx = out if out is not None else _made_on(stream, x.device,
-                                                  lambda: (torch.empty((n, d), dtype=x.dtype, device=x.device),))[0]
-        gx_ptr, _, gx_stride = _rows(gx, "out", (kind,), (n, d))
-    sums = _made_on(stream, x.device, lambda: tuple(torch.empty(d, dtype=w_dtype, device=x.device)
-                                                    for _ in range(int(need_weight) + int(need_bias))))
-    gw = sums[0] if need_weight else None
-    gb = sums[-1] if need_bias else None
-    nbytes = _norm_grad_bytes(n, d) if sums else 0
-    work, where = _workspace(nbytes, x.device, stream)
-    f32 = torch.float32
+        if out is None:
+            gx = _new((n, d), x.dtype, device, stream)
+            gx_ptr, gx_stride = gx.data_ptr(), d
+        else:
+            gx = out
+            gx_ptr, _, _, _, gx_stride = _rows(gx, "out", (kind,), (n, d))
+    gw = _new(d, w_dtype, device, stream) if need_weight else None
+    gb = _new(d, w_dtype, device, stream) if need_bias else None
+    nbytes = _norm_grad_bytes(n, d) if need_weight or need_bias else 0
+    work, where = _workspace(nbytes, device, stream)
     check(library().fs_layer_norm_backward(
-        g_ptr, g_stride, x_ptr, kind, n, d, x_stride, w, _type_of(w_dtype), 1 if mean is None else 0,
+        g_ptr, g_stride, x_ptr, kind, n, d, x_stride, w, w_kind, 1 if mean is None else 0,
         None if mean is None else _arg(mean, "mean", f32, (n,)), _arg(rstd, "rstd", f32, (n,)), gx_ptr, gx_stride,
         None if gw is None else gw.data_ptr(), None if gb is None else gb.data_ptr(), where, nbytes, _stream_of(x, stream)))
     return gx, gw, gb

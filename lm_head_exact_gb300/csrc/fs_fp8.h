@@ -92,10 +92,10 @@ struct NormGradProblem {
   int64_t gx_stride;
   void* gw;                 // nullable [d] of w_type
   void* gb;                 // nullable [d] of w_type
-  float* partials;          // norm_grad_blocks() x 2 x d
+  float* partials;          // norm_grad_blocks(n) x 2 x d
 };
-// Blocks that each leave one partial sum of the weight's and bias's gradients.
-int64_t norm_grad_blocks(int64_t n, int64_t d);
+// Blocks, at most, that each leave one partial sum of the weight's and bias's gradients.
+int64_t norm_grad_blocks(int64_t n);
 cudaError_t launch_norm_grad(const NormGradProblem& p, cudaStream_t stream);
 
 constexpr int64_t kNormMaxWidth = 32768;

@@ -215,7 +215,7 @@ fs_status fs_layer_norm(const void* x, int x_type, int64_t n, int64_t d, int64_t
 }
 
 size_t fs_layer_norm_backward_workspace_bytes(int64_t n, int64_t d) {
-  return n <= 0 || d <= 0 || d > kNormMaxWidth ? 0 : static_cast<size_t>(norm_grad_blocks(n, d)) * 2 * d * sizeof(float);
+  return n <= 0 || d <= 0 || d > kNormMaxWidth ? 0 : static_cast<size_t>(norm_grad_blocks(n)) * 2 * d * sizeof(float);
 }
 
 fs_status fs_layer_norm_backward(const void* g, int64_t g_row_stride, const void* x, int x_type, int64_t n, int64_t d,

@@ -19,18 +19,33 @@ namespace {
 constexpr int kSmallRow = 32;              // threads of a row that one warp takes
 constexpr int kRowsPerBlock = 8;           // rows (warps) of a block of such
 
-// kV elements from p (16-byte aligned where kV > 1).
+// kV elements as they lie in memory: 16 aligned bytes, or one element.
 template <typename T, int kV>
-__device__ __forceinline__ void load_group(const T* p, float (&v)[kV]) {
-  if constexpr (kV == 1) {
-    v[0] = to_float<T>(*p);
+struct Group {
+  uint4 raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&v)[kV]) const { unpack<T>(raw, v); }
+};
+template <typename T>
+struct Group<T, 1> {
+  T raw;
+  __device__ __forceinline__ void load(const T* p) { raw = *p; }
+  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = to_float<T>(raw); }
+};
+
+// kV weights from p, with 16-byte loads where they are aligned.
+template <typename W, int kV>
+__device__ __forceinline__ void load_weights(const W* p, float (&v)[kV]) {
+  if constexpr (kV < kVec<W>) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[j] = to_float<W>(p[j]);
   } else {
 #pragma unroll
-    for (int h = 0; h < kV; h += kVec<T>) {
-      float part[kVec<T>];
-      unpack<T>(*reinterpret_cast<const uint4*>(p + h), part);
+    for (int h = 0; h < kV; h += kVec<W>) {
+      float part[kVec<W>];
+      unpack<W>(*reinterpret_cast<const uint4*>(p + h), part);
 #pragma unroll
-      for (int j = 0; j < kVec<T>; ++j) v[h + j] = part[j];
+      for (int j = 0; j < kVec<W>; ++j) v[h + j] = part[j];
     }
   }
 }
@@ -41,6 +56,29 @@ __device__ __forceinline__ void store_group(T* p, const float (&v)[kV]) {
     *p = from_float<T>(v[0]);
   else
     *reinterpret_cast<uint4*>(p) = pack<T>(v);
+}
+
+// The same of a row's columns c .. c + kV - 1, of which only those in [0, d) exist.
+template <typename T, int kV>
+__device__ __forceinline__ void store_some(T* row, int c, int d, const float (&v)[kV]) {
+  if (c >= 0 && c + kV <= d) {
+    store_group<T, kV>(row + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+      if (c + j >= 0 && c + j < d) row[c + j] = from_float<T>(v[j]);
+  }
+}
+template <typename W, int kV>
+__device__ __forceinline__ void load_some(const W* p, int c, int d, float otherwise, float (&v)[kV]) {
+#pragma unroll
+  for (int j = 0; j < kV; ++j) v[j] = c + j >= 0 && c + j < d ? to_float<W>(p[c + j]) : otherwise;
+}
+
+// Elements from a 16-byte boundary to p.
+template <typename T>
+__device__ __forceinline__ int shift_of(const T* p) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -89,7 +127,9 @@ __global__ void __launch_bounds__(kOneWarp ? kSmallRow* kRowsPerBlock : 1024) no
   for (int i = 0; i < kN; ++i) {
     const int c = (i * threads + t) * kV;
     if (c < d) {
-      load_group<T, kV>(x + c, v[i]);
+      Group<T, kV> g;
+      g.load(x + c);
+      g.get(v[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < kV; ++j) v[i][j] = 0.0f;
@@ -134,40 +174,57 @@ __global__ void __launch_bounds__(kOneWarp ? kSmallRow* kRowsPerBlock : 1024) no
         w[j] = 1.0f;
         b[j] = 0.0f;
       }
-      if (p.weight != nullptr) load_group<W, kV>(static_cast<const W*>(p.weight) + c, w);
-      if (p.bias != nullptr) load_group<W, kV>(static_cast<const W*>(p.bias) + c, b);
+      if (p.weight != nullptr) load_weights<W, kV>(static_cast<const W*>(p.weight) + c, w);
+      if (p.bias != nullptr) load_weights<W, kV>(static_cast<const W*>(p.bias) + c, b);
 #pragma unroll
       for (int j = 0; j < kV; ++j) v[i][j] = fmaf(v[i][j] * rstd, w[j], b[j]);
     }
-    if constexpr (!kQuant) {
-      store_group<T, kV>(static_cast<T*>(p.y) + row * p.y_stride + c, v[i]);
-    } else if constexpr (kV > 1) {
-      // 128 columns are 16 lanes (8 elements each) or 32 (4 each)
+    if constexpr (!kQuant) store_group<T, kV>(static_cast<T*>(p.y) + row * p.y_stride + c, v[i]);
+  }
+  if constexpr (kQuant && kV == 8) {
+    // 128 columns are 16 lanes
+    float top[kN];
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      top[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) top[i] = fmaxf(top[i], fabsf(v[i][j]));
+    }
+    const int lane = threadIdx.x & 31;
+    const BlockScale s = spread_scale<kN>(top, lane, fp8_largest(kQuantType));
+    constexpr int kEach = 16 / kN;                         // lanes that hold a group's scale
+    const int mine = ((lane & 15) / kEach * threads + (t & ~15)) * kV;
+    if (lane % kEach == 0 && mine < d) p.scale[row * p.s_row + mine / kQuantBlock * p.s_col] = s.scale;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int c = (i * threads + t) * kV;
+      const float by = spread_get<kN>(s.inverse, i, lane);
+      if (c < d)
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.q) + row * p.q_stride + c) =
+            make_uint2(fp8_quad<kQuantType>(v[i][0], v[i][1], v[i][2], v[i][3], by),
+                       fp8_quad<kQuantType>(v[i][4], v[i][5], v[i][6], v[i][7], by));
+    }
+  } else if constexpr (kQuant) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      // 32 lanes hold 128 columns, or lie within them
+      const int c = (i * threads + t) * kV;
       float top = 0.0f;
 #pragma unroll
       for (int j = 0; j < kV; ++j) top = fmaxf(top, fabsf(v[i][j]));
 #pragma unroll
-      for (int o = 64 / kV; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const BlockScale s = block_scale(top, fp8_largest(kQuantType));
-      if (c < d) {
-        if (c % kQuantBlock == 0) p.scale[row * p.s_row + c / kQuantBlock * p.s_col] = s.scale;
-        uint8_t* dst = static_cast<uint8_t*>(p.q) + row * p.q_stride + c;
-        uint32_t o[kV / 4];
-#pragma unroll
-        for (int j = 0; j < kV; j += 4)
-          o[j / 4] = fp8_quad<kQuantType>(v[i][j], v[i][j + 1], v[i][j + 2], v[i][j + 3], s.inverse);
-        if constexpr (kV == 8)
-          *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
-        else
-          *reinterpret_cast<uint32_t*>(dst) = o[0];
-      }
-    } else {
-      // 32 lanes lie within one block of 128 columns
-      float top = fabsf(v[i][0]);
-#pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int block = (i * threads + (t & ~31)) / kQuantBlock;
-      if ((t & 31) == 0 && block * kQuantBlock < d) atomicMax(&tops[sub][block], __float_as_int(top));
+      if constexpr (kV == 4) {
+        const BlockScale s = block_scale(top, fp8_largest(kQuantType));
+        if (c < d) {
+          if (c % kQuantBlock == 0) p.scale[row * p.s_row + c / kQuantBlock * p.s_col] = s.scale;
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.q) + row * p.q_stride + c) =
+              fp8_quad<kQuantType>(v[i][0], v[i][1], v[i][2], v[i][3], s.inverse);
+        }
+      } else {
+        const int block = (i * threads + (t & ~31)) / kQuantBlock;
+        if ((t & 31) == 0 && block * kQuantBlock < d) atomicMax(&tops[sub][block], __float_as_int(top));
+      }
     }
   }
   if constexpr (kTops) {
@@ -183,11 +240,98 @@ __global__ void __launch_bounds__(kOneWarp ? kSmallRow* kRowsPerBlock : 1024) no
   }
 }
 
+// Rows that begin off a 16-byte boundary: a thread's groups begin at boundaries
+// all the same, `shift` elements before its columns, and what lies outside the row is
+// neither used nor written.  (An access never leaves the 16 bytes around an element
+// of the row.)  Element by element, 16384 rows of 4097 took seven times as long as
+// rows of 4096.  A block goes through rows whose numbers differ by multiples of
+// 8, which share their shift, so that the weights' columns stay in registers.
+template <typename T, typename W, int kE, bool kOneWarp>
+__global__ void __launch_bounds__(kOneWarp ? kSmallRow* kRowsPerBlock : 1024) norm_shift_kernel(const NormProblem p) {
+  constexpr int kV = kVec<T>, kN = kE / kV;
+  __shared__ float parts[2][2][32];
+  const int t = kOneWarp ? threadIdx.x & 31 : threadIdx.x;
+  const int threads = kOneWarp ? 32 : blockDim.x;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kOneWarp ? kRowsPerBlock : 1) + (kOneWarp ? threadIdx.x >> 5 : 0);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kOneWarp ? kRowsPerBlock : 1);
+  const int d = static_cast<int>(p.d);
+  const float inv_d = 1.0f / static_cast<float>(d);
+  pdl_launch_dependents();
+  pdl_wait();
+  if (kOneWarp && first >= p.n) return;                    // (no block barrier follows)
+  const T* x = static_cast<const T*>(p.x) + first * p.x_stride;
+  T* y = static_cast<T*>(p.y) + first * p.y_stride;
+  const int shift = shift_of(x);
+  float w[kN][kV], b[kN][kV];
+  Group<T, kV> next[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int c = (i * threads + t) * kV - shift;
+    if (p.weight != nullptr) {
+      load_some<W, kV>(static_cast<const W*>(p.weight), c, d, 0.0f, w[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kV; ++j) w[i][j] = 1.0f;
+    }
+    if (p.bias != nullptr) {
+      load_some<W, kV>(static_cast<const W*>(p.bias), c, d, 0.0f, b[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kV; ++j) b[i][j] = 0.0f;
+    }
+    if (c < d) next[i].load(x + c);
+  }
+  int turn = 0;
+#pragma unroll 1
+  for (int64_t row = first; row < p.n; row += step, y += step * p.y_stride, turn ^= 1) {
+    float v[kN][kV];
+    float sum = 0.0f;
+    x += step * p.x_stride;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int c = (i * threads + t) * kV - shift;
+      next[i].get(v[i]);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) {
+        if (c + j < 0 || c + j >= d) v[i][j] = 0.0f;
+        sum += v[i][j];
+      }
+      if (row + step < p.n && c < d) next[i].load(x + c);
+    }
+    const float mean = p.rms ? 0.0f : row_sum<kOneWarp>(sum, parts[turn][0]) * inv_d;
+    float squares = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int c = (i * threads + t) * kV - shift;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) {
+        v[i][j] = c + j < 0 || c + j >= d ? 0.0f : v[i][j] - mean;
+        squares = fmaf(v[i][j], v[i][j], squares);
+      }
+    }
+    const float rstd = rsqrtf(row_sum<kOneWarp>(squares, parts[turn][1]) * inv_d + p.eps);
+    if (t == 0) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int c = (i * threads + t) * kV - shift;
+      if (c >= d) break;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[i][j] = fmaf(v[i][j] * rstd, w[i][j], b[i][j]);
+      store_some<T, kV>(y, c, d, v[i]);
+    }
+  }
+}
+
 // Backward: a block goes through rows blockIdx.x, + gridDim.x, ... (a warp each
 // where rows are short) and keeps the columns' sums of g xh and g in registers;
 // they leave as one partial sum a block, added by norm_sum_kernel in the order
 // of the blocks, so that results do not depend on the run.
-template <typename T, typename W, int kV, int kE, bool kOneWarp>
+// The next row is on its way while a row is summed up.  kShift: see
+// norm_shift_kernel.
+template <typename T, typename W, int kV, int kE, bool kOneWarp, bool kShift>
 __global__ void __launch_bounds__(kOneWarp ? kSmallRow* kRowsPerBlock : (kE <= 16 ? 512 : 1024))
 norm_grad_kernel(const NormGradProblem p) {
   constexpr int kN = kE / kV;
@@ -199,46 +343,71 @@ norm_grad_kernel(const NormGradProblem p) {
   const int d = static_cast<int>(p.d);
   const float inv_d = 1.0f / static_cast<float>(d);
   const bool sums = p.gw != nullptr || p.gb != nullptr;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kOneWarp ? kRowsPerBlock : 1) + sub;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kOneWarp ? kRowsPerBlock : 1);
   pdl_launch_dependents();
   pdl_wait();
+  const T* x = static_cast<const T*>(p.x) + first * p.x_stride;
+  const T* g = static_cast<const T*>(p.g) + first * p.g_stride;
+  const int shift = kShift ? shift_of(x) : 0;
+  Group<T, kV> next_x[kN], next_g[kN];
   float w[kN][kV], gw[kN][kV], gb[kN][kV];
+  float mean = 0.0f, rstd = 0.0f;
+  if (first < p.n) {
+    mean = p.rms ? 0.0f : p.mean[first];
+    rstd = p.rstd[first];
+  }
 #pragma unroll
   for (int i = 0; i < kN; ++i) {
-    const int c = (i * threads + t) * kV;
+    const int c = (i * threads + t) * kV - shift;
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       gw[i][j] = gb[i][j] = 0.0f;
       w[i][j] = 1.0f;
     }
-    if (p.weight != nullptr && c < d) load_group<W, kV>(static_cast<const W*>(p.weight) + c, w[i]);
+    if (p.weight != nullptr && c < d) {
+      if constexpr (kShift)
+        load_some<W, kV>(static_cast<const W*>(p.weight), c, d, 0.0f, w[i]);
+      else
+        load_weights<W, kV>(static_cast<const W*>(p.weight) + c, w[i]);
+    }
+    if (first < p.n && c < d) {
+      next_x[i].load(x + c);
+      next_g[i].load(g + c);
+    }
   }
   int turn = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kOneWarp ? kRowsPerBlock : 1);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * (kOneWarp ? kRowsPerBlock : 1) + sub; row < p.n; row += step) {
-    const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
-    const T* g = static_cast<const T*>(p.g) + row * p.g_stride;
-    const float mean = p.rms ? 0.0f : p.mean[row], rstd = p.rstd[row];
+#pragma unroll 1
+  for (int64_t row = first; row < p.n; row += step) {
     float xh[kN][kV], a[kN][kV];
     float sum_a = 0.0f, sum_ax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int c = (i * threads + t) * kV;
-      if (c < d) {
-        load_group<T, kV>(x + c, xh[i]);
-        load_group<T, kV>(g + c, a[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-          xh[i][j] = mean;
-          a[i][j] = 0.0f;
-        }
-      }
+    const float row_mean = mean, row_rstd = rstd;
+    x += step * p.x_stride;
+    g += step * p.g_stride;
+    const bool more = row + step < p.n;
+    if (more) {
+      mean = p.rms ? 0.0f : p.mean[row + step];
+      rstd = p.rstd[row + step];
     }
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
+      const int c = (i * threads + t) * kV - shift;
+      next_x[i].get(xh[i]);
+      next_g[i].get(a[i]);
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        xh[i][j] = (xh[i][j] - mean) * rstd;
+        if (kShift ? c + j < 0 || c + j >= d : c >= d) {
+          xh[i][j] = row_mean;
+          a[i][j] = 0.0f;
+        }
+      }
+      if (more && c < d) {
+        next_x[i].load(x + c);
+        next_g[i].load(g + c);
+      }
+#pragma unroll
+      for (int j = 0; j < kV; ++j) {
+        xh[i][j] = (xh[i][j] - row_mean) * row_rstd;
         gw[i][j] = fmaf(a[i][j], xh[i][j], gw[i][j]);
         gb[i][j] += a[i][j];
         a[i][j] *= w[i][j];
@@ -265,27 +434,34 @@ norm_grad_kernel(const NormGradProblem p) {
     T* gx = static_cast<T*>(p.gx) + row * p.gx_stride;
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int c = (i * threads + t) * kV;
+      const int c = (i * threads + t) * kV - shift;
       if (c >= d) break;
       float o[kV];
 #pragma unroll
-      for (int j = 0; j < kV; ++j) o[j] = rstd * (a[i][j] - m_a - xh[i][j] * m_ax);
-      store_group<T, kV>(gx + c, o);
+      for (int j = 0; j < kV; ++j) o[j] = row_rstd * (a[i][j] - m_a - xh[i][j] * m_ax);
+      if constexpr (kShift)
+        store_some<T, kV>(gx, c, d, o);
+      else
+        store_group<T, kV>(gx + c, o);
     }
   }
   if (!sums) return;
   float* out = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * d;
   if constexpr (kOneWarp) {
-    // the warps' sums, one after another
+    // the warps' sums, one after another (a block's rows may have different shifts)
+    for (int c = threadIdx.x; c < 2 * 32 * kE; c += blockDim.x) cols[c] = 0.0f;
+    __syncthreads();
     for (int r = 0; r < kRowsPerBlock; ++r) {
       if (sub == r) {
 #pragma unroll
         for (int i = 0; i < kN; ++i)
 #pragma unroll
           for (int j = 0; j < kV; ++j) {
-            const int at = (i * 32 + t) * kV + j;
-            cols[at] = (r > 0 ? cols[at] : 0.0f) + gw[i][j];
-            cols[32 * kE + at] = (r > 0 ? cols[32 * kE + at] : 0.0f) + gb[i][j];
+            const int c = (i * 32 + t) * kV - shift + j;
+            if (c >= 0 && c < d) {
+              cols[c] += gw[i][j];
+              cols[32 * kE + c] += gb[i][j];
+            }
           }
       }
       __syncthreads();
@@ -297,12 +473,13 @@ norm_grad_kernel(const NormGradProblem p) {
   } else {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const int c = (i * threads + t) * kV;
-      if (c >= d) break;
 #pragma unroll
       for (int j = 0; j < kV; ++j) {
-        out[c + j] = gw[i][j];
-        out[d + c + j] = gb[i][j];
+        const int c = (i * threads + t) * kV - shift + j;
+        if (c >= 0 && c < d) {
+          out[c] = gw[i][j];
+          out[d + c] = gb[i][j];
+        }
       }
     }
   }
@@ -361,13 +538,33 @@ cudaError_t launch_norm_of(const NormProblem& p, cudaStream_t stream) {
   return launch_norm_as<T, W, kV, 32, false>(p, threads_for(p.d, 32), stream);
 }
 
+// Whether rows of these tensors have the same shift, row by row.
+template <typename T>
+bool same_shift(const void* a, int64_t a_stride, const void* b, int64_t b_stride) {
+  return (reinterpret_cast<uintptr_t>(a) - reinterpret_cast<uintptr_t>(b)) % 16 == 0 && (a_stride - b_stride) % kVec<T> == 0;
+}
+
+constexpr int kShiftElements = 16;         // of a row a thread takes where rows are shifted
+constexpr int kShiftBlocks = 608;          // a multiple of 8: 4 blocks for each SM of this GPU
+
 template <typename T, typename W>
 cudaError_t launch_norm_typed(const NormProblem& p, cudaStream_t stream) {
   constexpr int kV = kVec<T>;
   const int64_t size = sizeof(T);
   const bool vectors = p.d % kV == 0 && aligned16(p.x) && p.x_stride * size % 16 == 0 && aligned16(p.weight) &&
                        aligned16(p.bias) && (p.q != nullptr || (aligned16(p.y) && p.y_stride * size % 16 == 0));
-  return vectors ? launch_norm_of<T, W, kV>(p, stream) : launch_norm_of<T, W, 1>(p, stream);
+  if (vectors) return launch_norm_of<T, W, kV>(p, stream);
+  const int64_t wide = p.d + kV;             // columns with the shift before them
+  if (p.q == nullptr && wide <= 1024 * kShiftElements && same_shift<T>(p.x, p.x_stride, p.y, p.y_stride)) {
+    if (wide <= 32 * kShiftElements)
+      return launch_kernel(norm_shift_kernel<T, W, kShiftElements, true>,
+                           dim3(static_cast<unsigned>(std::min<int64_t>((p.n + kRowsPerBlock - 1) / kRowsPerBlock, kShiftBlocks))),
+                           dim3(kSmallRow * kRowsPerBlock), 0, stream, true, p);
+    return launch_kernel(norm_shift_kernel<T, W, kShiftElements, false>,
+                         dim3(static_cast<unsigned>(std::min<int64_t>(p.n, kShiftBlocks))),
+                         dim3(threads_for(wide, kShiftElements)), 0, stream, true, p);
+  }
+  return launch_norm_of<T, W, 1>(p, stream);
 }
 
 // Columns a thread of the backward pass takes, and the threads of a row.
@@ -375,27 +572,30 @@ struct GradShape {
   int elements, threads;      // threads 32: a warp a row
 };
 
-GradShape grad_shape(int64_t d) {
-  if (d <= 256) return {8, 32};
-  if (d <= 1024) return {32, 32};
-  if (d <= 512 * 16) return {16, threads_for(d, 16)};
-  return {32, threads_for(d, 32)};
+GradShape grad_shape(int64_t width) {
+  if (width <= 256) return {8, 32};
+  if (width <= 1024) return {32, 32};
+  if (width <= 512 * 16) return {16, threads_for(width, 16)};
+  return {32, threads_for(width, 32)};
 }
 
-template <typename T, typename W, int kV, int kE, bool kOneWarp>
-cudaError_t launch_grad_as(const NormGradProblem& p, int threads, cudaStream_t stream) {
-  const int64_t blocks = norm_grad_blocks(p.n, p.d);
-  return launch_kernel(norm_grad_kernel<T, W, kV, kE, kOneWarp>, dim3(static_cast<unsigned>(blocks)),
+constexpr int64_t kGradBlocks = 304;       // a multiple of 8: 2 blocks for each SM of this GPU
+
+template <typename T, typename W, int kV, int kE, bool kOneWarp, bool kShift>
+cudaError_t launch_grad_as(const NormGradProblem& p, int threads, int64_t* blocks, cudaStream_t stream) {
+  *blocks = std::min<int64_t>(kOneWarp ? (p.n + kRowsPerBlock - 1) / kRowsPerBlock : p.n, kGradBlocks);
+  return launch_kernel(norm_grad_kernel<T, W, kV, kE, kOneWarp, kShift>, dim3(static_cast<unsigned>(*blocks)),
                        dim3(kOneWarp ? kSmallRow * kRowsPerBlock : threads), 0, stream, true, p);
 }
 
-template <typename T, typename W, int kV>
-cudaError_t launch_grad_of(const NormGradProblem& p, cudaStream_t stream) {
-  const GradShape s = grad_shape(p.d);
+template <typename T, typename W, int kV, bool kShift>
+cudaError_t launch_grad_of(const NormGradProblem& p, int64_t* blocks, cudaStream_t stream) {
+  const GradShape s = grad_shape(kShift ? p.d + kV : p.d);
   if (s.threads == 32)
-    return s.elements == 8 ? launch_grad_as<T, W, kV, 8, true>(p, 32, stream) : launch_grad_as<T, W, kV, 32, true>(p, 32, stream);
-  return s.elements == 16 ? launch_grad_as<T, W, kV, 16, false>(p, s.threads, stream)
-                          : launch_grad_as<T, W, kV, 32, false>(p, s.threads, stream);
+    return s.elements == 8 ? launch_grad_as<T, W, kV, 8, true, kShift>(p, 32, blocks, stream)
+                           : launch_grad_as<T, W, kV, 32, true, kShift>(p, 32, blocks, stream);
+  return s.elements == 16 ? launch_grad_as<T, W, kV, 16, false, kShift>(p, s.threads, blocks, stream)
+                          : launch_grad_as<T, W, kV, 32, false, kShift>(p, s.threads, blocks, stream);
 }
 
 template <typename T, typename W>
@@ -405,10 +605,15 @@ cudaError_t launch_grad_typed(const NormGradProblem& p, cudaStream_t stream) {
   const bool vectors = p.d % kV == 0 && aligned16(p.x) && p.x_stride * size % 16 == 0 && aligned16(p.weight) &&
                        aligned16(p.g) && p.g_stride * size % 16 == 0 && aligned16(p.gx) &&
                        (p.gx == nullptr || p.gx_stride * size % 16 == 0);
-  cudaError_t e = vectors ? launch_grad_of<T, W, kV>(p, stream) : launch_grad_of<T, W, 1>(p, stream);
+  const bool shifted = p.d + kV <= kNormMaxWidth && same_shift<T>(p.x, p.x_stride, p.g, p.g_stride) &&
+                       (p.gx == nullptr || same_shift<T>(p.x, p.x_stride, p.gx, p.gx_stride));
+  int64_t blocks = 0;
+  const cudaError_t e = vectors   ? launch_grad_of<T, W, kV, false>(p, &blocks, stream)
+                        : shifted ? launch_grad_of<T, W, kV, true>(p, &blocks, stream)
+                                  : launch_grad_of<T, W, 1, false>(p, &blocks, stream);
   if (e != cudaSuccess || (p.gw == nullptr && p.gb == nullptr)) return e;
   return launch_kernel(norm_sum_kernel<W>, dim3(static_cast<unsigned>((2 * p.d + 31) / 32)), dim3(32 * kSumSlices), 0, stream,
-                       true, static_cast<const float*>(p.partials), norm_grad_blocks(p.n, p.d), p.d, static_cast<W*>(p.gw),
+                       true, static_cast<const float*>(p.partials), blocks, p.d, static_cast<W*>(p.gw),
                        static_cast<W*>(p.gb));
 }
 
@@ -427,10 +632,7 @@ cudaError_t launch_norm(const NormProblem& p, cudaStream_t stream) {
   return by_types(p.x_type, p.w_type, [&](auto x, auto w) { return launch_norm_typed<decltype(x), decltype(w)>(p, stream); });
 }
 
-int64_t norm_grad_blocks(int64_t n, int64_t d) {
-  const int64_t rows = grad_shape(d).threads == 32 ? kRowsPerBlock : 1;
-  return std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, 304));
-}
+int64_t norm_grad_blocks(int64_t n) { return std::min(n, kGradBlocks); }
 
 cudaError_t launch_norm_grad(const NormGradProblem& p, cudaStream_t stream) {
   return by_types(p.x_type, p.w_type, [&](auto x, auto w) { return launch_grad_typed<decltype(x), decltype(w)>(p, stream); });

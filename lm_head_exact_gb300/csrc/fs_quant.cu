@@ -5,10 +5,10 @@
 // for blocks of 1 x 128 or 128 x 128 of the matrix or of its transpose.  What
 // bounds it is memory: 2 (or 4) bytes read and 1 written per element, each
 // once.  A block of 256 threads takes a tile of up to 128 rows x 128 columns into
-// registers, 8 elements of a row a thread and load, finds the blocks' largest
-// values by shuffles (and through shared memory where a block spans the warps),
-// and writes whole 128-byte lines; the transpose's bytes cross shared memory,
-// swizzled so that neither side meets bank conflicts.
+// registers as it lies in memory, 8 elements of a row a thread and load, finds the
+// blocks' largest values by shuffles (and through shared memory where a block
+// spans the warps), and writes whole 128-byte lines; the transpose's bytes cross
+// shared memory, swizzled so that neither side meets bank conflicts.
 #include "fs_fp8.cuh"
 #include "fs_fp8.h"
 
@@ -19,105 +19,105 @@ constexpr int kThreads = 256;
 constexpr int kCols = 128;                 // of x a tile takes
 constexpr int kGroup = 8;                  // elements of a row a thread takes at a time
 
-__device__ __forceinline__ float half_warp_max(float v) {
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
 // kRows rows a thread: a tile of 16 kRows rows.  Thread t holds columns
 // 8 (t % 16) .. + 7 of rows kRows (t / 16) .. of the tile.
 template <typename T, int kType, int kRows, bool kTranspose, bool kSquare>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantProblem p, bool aligned) {
   constexpr bool kTile = kTranspose || kSquare;          // a whole 128 x 128 block is needed
   static_assert(!kTile || kRows == 8, "a tile of 128 rows");
-  __shared__ float tops[kSquare ? 8 : kTranspose ? 8 * kCols : 1];
+  __shared__ __align__(16) Tops<T> tops[kSquare || kTranspose ? 8 : 1][kTranspose && !kSquare ? 16 : 1];
   __shared__ __align__(16) uint8_t bytes[kTranspose ? kCols * 128 : 16];
+  const int lane = threadIdx.x & 31;
   const int col_in = (threadIdx.x & 15) * kGroup;
   const int row_in = (threadIdx.x >> 4) * kRows;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kCols + col_in;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 16 * kRows + row_in;
   pdl_launch_dependents();
   pdl_wait();
-  float v[kRows][kGroup];
+  Eight<T> v[kRows];
   const T* src = static_cast<const T*>(p.x) + r0 * p.x_stride + c0;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+#pragma unroll
+    for (int h = 0; h < 8 / kVec<T>; ++h) v[i].raw[h] = make_uint4(0u, 0u, 0u, 0u);
   if (aligned && c0 + kGroup <= p.cols) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int i = 0; i < kRows; ++i)
       if (r0 + i < p.rows) {
-        float part[kVec<T>];
 #pragma unroll
-        for (int h = 0; h < kGroup; h += kVec<T>) {
-          unpack<T>(*reinterpret_cast<const uint4*>(src + i * p.x_stride + h), part);
-#pragma unroll
-          for (int j = 0; j < kVec<T>; ++j) v[i][h + j] = part[j];
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) v[i][j] = 0.0f;
+        for (int h = 0; h < 8 / kVec<T>; ++h) v[i].raw[h] = reinterpret_cast<const uint4*>(src + i * p.x_stride)[h];
       }
-    }
   } else {
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
 #pragma unroll
       for (int j = 0; j < kGroup; ++j)
-        v[i][j] = r0 + i < p.rows && c0 + j < p.cols ? to_float<T>(src[i * p.x_stride + j]) : 0.0f;
+        if (r0 + i < p.rows && c0 + j < p.cols) reinterpret_cast<T*>(v[i].raw)[j] = src[i * p.x_stride + j];
   }
   constexpr float kLargest = fp8_largest(kType);
-  BlockScale s[kTranspose && !kSquare ? kGroup : kSquare ? 1 : kRows];
-  if constexpr (kSquare) {
-    float top = 0.0f;
+  float inverse[kTranspose && !kSquare ? kGroup : kSquare ? 1 : kRows];
+  if constexpr (kSquare || kTranspose) {
+    Tops<T> top;
+    top.clear();
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
+    for (int i = 0; i < kRows; ++i) top.add(v[i]);
+    top.join(16);
+    if constexpr (kSquare) {
+      float all[1] = {top.all()};
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) top = fmaxf(top, fabsf(v[i][j]));
-    top = half_warp_max(top);
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-    __syncthreads();
+      for (int o = 8; o > 0; o >>= 1) all[0] = fmaxf(all[0], __shfl_xor_sync(0xffffffffu, all[0], o));
+      float* shared = reinterpret_cast<float*>(tops);
+      if (lane == 0) shared[threadIdx.x >> 5] = all[0];
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, tops[w]);
-    s[0] = block_scale(top, kLargest);
-    if (threadIdx.x == 0)
-      p.scale[(kTranspose ? blockIdx.x : blockIdx.y) * p.s_row + (kTranspose ? blockIdx.y : blockIdx.x) * p.s_col] = s[0].scale;
-  } else if constexpr (kTranspose) {
-    // the blocks lie along x's rows: one for each column of the tile
+      for (int w = 0; w < 8; ++w) all[0] = fmaxf(all[0], shared[w]);
+      const BlockScale s = block_scale(all[0], kLargest);
+      inverse[0] = s.inverse;
+      if (threadIdx.x == 0)
+        p.scale[(kTranspose ? blockIdx.x : blockIdx.y) * p.s_row + (kTranspose ? blockIdx.y : blockIdx.x) * p.s_col] = s.scale;
+    } else {
+      // the blocks lie along x's rows: one for each column of the tile
+      if (lane < 16) tops[threadIdx.x >> 5][lane] = top;
+      __syncthreads();
+      float* scales = reinterpret_cast<float*>(bytes);   // (until the bytes are put down)
+      if (threadIdx.x < kCols) {
+        float m = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
-      float top = 0.0f;
+        for (int w = 0; w < 8; ++w) m = fmaxf(m, tops[w][threadIdx.x >> 3].column(threadIdx.x & 7));
+        const BlockScale s = block_scale(m, kLargest);
+        scales[threadIdx.x] = s.inverse;
+        const int64_t c = static_cast<int64_t>(blockIdx.x) * kCols + threadIdx.x;
+        if (c < p.cols) p.scale[c * p.s_row + blockIdx.y * p.s_col] = s.scale;
+      }
+      __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) top = fmaxf(top, fabsf(v[i][j]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-      if ((threadIdx.x & 16) == 0) tops[(threadIdx.x >> 5) * kCols + col_in + j] = top;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
-      float top = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) top = fmaxf(top, tops[w * kCols + col_in + j]);
-      s[j] = block_scale(top, kLargest);
-      if (threadIdx.x < 16 && c0 + j < p.cols) p.scale[(c0 + j) * p.s_row + blockIdx.y * p.s_col] = s[j].scale;
+      for (int j = 0; j < kGroup; ++j) inverse[j] = scales[col_in + j];
+      __syncthreads();
     }
   } else {
+    float top[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      float top = 0.0f;
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) top = fmaxf(top, fabsf(v[i][j]));
-      s[i] = block_scale(half_warp_max(top), kLargest);
-      if ((threadIdx.x & 15) == 0 && r0 + i < p.rows) p.scale[(r0 + i) * p.s_row + blockIdx.x * p.s_col] = s[i].scale;
+      Tops<T> t;
+      t.clear();
+      t.add(v[i]);
+      top[i] = t.all();
     }
+    const BlockScale s = spread_scale<kRows>(top, lane, kLargest);
+    constexpr int kEach = 16 / kRows;                      // lanes that hold a row's scale
+    const int64_t row = r0 + (lane & 15) / kEach;
+    if (lane % kEach == 0 && row < p.rows) p.scale[row * p.s_row + blockIdx.x * p.s_col] = s.scale;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) inverse[i] = spread_get<kRows>(s.inverse, i, lane);
   }
   uint8_t* q = static_cast<uint8_t*>(p.q);
   if constexpr (!kTranspose) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       if (r0 + i >= p.rows) break;
-      const float inverse = s[kSquare ? 0 : i].inverse;
-      const uint2 o = make_uint2(fp8_quad<kType>(v[i][0], v[i][1], v[i][2], v[i][3], inverse),
-                                 fp8_quad<kType>(v[i][4], v[i][5], v[i][6], v[i][7], inverse));
+      const float by = inverse[kSquare ? 0 : i];
+      const uint2 o = make_uint2(fp8_quad<kType>(v[i].value(0), v[i].value(1), v[i].value(2), v[i].value(3), by),
+                                 fp8_quad<kType>(v[i].value(4), v[i].value(5), v[i].value(6), v[i].value(7), by));
       uint8_t* dst = q + (r0 + i) * p.q_stride + c0;
       if (c0 + kGroup <= p.cols) {
         *reinterpret_cast<uint2*>(dst) = o;
@@ -133,11 +133,11 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantProblem p
     // g ^ (c / 8), so that the 16 lanes of a store lie in different banks
 #pragma unroll
     for (int j = 0; j < kGroup; ++j) {
-      const float inverse = s[kSquare ? 0 : j].inverse;
+      const float by = inverse[kSquare ? 0 : j];
       const int place = (threadIdx.x >> 4) ^ ((col_in >> 3) & 15);
       *reinterpret_cast<uint2*>(bytes + (col_in + j) * 128 + place * 8) =
-          make_uint2(fp8_quad<kType>(v[0][j], v[1][j], v[2][j], v[3][j], inverse),
-                     fp8_quad<kType>(v[4][j], v[5][j], v[6][j], v[7][j], inverse));
+          make_uint2(fp8_quad<kType>(v[0].value(j), v[1].value(j), v[2].value(j), v[3].value(j), by),
+                     fp8_quad<kType>(v[4].value(j), v[5].value(j), v[6].value(j), v[7].value(j), by));
     }
     __syncthreads();
     const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 128;            // first column of q's tile

@@ -93,6 +93,7 @@ struct NormGradProblem {
   void* gw;                 // nullable [d] of w_type
   void* gb;                 // nullable [d] of w_type
   float* partials;          // norm_grad_blocks(n) x 2 x d
+  int* err;
 };
 // Blocks, at most, that each leave one partial sum of the weight's and bias's gradients.
 int64_t norm_grad_blocks(int64_t n);

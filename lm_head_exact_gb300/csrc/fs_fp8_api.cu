@@ -274,9 +274,11 @@ fs_status fs_layer_norm_backward(const void* g, int64_t g_row_stride, const void
       FS_API_TRY(api_check_array(workspace, 16, "workspace"));
     }
   }
+  int* err = nullptr;
+  FS_API_TRY(api_error_word(&err, stream));
   FS_API_TRY(api_check_launch());
   const NormGradProblem p{g, g_row_stride, x, x_type, n, d, x_row_stride, weight, w_type, rms == 1, mean, rstd, grad_x,
-                          grad_x_row_stride, grad_weight, grad_bias, static_cast<float*>(workspace)};
+                          grad_x_row_stride, grad_weight, grad_bias, static_cast<float*>(workspace), err};
   return api_launched(launch_norm_grad(p, stream), "layer norm gradient launch");
   });
 }

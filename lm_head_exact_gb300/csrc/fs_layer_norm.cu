@@ -12,6 +12,7 @@
 
 #include "fs_fp8.cuh"
 #include "fs_fp8.h"
+#include "fs_fp8_ptx.cuh"
 
 namespace fs {
 namespace {
@@ -485,6 +486,134 @@ norm_grad_kernel(const NormGradProblem p) {
   }
 }
 
+// The backward pass of wide rows on 16-byte boundaries: rows of x and g come by bulk
+// copies into a ring of shared memory, kRing rows ahead, so that enough of them are
+// on their way whatever registers hold (16384 x 4096: 102 us with the next row in
+// registers, and more of them spilled).  A block's one barrier a row, which its sums need
+// anyway, says that the row's place may be filled again.
+constexpr int kRing = 4;
+
+template <typename T, typename W, int kE>
+__global__ void __launch_bounds__(512) norm_grad_ring_kernel(const NormGradProblem p, int ring) {
+  constexpr int kV = kVec<T>, kN = kE / kV;
+  extern __shared__ __align__(128) uint8_t rows[];         // [ring][2][d] of T
+  __shared__ float parts[2][2][32];
+  __shared__ uint64_t full[kRing];
+  __shared__ int abort_flag;
+  const int t = threadIdx.x, threads = blockDim.x;
+  const int d = static_cast<int>(p.d);
+  const uint32_t bytes = static_cast<uint32_t>(d * sizeof(T));
+  const float inv_d = 1.0f / static_cast<float>(d);
+  if (t == 0) {
+    for (int i = 0; i < ring; ++i) sm100::mbar_init(&full[i], 1);
+    abort_flag = 0;
+    sm100::fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_launch_dependents();
+  pdl_wait();
+  auto fill = [&](int64_t row, int slot) {
+    if (row >= p.n) return;
+    uint8_t* at = rows + static_cast<size_t>(slot) * 2 * bytes;
+    sm100::mbar_arrive_expect_tx(&full[slot], 2 * bytes);
+    sm100::bulk_load(at, static_cast<const T*>(p.x) + row * p.x_stride, bytes, &full[slot]);
+    sm100::bulk_load(at + bytes, static_cast<const T*>(p.g) + row * p.g_stride, bytes, &full[slot]);
+  };
+  const int64_t step = gridDim.x;
+  if (t == 0)
+    for (int i = 0; i < ring; ++i) fill(blockIdx.x + i * step, i);
+  float w[kN][kV], gw[kN][kV], gb[kN][kV];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int c = (i * threads + t) * kV;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      gw[i][j] = gb[i][j] = 0.0f;
+      w[i][j] = 1.0f;
+    }
+    if (p.weight != nullptr && c < d) load_weights<W, kV>(static_cast<const W*>(p.weight) + c, w[i]);
+  }
+  int turn = 0, slot = 0;
+  uint32_t phase = 0;
+  float next_mean = p.rms ? 0.0f : p.mean[blockIdx.x], next_rstd = p.rstd[blockIdx.x];
+#pragma unroll 1
+  for (int64_t row = blockIdx.x; row < p.n; row += step) {
+    const float mean = next_mean, rstd = next_rstd;
+    if (row + step < p.n) {                                // (a row ahead: the loads take as long as a row)
+      next_mean = p.rms ? 0.0f : p.mean[row + step];
+      next_rstd = p.rstd[row + step];
+    }
+    // (a wait that gives up leaves the error word set; the block goes on with
+    // whatever lies there, so that its barriers stay whole)
+    sm100::mbar_wait(&full[slot], phase, p.err, &abort_flag);
+    const T* x = reinterpret_cast<const T*>(rows + static_cast<size_t>(slot) * 2 * bytes);
+    const T* g = x + d;
+    float xh[kN][kV], a[kN][kV];
+    float sum_a = 0.0f, sum_ax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int c = (i * threads + t) * kV;
+      if (c < d) {
+        unpack<T>(*reinterpret_cast<const uint4*>(x + c), xh[i]);
+        unpack<T>(*reinterpret_cast<const uint4*>(g + c), a[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+          xh[i][j] = mean;
+          a[i][j] = 0.0f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kV; ++j) {
+        xh[i][j] = (xh[i][j] - mean) * rstd;
+        gw[i][j] = fmaf(a[i][j], xh[i][j], gw[i][j]);
+        gb[i][j] += a[i][j];
+        a[i][j] *= w[i][j];
+        sum_a += a[i][j];
+        sum_ax = fmaf(a[i][j], xh[i][j], sum_ax);
+      }
+    }
+    sum_a = warp_sum(sum_a);
+    sum_ax = warp_sum(sum_ax);
+    // (two sets in turn: a thread that is a row ahead does not overwrite what another still reads)
+    if ((t & 31) == 0) {
+      parts[turn][0][t >> 5] = sum_a;
+      parts[turn][1][t >> 5] = sum_ax;
+    }
+    __syncthreads();
+    if (t == 0) fill(row + ring * step, slot);
+    if (++slot == ring) { slot = 0; phase ^= 1; }
+    if (p.gx == nullptr) continue;
+    const bool mine = (t & 31) < (threads >> 5);
+    sum_a = warp_sum(mine ? parts[turn][0][t & 31] : 0.0f);
+    sum_ax = warp_sum(mine ? parts[turn][1][t & 31] : 0.0f);
+    turn ^= 1;
+    const float m_a = p.rms ? 0.0f : sum_a * inv_d, m_ax = sum_ax * inv_d;
+    T* gx = static_cast<T*>(p.gx) + row * p.gx_stride;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int c = (i * threads + t) * kV;
+      if (c >= d) break;
+      float o[kV];
+#pragma unroll
+      for (int j = 0; j < kV; ++j) o[j] = rstd * (a[i][j] - m_a - xh[i][j] * m_ax);
+      store_group<T, kV>(gx + c, o);
+    }
+  }
+  if (p.gw == nullptr && p.gb == nullptr) return;
+  float* out = p.partials + static_cast<int64_t>(blockIdx.x) * 2 * d;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const int c = (i * threads + t) * kV;
+    if (c >= d) break;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      out[c + j] = gw[i][j];
+      out[d + c + j] = gb[i][j];
+    }
+  }
+}
+
 // Sums over the blocks' partials: 32 columns a block of threads, 8 slices of the
 // partials, joined in the order of the slices.
 constexpr int kSumSlices = 16;
@@ -598,6 +727,21 @@ cudaError_t launch_grad_of(const NormGradProblem& p, int64_t* blocks, cudaStream
                           : launch_grad_as<T, W, kV, 32, false, kShift>(p, s.threads, blocks, stream);
 }
 
+// The ring takes whole rows of more than a warp's, where two of them fit.
+constexpr int kRingBytes = 96 * 1024;      // a block's, of which two are on an SM
+
+template <typename T, typename W>
+cudaError_t launch_grad_ring(const NormGradProblem& p, int64_t* blocks, cudaStream_t stream) {
+  const int bytes = static_cast<int>(2 * p.d * sizeof(T)), ring = std::min(kRing, kRingBytes / bytes);
+  *blocks = std::min<int64_t>(p.n, kGradBlocks);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = raise_smem_limit<norm_grad_ring_kernel<T, W, 16>>(dev, kRingBytes);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(norm_grad_ring_kernel<T, W, 16>, dim3(static_cast<unsigned>(*blocks)), dim3(threads_for(p.d, 16)),
+                       ring * bytes, stream, true, p, ring);
+}
+
 template <typename T, typename W>
 cudaError_t launch_grad_typed(const NormGradProblem& p, cudaStream_t stream) {
   constexpr int kV = kVec<T>;
@@ -608,7 +752,9 @@ cudaError_t launch_grad_typed(const NormGradProblem& p, cudaStream_t stream) {
   const bool shifted = p.d + kV <= kNormMaxWidth && same_shift<T>(p.x, p.x_stride, p.g, p.g_stride) &&
                        (p.gx == nullptr || same_shift<T>(p.x, p.x_stride, p.gx, p.gx_stride));
   int64_t blocks = 0;
-  const cudaError_t e = vectors   ? launch_grad_of<T, W, kV, false>(p, &blocks, stream)
+  const bool ring = vectors && p.d > 1024 && p.d <= 512 * 16 && 4 * p.d * size <= kRingBytes && p.n > kGradBlocks;
+  const cudaError_t e = ring      ? launch_grad_ring<T, W>(p, &blocks, stream)
+                        : vectors ? launch_grad_of<T, W, kV, false>(p, &blocks, stream)
                         : shifted ? launch_grad_of<T, W, kV, true>(p, &blocks, stream)
                                   : launch_grad_of<T, W, 1, false>(p, &blocks, stream);
   if (e != cudaSuccess || (p.gw == nullptr && p.gb == nullptr)) return e;

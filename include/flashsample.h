@@ -484,9 +484,10 @@ FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, 
  * (i, j) has its scale at scale[i * scale_row_stride + j * scale_col_stride];
  * a row i is one row of q (block_rows 1) or 128 (block_rows 128).  q times its
  * scale is the value.  Rows of scales side by side (scale_row_stride 1) are
- * read fastest where block_rows is 1.  None of these calls needs a workspace,
- * but for fs_layer_norm_backward's, which comes from the caller as the training
- * calls' does.  Widths need not be multiples of anything.
+ * read fastest where block_rows is 1.  Widths need not be multiples of anything.
+ * fs_sample_fp8 uses the sampling workspace of (device, stream);
+ * fs_layer_norm_backward's comes from the caller as the training calls' does;
+ * the others need none.  fs_workspace_reserve() makes all of them capturable.
  * ------------------------------------------------------------------------ */
 
 /* 8-bit element types, beside FS_TYPE_F32, _BF16 and _F16. */
@@ -514,10 +515,10 @@ FS_API fs_status fs_quantize_fp8(const void* x, int x_type, int64_t rows, int64_
  * (block_rows 1 or 128):
  *   out[i, j] = sum over blocks of a_scale b_scale (sum within the block of a[i, :] b[j, :])
  * The products of a block are summed by the tensor cores, the blocks in fp32
- * registers, in an order that the sizes fix; a_scale b_scale is formed first, in fp32 (its overflow
- * is an infinity).  out: fp32, bf16 or fp16, rows out_row_stride >= n elements
- * apart, rounded once.  Types of a and b may differ.  m, n, k < 2^31 - 1024; k == 0
- * gives zeros.  out overlaps neither a nor b.
+ * registers, in an order that the sizes fix; a_scale b_scale is formed first, in
+ * fp32 (its overflow is an infinity).  out: fp32, bf16 or fp16, rows
+ * out_row_stride >= n elements apart, rounded once.  Types of a and b may differ.
+ * m, n <= 2^31 - 1024, k <= 2^24; k == 0 gives zeros.  out overlaps neither a nor b.
  * For a linear layer in training: y = x8 W8^T, grad_x = g8 (W^T)8^T with
  * W^T from a transposing fs_quantize_fp8 (of 128 x 128 blocks: the same
  * values as W's), grad_W = (g^T)8 (x^T)8^T, both quantised along the tokens.
@@ -534,8 +535,8 @@ FS_API fs_status fs_fp8_matmul(const void* a, int a_type, int64_t a_row_stride, 
  * fs_layer_norm), W by rows or in blocks of 128 x 128 (W_block_rows).  The
  * same noise, temperatures, bias, ties and outputs as fs_sample_ex, over the
  * logits that fs_fp8_matmul forms; reads half the bytes of a bf16 head.
- * d < 2^31 - 1024, B and V < 2^31.  Uses the sampling workspace of
- * (device, stream): fs_workspace_reserve() before a capture.
+ * d <= 2^24, B and V <= 2^31 - 1024.  A row's samples do not depend on the
+ * batch beyond the order in which sizes have its products summed.
  */
 FS_API fs_status fs_sample_fp8(const void* h, int64_t h_row_stride, const float* h_scale, int64_t h_scale_row_stride,
                                int64_t h_scale_col_stride, const void* W, int64_t W_row_stride, const float* W_scale,

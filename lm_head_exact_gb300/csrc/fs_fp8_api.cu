@@ -11,6 +11,7 @@ namespace fs {
 namespace {
 
 constexpr int64_t kMaxSize = (int64_t(1) << 31) - 1024;
+constexpr int64_t kMaxDepth = int64_t(1) << 24;      // of k: a tile then takes a tenth of what a wait allows
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 
 bool is_wide(int type) { return type >= FS_TYPE_F32 && type <= FS_TYPE_F16; }
@@ -98,8 +99,8 @@ fs_status fs_fp8_matmul(const void* a, int a_type, int64_t a_row_stride, const f
   api_begin();
   return guarded([&]() -> fs_status {
   if (m < 0 || n < 0 || k < 0) return api_fail(FS_ERR_INVALID_ARG, "need m, n, k >= 0");
-  if (m > kMaxSize || n > kMaxSize || k > kMaxSize)
-    return api_fail(FS_ERR_UNSUPPORTED, "m, n and k must be <= %lld", (long long)kMaxSize);
+  if (m > kMaxSize || n > kMaxSize || k > kMaxDepth)
+    return api_fail(FS_ERR_UNSUPPORTED, "m and n must be <= %lld, k <= %lld", (long long)kMaxSize, (long long)kMaxDepth);
   if (!is_wide(out_type)) return api_fail(FS_ERR_INVALID_ARG, "out: unknown type %d", out_type);
   FS_API_TRY(check_rows(m, n, out_row_stride, "out"));
   FS_API_TRY(check_fp8(a, a_type, m, k, a_row_stride, a_scale, a_scale_row_stride, a_scale_col_stride, 1, "a"));
@@ -133,8 +134,8 @@ fs_status fs_sample_fp8(const void* h, int64_t h_row_stride, const float* h_scal
   return guarded([&]() -> fs_status {
   if (B < 0 || d <= 0 || V < 0) return api_fail(FS_ERR_INVALID_ARG, "need B >= 0, d > 0, V >= 0 (got %lld, %lld, %lld)",
                                                 (long long)B, (long long)d, (long long)V);
-  if (B > kMaxSize || d > kMaxSize || V > kMaxSize)
-    return api_fail(FS_ERR_UNSUPPORTED, "B, d and V must be <= %lld", (long long)kMaxSize);
+  if (B > kMaxSize || d > kMaxDepth || V > kMaxSize)
+    return api_fail(FS_ERR_UNSUPPORTED, "B and V must be <= %lld, d <= %lld", (long long)kMaxSize, (long long)kMaxDepth);
   FS_API_TRY(check_fp8(h, FS_TYPE_E4M3, B, d, h_row_stride, h_scale, h_scale_row_stride, h_scale_col_stride, 1, "h"));
   if (B == 0) return FS_OK;
   FS_API_TRY(check_fp8(W, FS_TYPE_E4M3, V, d, W_row_stride, W_scale, W_scale_row_stride, W_scale_col_stride, W_block_rows, "W"));

@@ -556,18 +556,18 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
       // Adds block kb's sums, while the next block's are loaded where there are registers for them.
       auto finish = [&](int kb, uint32_t (&r)[kLoads][kRegs], uint32_t (&r_next)[kLoads][kRegs]) {
         const int pos = (kb - k0) % kPer, at = (kb - k0) % kAhead;
-                  // the factors of this block: of the thread's rows and columns
-                  const float* lane_scales = scales + (fill % kSlots * kAhead + at) * S::kScaleWords;
-                  const float* col_scales = lane_scales + kLanes;
-                  float f[kLaneScales && kColScales ? 4 : 1];
-                  if constexpr (kLaneScales && kColScales) {
+        // the factors of this block: of the thread's rows and columns
+        const float* lane_scales = scales + (fill % kSlots * kAhead + at) * S::kScaleWords;
+        const float* col_scales = lane_scales + kLanes;
+        float f[kLaneScales && kColScales ? 4 : 1];
+        if constexpr (kLaneScales && kColScales) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = lane_scales[quad * 32 + 8 * i + (lane >> 2)];
-                  } else if constexpr (kLaneScales) {
-                    f[0] = lane_scales[quad * 32 + lane] * col_scales[part];
-                  } else {
-                    f[0] = lane_scales[0];
-                  }
+          for (int i = 0; i < 4; ++i) f[i] = lane_scales[quad * 32 + 8 * i + (lane >> 2)];
+        } else if constexpr (kLaneScales) {
+          f[0] = lane_scales[quad * 32 + lane] * col_scales[part];
+        } else {
+          f[0] = lane_scales[0];
+        }
         if (live) {
 #pragma unroll
           for (int q = 0; q < kLoads; ++q) tmem_ld_wait_for(r[q]);

@@ -17,6 +17,11 @@ over the gradients of all parameters: grad_W and the body's, not grad_h, which
 is the gradient of activations.  Here, where the body is a fixed set of hidden
 states, the head is all there is to update and to clip.
 
+With a ``FinalNorm``, the hidden states are those ahead of the model's last norm:
+they are normed for sampling and scoring, grad_h is the gradient ahead of the
+norm, and the norm's own gradients come with it (parameters, to clip with
+grad_W).
+
 Usage: ``python -m lm_head_exact_gb300.policy_step [steps]`` on a GPU.
 """
 
@@ -26,9 +31,22 @@ from . import binding as fs
 
 
 @dataclass
+class FinalNorm:
+    """The model's last norm, between its hidden states and the head."""
+    weight: object          # [d] bf16 or fp32
+    bias: object = None     # [d] of weight's type
+    eps: float = 1e-5
+    rms: bool = False       # without the mean
+
+    def __call__(self, h):
+        """(normed, mean, rstd) of hidden states."""
+        return fs.layer_norm(h, self.weight, self.bias, eps=self.eps, rms=self.rms)
+
+
+@dataclass
 class Rollout:
     """Tokens drawn from the policy: packed sequences and what they earned."""
-    h: object               # bf16 [N, d] hidden states
+    h: object               # bf16 [N, d] hidden states (ahead of the final norm, where there is one)
     ids: object             # int64 [N] sampled tokens
     temp: object            # fp32 [N] sampling temperatures
     seq_starts: object      # int64 [S + 1]
@@ -38,14 +56,15 @@ class Rollout:
     bias: object = None     # fp32 [N, V] or [V], the sampler's, under which the tokens are scored too
 
 
-def roll_out(h, W, temp, seq_starts, reward, seed, step, bias=None):
+def roll_out(h, W, temp, seq_starts, reward, seed, step, bias=None, norm=None):
     """Sample a token for every hidden state and score it under W (and the
     sampler's ``bias``, for instance -inf at forbidden tokens); ``reward``
     maps the ids to one value per sequence, which become advantages by
     subtracting their mean and dividing by their spread (one sequence alone
-    has neither: advantage 0)."""
-    ids, _ = fs.sample(h, W, temp, seed, step, bias=bias)
-    old_logp, _ = fs.token_logprobs(h, W, ids, temp, bias=bias)
+    has neither: advantage 0).  ``norm``: the FinalNorm ahead of the head."""
+    normed = h if norm is None else norm(h)[0]
+    ids, _ = fs.sample(normed, W, temp, seed, step, bias=bias)
+    old_logp, _ = fs.token_logprobs(normed, W, ids, temp, bias=bias)
     r = reward(ids)
     spread = r.std() if r.numel() > 1 else 0.0
     advantages = ((r - r.mean()) / (spread + 1e-6)).contiguous()
@@ -59,10 +78,12 @@ class StepResult:
     grad_h: object          # bf16 [N, d]
     grad_W: object          # bf16 [V, d]
     logp: object            # fp32 [N]
+    grad_norm_weight: object = None   # [d], the final norm's, where there is one
+    grad_norm_bias: object = None     # [d], where it has a bias
 
 
 def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef=0.0, mean="token", max_norm=None,
-                keep_logits=True):
+                keep_logits=True, norm=None):
     """Loss and gradients of one step on ``rollout`` under the head W.
     ``keep_logits`` spends 4 bytes per token and vocabulary row to form the
     logits once instead of twice.  Rows without a token (the sampler's -1, an
@@ -71,21 +92,31 @@ def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef
     The gradients are not clipped here: the norm of the model's gradient is
     known after the body's backward pass only (clip_grad_norm over all
     parameters' gradients).  ``max_norm`` is for something else: it bounds the
-    norm of grad_h and grad_W taken as one vector, that is of the step's whole
-    signal into head and body, and scales both by one factor."""
+    norm of grad_h and grad_W (and the final norm's gradients) taken as one
+    vector, that is of the step's whole signal into head and body, and scales
+    all by one factor.
+
+    ``norm``: the present policy's FinalNorm; grad_h is then the gradient of the
+    rollout's hidden states ahead of it."""
     r = rollout
     n, V = r.h.shape[0], W.shape[0]
+    h, mu, rstd = (r.h, None, None) if norm is None else norm(r.h)
     kept = fs.logprob_buffer(n, V, device=r.h.device) if keep_logits else None
-    logp, lse = fs.token_logprobs(r.h, W, r.ids, r.temp, bias=r.bias, kept=kept)
+    logp, lse = fs.token_logprobs(h, W, r.ids, r.temp, bias=r.bias, kept=kept)
     # (unscored rows have logp 0 on both sides: a ratio of 1, and a part in the means)
     scored = (r.ids >= 0) & (r.ids < V) & (r.temp >= 0)
     mask = scored if r.mask is None else r.mask & scored
     stats, grad_logp = fs.policy_loss(logp, r.old_logp, r.advantages, seq_starts=r.seq_starts, mask=mask,
                                       ref_logp=ref_logp, clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef,
                                       mean=mean, adv_per_seq=True)
-    grad_h, grad_W = fs.token_logprobs_backward(r.h, W, r.ids, r.temp, logp, lse, grad_logp, bias=r.bias, kept=kept)
-    norm = None if max_norm is None else fs.clip_grad_norm([grad_h, grad_W], max_norm)
-    return StepResult(stats, norm, grad_h, grad_W, logp)
+    grad_h, grad_W = fs.token_logprobs_backward(h, W, r.ids, r.temp, logp, lse, grad_logp, bias=r.bias, kept=kept)
+    grad_weight = grad_bias = None
+    if norm is not None:
+        grad_h, grad_weight, grad_bias = fs.layer_norm_backward(grad_h, r.h, norm.weight, mu, rstd,
+                                                                need_bias=norm.bias is not None, out=grad_h)
+    grads = [g for g in (grad_h, grad_W, grad_weight, grad_bias) if g is not None]
+    total = None if max_norm is None else fs.clip_grad_norm(grads, max_norm)
+    return StepResult(stats, total, grad_h, grad_W, logp, grad_weight, grad_bias)
 
 
 def train_toy(steps=20, V=48, d=64, sequences=256, length=4, lr=6.0, seed=1234, device="cuda"):

@@ -19,6 +19,12 @@ of a step are one CUDA-graph replay, so the step is bound by the GPU, not by
 the host's launch rate.  Timing: CUDA events on one stream, around the whole
 loop for the step time and around each step's LM-head call for the head time
 (see ``DecodeLoop.run``).
+
+With ``fp8`` the loop runs in 8 bits on the library's own kernels: every weight
+is quantised once in blocks of 128 x 128, norms write 8-bit hidden states with a
+scale for each 128 columns, the projections are 8-bit products of those
+(``fp8_matmul``), and the head samples from 8-bit weights (``sample_fp8``).  A
+step then reads half the bytes of the bf16 one.
 """
 
 from dataclasses import dataclass
@@ -44,9 +50,11 @@ class DecodeLoop:
 
     ``layers`` decoder layers of the shapes in ``layer`` (default: Llama-3-8B),
     weights ~ N(0, 1/fan_in) in bf16, drawn on the device from ``seed``.
+    ``fp8``: the same weights quantised, head included (the embedding stays
+    bf16).
     """
 
-    def __init__(self, W, layers=32, layer=None, seed=0):
+    def __init__(self, W, layers=32, layer=None, seed=0, fp8=False):
         import torch
         self.torch = torch
         self.W = W
@@ -57,8 +65,11 @@ class DecodeLoop:
 
         def mat(n_in, n_out):
             m = torch.randn((n_out, n_in), generator=g, device=W.device, dtype=torch.float32)
-            return (m * (n_in ** -0.5)).to(torch.bfloat16)
+            m = (m * (n_in ** -0.5)).to(torch.bfloat16)
+            return fs.quantize_fp8(m, block_rows=128) if fp8 else m
 
+        self.fp8 = fp8
+        self.W8 = fs.quantize_fp8(W, block_rows=128) if fp8 else None
         self.layers = []
         for _ in range(layers):
             self.layers.append(dict(
@@ -72,9 +83,24 @@ class DecodeLoop:
         xf = x.float()
         return (xf * (xf.pow(2).mean(-1, keepdim=True) + 1e-6).rsqrt()).to(x.dtype)
 
+    def _body_fp8(self, x):
+        """The decoder layers in 8 bits; the last norm's result is quantised for
+        the head: (q [B, d], scale)."""
+        torch = self.torch
+        norm = lambda v: fs.layer_norm_fp8(v, eps=1e-6, rms=True)  # noqa: E731
+        for L in self.layers:
+            y = fs.fp8_matmul(*norm(x), *L["qkv"])
+            x = x + fs.fp8_matmul(*fs.quantize_fp8(y[:, : self.q]), *L["o"])      # projections only (no KV cache)
+            gu = fs.fp8_matmul(*norm(x), *L["gate_up"])
+            g, u = gu[:, : self.ffn], gu[:, self.ffn:]
+            x = x + fs.fp8_matmul(*fs.quantize_fp8(torch.nn.functional.silu(g) * u), *L["down"])
+        return norm(x)
+
     def body(self, x):
         """The decoder layers on hidden states x [B, d] (bf16)."""
         torch = self.torch
+        if self.fp8:
+            return self._body_fp8(x)
         for L in self.layers:
             y = self._rms(x) @ L["qkv"].t()
             x = x + y[:, : self.q] @ L["o"].t()             # projections only (no KV cache)
@@ -84,7 +110,11 @@ class DecodeLoop:
         return self._rms(x)
 
     def _head(self, x, temp, seed, step, ids, mx, fused, stream):
-        if fused:
+        if self.fp8:
+            if not fused:
+                raise ValueError("the unfused pipeline has no 8-bit form")
+            fs.sample_fp8(*x, *self.W8, temp, seed, step, out=(ids, mx), stream=stream)
+        elif fused:
             fs.sample(x, self.W, temp, seed, step, out=(ids, mx), stream=stream)
         else:
             fs.sample_unfused(x, self.W, temp, seed, step, out=(ids, mx), stream=stream)
@@ -145,6 +175,25 @@ class DecodeLoop:
         step_us = t0.elapsed_time(t1) / steps * 1e3
         head_us = sum(a.elapsed_time(b) for a, b in ev) / steps * 1e3
         return StepTiming(step_us, head_us), ids
+
+
+def measure_fp8(W, batches=(1, 16, 64), layers=32, steps=10, warmup=3, layer=None, seed=1234):
+    """The loop in bf16 and in 8 bits, per batch: one dict each with step and
+    head µs of both and the step-time reduction 8 bits give."""
+    import torch
+    V = W.shape[0]
+    out = [{"B": B, "layers": layers} for B in batches]
+    for arm, fp8 in (("bf16", False), ("fp8", True)):
+        loop = DecodeLoop(W, layers=layers, layer=layer, fp8=fp8)
+        for r in out:
+            g = torch.Generator(device=W.device).manual_seed(r["B"])
+            ids0 = torch.randint(0, V, (r["B"],), generator=g, device=W.device)
+            t, _ = loop.run(ids0, torch.ones(r["B"], device=W.device), steps, seed=seed, warmup=warmup)
+            r[f"{arm}_step_us"], r[f"{arm}_head_us"] = round(t.step_us, 1), round(t.head_us, 1)
+        del loop
+    for r in out:
+        r["step_time_reduction"] = round(1.0 - r["fp8_step_us"] / r["bf16_step_us"], 4)
+    return out
 
 
 def measure(W, batches=(1, 16, 256), layers=32, steps=10, warmup=3, layer=None, seed=1234):

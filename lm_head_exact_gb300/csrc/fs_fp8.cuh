@@ -9,8 +9,17 @@
 #include <cstdint>
 
 #include "flashsample.h"
+#include "fs_device.cuh"
 
 namespace fs {
+
+// Waits for what lies ahead in the stream, then lets the next kernel start: one
+// that reads weights before its own wait must not begin while a kernel ahead of
+// this one may still write them.
+__device__ __forceinline__ void pdl_wait_then_launch() {
+  pdl_wait();
+  pdl_launch_dependents();
+}
 
 template <typename T> __device__ __forceinline__ float to_float(T v);
 template <> __device__ __forceinline__ float to_float<float>(float v) { return v; }

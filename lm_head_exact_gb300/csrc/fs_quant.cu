@@ -32,8 +32,7 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantProblem p
   const int row_in = (threadIdx.x >> 4) * kRows;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kCols + col_in;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 16 * kRows + row_in;
-  pdl_launch_dependents();
-  pdl_wait();
+  pdl_wait_then_launch();
   Eight<T> v[kRows];
   const T* src = static_cast<const T*>(p.x) + r0 * p.x_stride + c0;
 #pragma unroll

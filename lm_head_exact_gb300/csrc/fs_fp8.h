@@ -49,6 +49,9 @@ struct Fp8Product {
   int64_t out_stride;
 };
 cudaError_t launch_fp8_matmul(const Fp8Product& p, int* err, cudaStream_t stream);
+// The same where there is little to read (fs_fp8_rows.cu).
+bool fp8_rows_takes(const Fp8Product& p);
+cudaError_t launch_fp8_rows(const Fp8Product& p, cudaStream_t stream);
 
 // The sampler: rows of a are the batch, rows of b the vocabulary (p.h, p.W and
 // p.d of the Problem are not looked at).

@@ -174,6 +174,18 @@ def test_product_of_many_tiles(fs, torch_cuda, m, n, k):
     check_product(fs.fp8_matmul(a.q, a.scale, c.q, c.scale), a, c, "bf16", f"{m} x {n} x {k} by rows")
 
 
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("m,n,k", [(1, 33000, 4200), (9, 8200, 4100), (16, 6145, 4112), (31, 4100, 4200), (20, 3000, 8200),
+                                   (64, 1000, 16400), (33, 130, 80000), (64, 7, 1000003), (7, 10, 300000), (65, 20000, 1100)])
+def test_product_of_few_rows(fs, torch_cuda, m, n, k, block):
+    """Few rows of a, with more of b to read than the smallest products have."""
+    torch = torch_cuda
+    a, b = Operand(torch, m, k, seed=k % 2), Operand(torch, n, k, block, seed=n % 2)
+    for kind in ("fp32", "bf16"):
+        check_product(fs.fp8_matmul(a.q, a.scale, b.q, b.scale, out_dtype=dtype_of(torch, kind)), a, b, kind, f"{m} x {n} x {k}")
+    assert fs.device_error() == 0
+
+
 def test_product_into_a_view(fs, torch_cuda):
     """Rows further apart than they are long, off any alignment; nothing else is
     written."""
@@ -199,6 +211,20 @@ def test_product_keeps_nan_and_infinity_in_their_rows(fs, torch_cuda):
     scale[5, 1] = float("inf")
     got = fs.fp8_matmul(bits.view(torch.float8_e4m3fn) if bits.stride(0) % 16 == 0 else _pitched(torch, bits), scale,
                         b.q, b.scale, out_dtype=torch.float32)
+    assert bool(got[3].isnan().all()) and not bool(got[5].isfinite().any())
+    rows = [i for i in range(20) if i not in (3, 5)]
+    assert bool((got[rows] == clean[rows]).all())
+
+
+def test_large_product_of_few_rows_keeps_nan_and_infinity_in_their_rows(fs, torch_cuda):
+    torch = torch_cuda
+    a, b = Operand(torch, 20, 4300), Operand(torch, 4200, 4300, 128)
+    clean = fs.fp8_matmul(a.q, a.scale, b.q, b.scale, out_dtype=torch.float32)
+    bits = a.q.view(torch.uint8).clone()
+    bits[3, 4290] = 0x7f
+    scale = a.scale.clone()
+    scale[5, 1] = float("inf")
+    got = fs.fp8_matmul(_pitched(torch, bits), scale, b.q, b.scale, out_dtype=torch.float32)
     assert bool(got[3].isnan().all()) and not bool(got[5].isfinite().any())
     rows = [i for i in range(20) if i not in (3, 5)]
     assert bool((got[rows] == clean[rows]).all())

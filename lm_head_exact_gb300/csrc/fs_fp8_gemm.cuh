@@ -40,6 +40,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fs_epilogue.cuh"
 #include "fs_finish.cuh"
@@ -60,6 +61,7 @@ constexpr int kLanes = 128;                    // rows on a CTA's lanes
 constexpr int kBK = 128;                       // elements and bytes of a row in a stage
 constexpr int kLTile = kLanes * kBK;
 constexpr int kPitch = 33;                     // words of a staged row of 32
+constexpr int kBulkPitch = 144;                // bytes of a staged row of 128 (bulk copies want multiples of 16)
 constexpr int kBarBytes = 1024;
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxSplits = 8;
@@ -67,7 +69,7 @@ constexpr int kMaxSplits = 8;
 constexpr int kAhead = 4;                      // blocks whose scales are brought at a time
 constexpr int kSlots = 2;                      // times that many
 
-template <Form kForm, int kBN, bool kColScales>
+template <Form kForm, int kBN, bool kSample, bool kColScales>
 struct Shape {
   static constexpr bool kSwap = kForm == kThin;
   static constexpr int kCtas = kForm == kPair ? 2 : 1;
@@ -97,7 +99,7 @@ struct Shape {
   // one for each part).
   static constexpr int kScaleWords = kLanes + (kColScales ? kBN : 4);
   static constexpr int kScaleBytes = kSlots * kAhead * kScaleWords * 4;
-  static constexpr int kWarpWords = 32 * kPitch;          // of a warp's staging area
+  static constexpr int kWarpWords = 32 * (kSwap || kSample ? kPitch : kBulkPitch / 4);   // of a warp's staging area
   static constexpr int kStagingBytes = kEpiWarps * kWarpWords * 4;
   static constexpr int kKeyBytes = kSwap ? kBN * 8 : 0;
   static constexpr int kFit = (kSmemLimit - 1024 - kBarBytes - kStagingBytes - kScaleBytes - kKeyBytes) / kStageBytes;
@@ -125,6 +127,7 @@ struct Args {
   void* out;
   int out_type;
   int64_t out_stride;
+  bool bulk;                 // the output's rows lie on 16-byte boundaries
   Problem p;                 // sampling
   Finish f;
   int* err;
@@ -178,6 +181,62 @@ __device__ __forceinline__ void store_rows(const Args& a, const float* stage, in
   }
 }
 
+// A warp's sums, 32 rows x 64 columns, to whole columns of the output by bulk
+// copies of a lane's row, 128 bytes each, which are on their way while the next
+// tile's sums are added up (stored by the warps, 32 columns at a time, a tile
+// took 8500 clocks to leave).
+// kFrag: in fragments, see the kernel.  32-bit outputs take two turns.
+template <typename T, bool kFrag>
+__device__ __forceinline__ void store_bulk(const Args& a, const float (&acc)[64], uint32_t* stage, int64_t row0, int64_t col0) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kTurns = sizeof(T) / 2, kCols = 64 / kTurns;
+  uint8_t* rows = reinterpret_cast<uint8_t*>(stage);
+  const auto word = [](float lo, float hi) {
+    return pair_word(std::is_same<T, __half>::value ? FS_TYPE_F16 : FS_TYPE_BF16, lo, hi);
+  };
+#pragma unroll
+  for (int turn = 0; turn < kTurns; ++turn) {
+    sm100::bulk_wait_read();
+    __syncwarp();
+    if constexpr (kFrag) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (kTurns == 2 && q / 2 != turn) continue;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const int row = 16 * (q & 1) + 8 * (i >> 1 & 1) + (lane >> 2);
+          const int col = 32 * (q >> 1) - turn * kCols + 8 * (i >> 2) + 2 * (lane & 3);
+          uint8_t* at = rows + row * kBulkPitch + col * sizeof(T);
+          const float lo = acc[16 * q + i], hi = acc[16 * q + i + 1];
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<float2*>(at) = make_float2(lo, hi);
+          else
+            *reinterpret_cast<uint32_t*>(at) = word(lo, hi);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint4 v;
+        if constexpr (sizeof(T) == 4) {
+          const float* from = acc + turn * kCols + 4 * j;
+          v = make_uint4(__float_as_uint(from[0]), __float_as_uint(from[1]), __float_as_uint(from[2]), __float_as_uint(from[3]));
+        } else {
+          const float* from = acc + 8 * j;
+          v = make_uint4(word(from[0], from[1]), word(from[2], from[3]), word(from[4], from[5]), word(from[6], from[7]));
+        }
+        *reinterpret_cast<uint4*>(rows + lane * kBulkPitch + 16 * j) = v;
+      }
+    }
+    sm100::fence_async_shared();
+    __syncwarp();
+    if (row0 + lane < a.l_rows)
+      sm100::bulk_store(static_cast<T*>(a.out) + (row0 + lane) * a.out_stride + col0 + turn * kCols,
+                        sm100::smem_u32(rows + lane * kBulkPitch), 128);
+    sm100::bulk_commit();
+  }
+}
+
 // The sampling kernels' scan (fs_epilogue.cuh) of 32 staged logits of one row,
 // ids v0 .. v0 + 31 (a multiple of 4 first), kStep words apart: the same scores in
 // the same order, in a loop over the counters' quads.  (Unrolled, with and without
@@ -213,9 +272,9 @@ __device__ __forceinline__ Best scan_staged(const float* at, int64_t v0, int64_t
 // whole lanes, where every thread needs them all, reading them took as much
 // of shared memory's bandwidth as the operands do.
 template <Form kForm, int kBN, bool kSample, bool kLaneScales, bool kColScales, bool kSplit>
-__global__ void __launch_bounds__(Shape<kForm, kBN, kColScales>::kThreads, 1)
+__global__ void __launch_bounds__(Shape<kForm, kBN, kSample, kColScales>::kThreads, 1)
 kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUtensorMap tmap_c, const Args a) {
-  using S = Shape<kForm, kBN, kColScales>;
+  using S = Shape<kForm, kBN, kSample, kColScales>;
   constexpr bool kSwap = S::kSwap, kPairs = kForm == kPair;
   static_assert(kColScales || kLaneScales, "scales of a tile of lanes are folded into those of the columns");
   constexpr int kStages = S::kStages, kBufs = S::kBufs, kPart = S::kPart, kGroups = S::kGroups;
@@ -652,7 +711,20 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
               red[kSwap ? col * (kLanes + 1) + row : row * (kBN + 1) + col] = acc[q * kRegs + i];
             }
         }
+      } else if (live && !kSample && !kSwap && a.bulk && c0 + kPart <= a.c_rows) {
+        if constexpr (!kSample && !kSwap) {
+          if (a.out_type == FS_TYPE_F32)
+            store_bulk<float, kColScales>(a, acc, reinterpret_cast<uint32_t*>(stage), l0, c0);
+          else if (a.out_type == FS_TYPE_BF16)
+            store_bulk<__nv_bfloat16, kColScales>(a, acc, reinterpret_cast<uint32_t*>(stage), l0, c0);
+          else
+            store_bulk<__half, kColScales>(a, acc, reinterpret_cast<uint32_t*>(stage), l0, c0);
+        }
       } else if (live) {
+        if constexpr (!kSample && !kSwap) {
+          bulk_wait_read();
+          __syncwarp();
+        }
         // 32 rows x 32 columns at a time through the staging area: a lane then scans
         // a row (with kSwap, where lanes are vocabulary ids, a column), or a store
         // covers whole rows of the output
@@ -700,6 +772,7 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
         }
       }
     }
+    if constexpr (!kSample && !kSwap && !kSplit) bulk_wait();
     if constexpr (kSample) {
       if constexpr (kSwap) {
         // the CTA's warps first: few rows would otherwise gather all warps' candidates
@@ -768,7 +841,7 @@ int sm_count();
 template <Form kForm, int kBN, bool kSample, bool kLaneScales, bool kColScales, bool kSplit>
 cudaError_t launch(Args a, const Fp8Matrix& ma, const Fp8Matrix& mb, int64_t m, int64_t n, int64_t k, int ctas,
                    cudaStream_t stream) {
-  using S = Shape<kForm, kBN, kColScales>;
+  using S = Shape<kForm, kBN, kSample, kColScales>;
   constexpr bool kSwap = S::kSwap;
   const Fp8Matrix& l = kSwap ? mb : ma;
   const Fp8Matrix& c = kSwap ? ma : mb;

@@ -127,7 +127,6 @@ cudaError_t launch_fp8_matmul(const Fp8Product& p, int* err, cudaStream_t stream
   a.out = p.out;
   a.out_type = p.out_type;
   a.out_stride = p.out_stride;
-  a.bulk = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 && p.out_stride * (p.out_type == FS_TYPE_F32 ? 4 : 2) % 16 == 0;
   a.err = err;
   if (s.form == kThin) return s.bn == 16 ? thin<16>(a, p, stream) : s.bn == 32 ? thin<32>(a, p, stream) : thin<64>(a, p, stream);
   return s.form == kPair ? wide<kPair, 192>(a, p, stream) : wide<kWide, 192>(a, p, stream);

@@ -61,7 +61,6 @@ constexpr int kLanes = 128;                    // rows on a CTA's lanes
 constexpr int kBK = 128;                       // elements and bytes of a row in a stage
 constexpr int kLTile = kLanes * kBK;
 constexpr int kPitch = 33;                     // words of a staged row of 32
-constexpr int kBulkPitch = 144;                // bytes of a staged row of 128 (bulk copies want multiples of 16)
 constexpr int kBarBytes = 1024;
 constexpr int kSmemLimit = 232448;
 constexpr int kMaxSplits = 8;
@@ -99,7 +98,7 @@ struct Shape {
   // one for each part).
   static constexpr int kScaleWords = kLanes + (kColScales ? kBN : 4);
   static constexpr int kScaleBytes = kSlots * kAhead * kScaleWords * 4;
-  static constexpr int kWarpWords = 32 * (kSwap || kSample ? kPitch : kBulkPitch / 4);   // of a warp's staging area
+  static constexpr int kWarpWords = 32 * (kSwap || kSample ? kPitch : 32);  // of a warp's staging area (a box for TMA: whole KB)
   static constexpr int kStagingBytes = kEpiWarps * kWarpWords * 4;
   static constexpr int kKeyBytes = kSwap ? kBN * 8 : 0;
   static constexpr int kFit = (kSmemLimit - 1024 - kBarBytes - kStagingBytes - kScaleBytes - kKeyBytes) / kStageBytes;
@@ -127,7 +126,7 @@ struct Args {
   void* out;
   int out_type;
   int64_t out_stride;
-  bool bulk;                 // the output's rows lie on 16-byte boundaries
+  int64_t tma_cols;          // of the output: a warp's columns that end up to here are stored by TMA
   Problem p;                 // sampling
   Finish f;
   int* err;
@@ -152,7 +151,8 @@ __device__ __forceinline__ void store_one(const Args& a, int64_t row, int64_t co
     static_cast<__half*>(a.out)[at] = __float2half_rn(v);
 }
 
-// 32 staged rows of 32 columns to the output, whole rows of them by a store.
+// 32 staged rows of 32 columns, column c of row r at c ^ r, to the output, whole
+// rows of them by a store: outputs off 16-byte boundaries, and ends of rows.
 __device__ __forceinline__ void store_rows(const Args& a, const float* stage, int64_t row0, int64_t col0) {
   const int lane = threadIdx.x & 31;
   const int rows = static_cast<int>(min(static_cast<int64_t>(32), a.l_rows - row0));
@@ -161,7 +161,7 @@ __device__ __forceinline__ void store_rows(const Args& a, const float* stage, in
     float* dst = static_cast<float*>(a.out) + row0 * a.out_stride + col0 + lane;
     if (lane < cols) {
 #pragma unroll 4
-      for (int i = 0; i < rows; ++i, dst += a.out_stride) *dst = stage[i * kPitch + lane];
+      for (int i = 0; i < rows; ++i, dst += a.out_stride) *dst = stage[i * 32 + (lane ^ i)];
     }
     return;
   }
@@ -171,7 +171,7 @@ __device__ __forceinline__ void store_rows(const Args& a, const float* stage, in
   const bool whole = (reinterpret_cast<uintptr_t>(a.out) & 3) == 0 && (a.out_stride & 1) == 0 && (col0 & 1) == 0;
 #pragma unroll 4
   for (int i = row; i < rows; i += 2, dst += 2 * a.out_stride) {
-    const uint32_t w = pair_word(a.out_type, stage[i * kPitch + col], stage[i * kPitch + col + 1]);
+    const uint32_t w = pair_word(a.out_type, stage[i * 32 + (col ^ i)], stage[i * 32 + (col + 1 ^ i)]);
     if (whole && col + 1 < cols) {
       *reinterpret_cast<uint32_t*>(dst) = w;
     } else {
@@ -181,22 +181,21 @@ __device__ __forceinline__ void store_rows(const Args& a, const float* stage, in
   }
 }
 
-// A warp's sums, 32 rows x 64 columns, to whole columns of the output by bulk
-// copies of a lane's row, 128 bytes each, which are on their way while the next
-// tile's sums are added up (stored by the warps, 32 columns at a time, a tile
-// took 8500 clocks to leave).
-// kFrag: in fragments, see the kernel.  32-bit outputs take two turns.
+// A warp's sums, 32 rows x 64 columns, to the output by a TMA store, 128 bytes a
+// row, that is on its way while the next tile's sums are added up.  (Stored by the
+// warps, 32 columns at a time, a tile took 8500 clocks to leave.)  32-bit outputs take
+// two turns.  The box lies swizzled, 16 bytes by 16, so that neither rows nor
+// fragments (kFrag, see the kernel) meet bank conflicts.
 template <typename T, bool kFrag>
-__device__ __forceinline__ void store_bulk(const Args& a, const float (&acc)[64], uint32_t* stage, int64_t row0, int64_t col0) {
+__device__ __forceinline__ void store_tile(const CUtensorMap* out, const float (&acc)[64], uint8_t* box, int64_t row0, int64_t col0) {
   const int lane = threadIdx.x & 31;
   constexpr int kTurns = sizeof(T) / 2, kCols = 64 / kTurns;
-  uint8_t* rows = reinterpret_cast<uint8_t*>(stage);
   const auto word = [](float lo, float hi) {
     return pair_word(std::is_same<T, __half>::value ? FS_TYPE_F16 : FS_TYPE_BF16, lo, hi);
   };
 #pragma unroll
   for (int turn = 0; turn < kTurns; ++turn) {
-    sm100::bulk_wait_read();
+    if (lane == 0) sm100::bulk_wait_read();                // the box's last store has been read
     __syncwarp();
     if constexpr (kFrag) {
 #pragma unroll
@@ -205,13 +204,13 @@ __device__ __forceinline__ void store_bulk(const Args& a, const float (&acc)[64]
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
           const int row = 16 * (q & 1) + 8 * (i >> 1 & 1) + (lane >> 2);
-          const int col = 32 * (q >> 1) - turn * kCols + 8 * (i >> 2) + 2 * (lane & 3);
-          uint8_t* at = rows + row * kBulkPitch + col * sizeof(T);
+          const int at = (32 * (q >> 1) - turn * kCols + 8 * (i >> 2) + 2 * (lane & 3)) * static_cast<int>(sizeof(T));
+          uint8_t* dst = box + row * 128 + ((at >> 4 ^ (row & 7)) << 4) + (at & 15);
           const float lo = acc[16 * q + i], hi = acc[16 * q + i + 1];
           if constexpr (sizeof(T) == 4)
-            *reinterpret_cast<float2*>(at) = make_float2(lo, hi);
+            *reinterpret_cast<float2*>(dst) = make_float2(lo, hi);
           else
-            *reinterpret_cast<uint32_t*>(at) = word(lo, hi);
+            *reinterpret_cast<uint32_t*>(dst) = word(lo, hi);
         }
       }
     } else {
@@ -225,15 +224,15 @@ __device__ __forceinline__ void store_bulk(const Args& a, const float (&acc)[64]
           const float* from = acc + 8 * j;
           v = make_uint4(word(from[0], from[1]), word(from[2], from[3]), word(from[4], from[5]), word(from[6], from[7]));
         }
-        *reinterpret_cast<uint4*>(rows + lane * kBulkPitch + 16 * j) = v;
+        *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = v;
       }
     }
     sm100::fence_async_shared();
     __syncwarp();
-    if (row0 + lane < a.l_rows)
-      sm100::bulk_store(static_cast<T*>(a.out) + (row0 + lane) * a.out_stride + col0 + turn * kCols,
-                        sm100::smem_u32(rows + lane * kBulkPitch), 128);
-    sm100::bulk_commit();
+    if (lane == 0) {
+      sm100::tma_store_2d(out, box, static_cast<int32_t>((col0 + turn * kCols) * sizeof(T)), static_cast<int32_t>(row0));
+      sm100::bulk_commit();
+    }
   }
 }
 
@@ -273,7 +272,8 @@ __device__ __forceinline__ Best scan_staged(const float* at, int64_t v0, int64_t
 // of shared memory's bandwidth as the operands do.
 template <Form kForm, int kBN, bool kSample, bool kLaneScales, bool kColScales, bool kSplit>
 __global__ void __launch_bounds__(Shape<kForm, kBN, kSample, kColScales>::kThreads, 1)
-kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUtensorMap tmap_c, const Args a) {
+kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUtensorMap tmap_c,
+       const __grid_constant__ CUtensorMap tmap_o, const Args a) {
   using S = Shape<kForm, kBN, kSample, kColScales>;
   constexpr bool kSwap = S::kSwap, kPairs = kForm == kPair;
   static_assert(kColScales || kLaneScales, "scales of a tile of lanes are folded into those of the columns");
@@ -711,18 +711,18 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
               red[kSwap ? col * (kLanes + 1) + row : row * (kBN + 1) + col] = acc[q * kRegs + i];
             }
         }
-      } else if (live && !kSample && !kSwap && a.bulk && c0 + kPart <= a.c_rows) {
+      } else if (live && !kSample && !kSwap && c0 + kPart <= a.tma_cols) {
         if constexpr (!kSample && !kSwap) {
           if (a.out_type == FS_TYPE_F32)
-            store_bulk<float, kColScales>(a, acc, reinterpret_cast<uint32_t*>(stage), l0, c0);
+            store_tile<float, kColScales>(&tmap_o, acc, reinterpret_cast<uint8_t*>(stage), l0, c0);
           else if (a.out_type == FS_TYPE_BF16)
-            store_bulk<__nv_bfloat16, kColScales>(a, acc, reinterpret_cast<uint32_t*>(stage), l0, c0);
+            store_tile<__nv_bfloat16, kColScales>(&tmap_o, acc, reinterpret_cast<uint8_t*>(stage), l0, c0);
           else
-            store_bulk<__half, kColScales>(a, acc, reinterpret_cast<uint32_t*>(stage), l0, c0);
+            store_tile<__half, kColScales>(&tmap_o, acc, reinterpret_cast<uint8_t*>(stage), l0, c0);
         }
       } else if (live) {
         if constexpr (!kSample && !kSwap) {
-          bulk_wait_read();
+          if (lane == 0) bulk_wait_read();
           __syncwarp();
         }
         // 32 rows x 32 columns at a time through the staging area: a lane then scans
@@ -738,7 +738,7 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
             const float v = c == 0 ? acc[j] : acc[j + kNext];
             const int q = kColScales ? j / kRegs : 0, i = j % kRegs;
             const int row = kColScales ? frag_row(q, i) : lane, col = kColScales ? frag_col(q, i) : i;
-            stage[kSwap && !kSample ? col * kPitch + row : row * kPitch + col] = v;
+            stage[kSample ? row * kPitch + col : kSwap ? col * kPitch + row : row * 32 + (col ^ row)] = v;
           }
           __syncwarp();
           if constexpr (kSample) {
@@ -772,7 +772,9 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
         }
       }
     }
-    if constexpr (!kSample && !kSwap && !kSplit) bulk_wait();
+    if constexpr (!kSample && !kSwap && !kSplit) {
+      if (lane == 0) bulk_wait();
+    }
     if constexpr (kSample) {
       if constexpr (kSwap) {
         // the CTA's warps first: few rows would otherwise gather all warps' candidates
@@ -856,6 +858,15 @@ cudaError_t launch(Args a, const Fp8Matrix& ma, const Fp8Matrix& mb, int64_t m, 
   CUtensorMap tl, tc;
   if (!encode_rows_u8(&tl, l.q, a.l_rows, k, l.stride, kBK, a.box_l) || !encode_rows_u8(&tc, c.q, a.c_rows, k, c.stride, kBK, a.box_c))
     return cudaErrorInvalidValue;
+  CUtensorMap to = tc;                                     // (of the output, where it is used)
+  if constexpr (!kSample && !kSwap && !kSplit) {
+    const int64_t width = a.out_type == FS_TYPE_F32 ? 4 : 2;
+    // (a TMA store leaves out what lies behind the last column by 16 bytes, not by
+    // elements: rows that end within 16 have their last columns stored by the warps)
+    if (reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride * width % 16 == 0 && n * width <= INT32_MAX - 1024 &&
+        encode_rows_u8(&to, a.out, m, n * width, a.out_stride * width, 128, 32))
+      a.tma_cols = n * width % 16 == 0 ? INT64_MAX : n;
+  }
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   constexpr auto fn = kernel<kForm, kBN, kSample, kLaneScales, kColScales, kSplit>;
@@ -884,7 +895,7 @@ cudaError_t launch(Args a, const Fp8Matrix& ma, const Fp8Matrix& mb, int64_t m, 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, fn, tl, tc, a);
+  return cudaLaunchKernelEx(&cfg, fn, tl, tc, to, a);
 }
 
 // Tiles of a launch; false where their number passes 31 bits.

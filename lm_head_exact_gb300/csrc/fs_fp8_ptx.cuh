@@ -200,11 +200,5 @@ __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
   return v;
 }
 
-// `bytes` of this CTA's shared memory to global memory (both on 16-byte
-// boundaries, a multiple of 16); see tma_store_2d.
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src_smem, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src_smem), "r"(bytes) : "memory");
-}
-
 }  // namespace sm100
 }  // namespace fs

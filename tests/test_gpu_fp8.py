@@ -201,6 +201,23 @@ def test_product_into_a_view(fs, torch_cuda):
             assert bool((memory == 7.0).all())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("block", [1, 128])
+@pytest.mark.parametrize("m,n,k", [(65, 193, 128), (129, 71, 200), (300, 1000, 256), (257, 6, 100), (70, 449, 17),
+                                   (1500, 2049, 128)])
+def test_product_into_an_aligned_view(fs, torch_cuda, m, n, k, block, kind):
+    """Rows on 16-byte boundaries that end anywhere: nothing behind them, or
+    behind the last one, is written."""
+    torch = torch_cuda
+    a, b = Operand(torch, m, k, seed=n % 2), Operand(torch, n, k, block, seed=m % 2)
+    memory = torch.full((m + 2, (n + 31) // 16 * 16), 7.0, dtype=dtype_of(torch, kind), device="cuda")
+    out = memory[1:-1, 8:8 + n]
+    fs.fp8_matmul(a.q, a.scale, b.q, b.scale, out=out)
+    check_product(out, a, b, kind, "aligned view")
+    memory[1:-1, 8:8 + n] = 7.0
+    assert bool((memory == 7.0).all()) and fs.device_error() == 0
+
+
 def test_product_keeps_nan_and_infinity_in_their_rows(fs, torch_cuda):
     torch = torch_cuda
     a, b = Operand(torch, 20, 300), Operand(torch, 140, 300, 128)

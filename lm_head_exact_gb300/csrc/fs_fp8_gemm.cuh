@@ -236,13 +236,30 @@ __device__ __forceinline__ void store_tile(const CUtensorMap* out, const float (
   }
 }
 
+// The best score that any CTA has pushed for a row so far.
+__device__ __forceinline__ float best_so_far(const unsigned long long* key) {
+  unsigned long long k;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(k) : "l"(key) : "memory");
+  return unpack_key(k).z;
+}
+
 // The sampling kernels' scan (fs_epilogue.cuh) of 32 staged logits of one row,
 // ids v0 .. v0 + 31 (a multiple of 4 first), kStep words apart: the same scores in
 // the same order, in a loop over the counters' quads.  (Unrolled, with and without
 // bias, it made kernels of 200 KB, whose other parts then waited for instructions.)
+//
+// `bar`: a score that some id of the row has reached; only ids that reach it
+// count.  A quad is left out where its largest scaled logit x and the largest noise
+// do not, and, once its random words are there, where their noise does not: g(u) =
+// -log(-log u) < bar - x where 1 - u >= exp(x - bar), as -log u >= 1 - u.  The
+// margin is above all roundings: of x, of the difference and of the score (half an ulp
+// of each, 2^-24 of |bar| + |x|), of g (2e-6) and of __expf (3e-6 of it); 1 - u is
+// exact.  With the bar of all CTAs nearly every quad stops there, before its
+// logarithms (256 rows x 4096 x 128256: 271 -> 226 us, of which the sums take 172).
 template <int kStep>
-__device__ __forceinline__ Best scan_staged(const float* at, int64_t v0, int64_t V, const RowScan& s, Best best) {
+__device__ __forceinline__ Best scan_staged(const float* at, int64_t v0, int64_t V, const RowScan& s, Best best, float bar) {
   const unsigned lanes = __activemask();
+  bar = fmaxf(bar, best.z);
 #pragma unroll 1
   for (int q = 0; q < 8; ++q, at += 4 * kStep, v0 += 4) {
     float x[4];
@@ -252,12 +269,17 @@ __device__ __forceinline__ Best scan_staged(const float* at, int64_t v0, int64_t
       if (s.bias_row != nullptr && v0 + e < V) x[e] += __ldg(s.bias_row + v0 + e);
     }
     const float most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    if (!__any_sync(lanes, (s.greedy ? most : fmaf(most, s.inv_t, kGumbelMax)) > best.z)) continue;
+    if (!__any_sync(lanes, (s.greedy ? most : fmaf(most, s.inv_t, kGumbelMax)) >= bar)) continue;
     const uint4 w = noise_words(s.key, static_cast<uint32_t>(v0 >> 2), s.row, s.step_lo, s.step_hi);
+    const float scaled = most * s.inv_t, margin = fmaf(1e-6f, fabsf(bar) + fabsf(scaled), 1e-3f);
+    const uint32_t top = max(max(w.x, w.y), max(w.z, w.w)) >> 9;
+    const float rest = fmaf(static_cast<float>(0x7fffffu - top), 0x1p-23f, 0x1p-24f);     // 1 - u of the largest word
+    if (!__any_sync(lanes, s.greedy || !(rest >= __expf(scaled - bar + margin)))) continue;
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       keep_best(best, perturbed<false>(s, x[e], words[e], 0), static_cast<int32_t>(v0 + e));
+    bar = fmaxf(bar, best.z);
   }
   return best;
 }
@@ -732,6 +754,10 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
 #pragma unroll 1
         for (int c = 0; c < kPart; c += 32) {
           if (c0 + c >= a.c_rows) break;
+          float bar = -INFINITY;
+          if constexpr (kSample) {
+            if (scan_row + (kSwap ? c : 0) < a.p.B) bar = best_so_far(a.f.keys + scan_row + (kSwap ? c : 0));
+          }
 #pragma unroll
           for (int j = 0; j < (kPart < 32 ? kPart : 32); ++j) {
             constexpr int kNext = kPart > 32 ? 32 : 0;     // in acc, of the other 32 columns
@@ -755,8 +781,12 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
               scan.bias_row = a.p.bias != nullptr ? a.p.bias + row * a.p.bias_stride : nullptr;
               const int64_t v0 = kSwap ? l0 : c0 + c;
               const Best b = scan_staged<kSwap ? kPitch : 1>(stage + (kSwap ? lane : lane * kPitch), v0, a.p.V_local, scan,
-                                                             c == 0 ? best[0] : best[kScans - 1]);
+                                                             c == 0 ? best[0] : best[kScans - 1], bar);
               if (c == 0 || kScans == 1) best[0] = b; else best[kScans - 1] = b;
+              if (b.z > bar) {                             // for the other warps' scans
+                const unsigned long long key = pack_key(b.z, b.id);
+                if (!kSwap || atomicMax(keys + row, key) < key) atomicMax(a.f.keys + row, key);
+              }
             }
           } else if constexpr (kSwap) {
             // lanes lie along a row of the output

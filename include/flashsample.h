@@ -518,7 +518,8 @@ FS_API fs_status fs_quantize_fp8(const void* x, int x_type, int64_t rows, int64_
  * registers, in an order that the sizes fix; a_scale b_scale is formed first, in
  * fp32 (its overflow is an infinity).  out: fp32, bf16 or fp16, rows
  * out_row_stride >= n elements apart, rounded once.  Types of a and b may differ.
- * m, n <= 2^31 - 1024, k <= 2^24; k == 0 gives zeros.  out overlaps neither a nor b.
+ * m, n <= 2^31 - 1024, k <= 2^24; k == 0 gives zeros.  out overlaps neither a nor
+ * b, nor their scales (those are not checked).
  * For a linear layer in training: y = x8 W8^T, grad_x = g8 (W^T)8^T with
  * W^T from a transposing fs_quantize_fp8 (of 128 x 128 blocks: the same
  * values as W's), grad_W = (g^T)8 (x^T)8^T, both quantised along the tokens.

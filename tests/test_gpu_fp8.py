@@ -325,6 +325,36 @@ def test_samples(fs, torch_cuda, B, d, V, block, bias):
     assert fs.device_error() == 0
 
 
+@pytest.mark.parametrize("B", [4, 40, 130, 300])
+@pytest.mark.parametrize("what", ["flat", "peaked", "forbidden", "shifted"])
+def test_samples_of_extreme_rows(fs, torch_cuda, B, what):
+    """Rows whose scores are all noise, none, or far from zero: what is left
+    out early does not change a sample."""
+    from _helpers import compare
+    torch = torch_cuda
+    d, V = 128, 21001
+    h, W, _, _, logits = sample_case(torch, B, d, V)
+    rng = np.random.default_rng(B)
+    temp = np.array([1.0, 0.0, 0.1, 1e3, 0.5, 30.0], np.float32)[np.arange(B) % 6]
+    bias = np.zeros(V, np.float32)
+    if what == "flat":
+        h.scale.zero_()                                        # every logit 0: greedy takes the smallest id
+        logits = np.zeros_like(logits)
+    elif what == "peaked":
+        bias[rng.integers(0, V, 5)] = 25.0
+    elif what == "forbidden":
+        bias[:] = -np.inf
+        bias[rng.integers(0, V, 3)] = -4.0
+    else:
+        bias[:] = -60.0 + 40.0 * (rng.random(V) < 1e-3)
+    ids, mx = fs.sample_fp8(h.q, h.scale, W.q, W.scale, to_device(temp, torch), 99, 7, bias=to_device(bias, torch))
+    ref = sampler.sample_from_logits(logits + bias, temp, 99, 7, np.arange(B), np.arange(V))
+    compare(ids.cpu().numpy(), mx.cpu().numpy(), ref, what=f"8-bit head, {what} rows, B={B}")
+    if what == "flat":
+        assert bool((ids.cpu()[torch.from_numpy(temp) == 0] == 0).all())
+    assert fs.device_error() == 0
+
+
 def test_samples_of_a_large_head(fs, torch_cuda):
     """All SMs with several tiles each, over a vocabulary that ends inside one."""
     from _helpers import compare

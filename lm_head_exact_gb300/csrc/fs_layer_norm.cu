@@ -99,6 +99,8 @@ __device__ __forceinline__ float row_sum(float v, float* parts) {
   return warp_sum((threadIdx.x & 31) < (blockDim.x >> 5) ? parts[threadIdx.x & 31] : 0.0f);
 }
 
+constexpr int kRowsAhead = 608;            // that a block asks for: 4 for each SM of this GPU
+
 // A row on `threads` threads: thread t holds the groups of kV columns
 // i * threads + t.  kE elements a thread.
 template <typename T, typename W, int kV, int kE, bool kOneWarp, int kQuantType>
@@ -117,6 +119,10 @@ __global__ void __launch_bounds__(kOneWarp ? kSmallRow* kRowsPerBlock : 1024) no
   pdl_wait_then_launch();
   if (kOneWarp && row >= p.n) return;                    // (no block barrier follows)
   const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+  // (to L2 while this row is summed up: 16384 x 4096 57.0 -> 53.0 us; 304 rows ahead the same, 2432 55.3)
+  if constexpr (!kOneWarp && kV > 1) {
+    if (t == 0 && row + kRowsAhead < p.n) sm100::bulk_prefetch(x + kRowsAhead * p.x_stride, d * sizeof(T));
+  }
   if constexpr (kTops) {
     for (int i = t; i < (d + kQuantBlock - 1) / kQuantBlock; i += threads) tops[sub][i] = 0;
     if constexpr (kOneWarp) __syncwarp(); else __syncthreads();

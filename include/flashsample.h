@@ -488,6 +488,10 @@ FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, 
  * fs_sample_fp8 uses the sampling workspace of (device, stream);
  * fs_layer_norm_backward's comes from the caller as the training calls' does;
  * the others need none.  fs_workspace_reserve() makes all of them capturable.
+ * Their kernels always launch as programmatic dependents (fs_set_launch_overlap
+ * does not change them) and read and write nothing ahead of their wait.  What
+ * is said there of W holds for what these calls write, too: one whose output is
+ * the W of fs_sample or fs_sample_ex must not be the call right before it.
  * ------------------------------------------------------------------------ */
 
 /* 8-bit element types, beside FS_TYPE_F32, _BF16 and _F16. */

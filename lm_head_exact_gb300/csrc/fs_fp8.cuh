@@ -15,7 +15,11 @@ namespace fs {
 
 // Waits for what lies ahead in the stream, then lets the next kernel start: one
 // that reads weights before its own wait must not begin while a kernel ahead of
-// this one may still write them.
+// this one may still write them.  For kernels whose own results no such reader
+// takes: 8-bit matrices, samples.  One that writes a caller's matrix of 16- or
+// 32-bit elements waits only: it lets the next kernel start by its end, for
+// whatever follows may, before its wait, let one start that reads the matrix
+// as an LM head before its own.
 __device__ __forceinline__ void pdl_wait_then_launch() {
   pdl_wait();
   pdl_launch_dependents();

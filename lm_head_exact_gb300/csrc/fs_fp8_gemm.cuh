@@ -560,7 +560,7 @@ kernel(const __grid_constant__ CUtensorMap tmap_l, const __grid_constant__ CUten
     const uint32_t sempty0 = smem_u32(sempty_bar);
     const int n_k = k1 - k0, n_use = (n_k + kPer - 1) / kPer, n_fill = (n_k + kAhead - 1) / kAhead;
     pdl_wait();
-    if (warp == 0) pdl_launch_dependents();                // (see pdl_wait_then_launch; nothing else fits beside this block)
+    if (kSample && warp == 0) pdl_launch_dependents();     // (see pdl_wait_then_launch; nothing else fits beside this block)
     // Columns of a TMEM load, its registers, and the loads of a block.  In
     // fragments, load q holds lanes 16 (q % 2) .. of 32 columns from 32 (q / 2) on:
     // register i lies in row 16 (q % 2) + 8 (i / 2 % 2) + lane / 4 and column

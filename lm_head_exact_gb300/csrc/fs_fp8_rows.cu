@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) rows_kernel(const RowsArgs p) 
     for (int e = 0; e < 4; ++e) sum[e] = fmaf(d[e], xs[e & 1] * ws[e >> 1], sum[e]);
   };
   skip(warp);
-  pdl_wait_then_launch();
+  pdl_wait();
   int kb = warp;
 #pragma unroll 1
   for (; kb < whole; kb += kWarps * kDeep) {

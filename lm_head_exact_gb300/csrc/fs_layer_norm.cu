@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kOneWarp ? kSmallRow* kRowsPerBlock : 1024) no
   const int sub = kOneWarp ? threadIdx.x >> 5 : 0;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kOneWarp ? kRowsPerBlock : 1) + sub;
   const int d = static_cast<int>(p.d);
-  pdl_wait_then_launch();
+  if constexpr (kQuant) pdl_wait_then_launch(); else pdl_wait();
   if (kOneWarp && row >= p.n) return;                    // (no block barrier follows)
   const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
   // (to L2 while this row is summed up: 16384 x 4096 57.0 -> 53.0 us; 304 rows ahead the same, 2432 55.3)
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kOneWarp ? kSmallRow* kRowsPerBlock : 1024) no
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kOneWarp ? kRowsPerBlock : 1);
   const int d = static_cast<int>(p.d);
   const float inv_d = 1.0f / static_cast<float>(d);
-  pdl_wait_then_launch();
+  pdl_wait();
   if (kOneWarp && first >= p.n) return;                    // (no block barrier follows)
   const T* x = static_cast<const T*>(p.x) + first * p.x_stride;
   T* y = static_cast<T*>(p.y) + first * p.y_stride;
@@ -350,7 +350,8 @@ norm_grad_kernel(const NormGradProblem p) {
   const bool sums = p.gw != nullptr || p.gb != nullptr;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kOneWarp ? kRowsPerBlock : 1) + sub;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kOneWarp ? kRowsPerBlock : 1);
-  pdl_wait_then_launch();
+  pdl_wait();
+  if (sums) pdl_launch_dependents();                       // (norm_sum_kernel, which waits first)
   const T* x = static_cast<const T*>(p.x) + first * p.x_stride;
   const T* g = static_cast<const T*>(p.g) + first * p.g_stride;
   const int shift = kShift ? shift_of(x) : 0;
@@ -513,7 +514,8 @@ __global__ void __launch_bounds__(512) norm_grad_ring_kernel(const NormGradProbl
     sm100::fence_barrier_init();
   }
   __syncthreads();
-  pdl_wait_then_launch();
+  pdl_wait();
+  if (p.gw != nullptr || p.gb != nullptr) pdl_launch_dependents();     // (norm_sum_kernel, which waits first)
   auto fill = [&](int64_t row, int slot) {
     if (row >= p.n) return;
     uint8_t* at = rows + static_cast<size_t>(slot) * 2 * bytes;
@@ -626,7 +628,7 @@ __global__ void __launch_bounds__(32 * kSumSlices) norm_sum_kernel(const float* 
   __shared__ float sums[kSumSlices][33];
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;     // of [gw, gb]
   const int slice = threadIdx.x / 32;
-  pdl_wait_then_launch();
+  pdl_wait();
   float s = 0.0f;
   if (c < 2 * d) {
 #pragma unroll 4

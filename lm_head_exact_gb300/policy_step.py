@@ -87,7 +87,8 @@ def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef
     """Loss and gradients of one step on ``rollout`` under the head W.
     ``keep_logits`` spends 4 bytes per token and vocabulary row to form the
     logits once instead of twice.  Rows without a token (the sampler's -1, an
-    invalid temperature) take no part, whatever the rollout's mask says.
+    invalid temperature) take no part, whatever the rollout's mask says, and
+    their hidden states may hold anything.
 
     The gradients are not clipped here: the norm of the model's gradient is
     known after the body's backward pass only (clip_grad_norm over all
@@ -112,7 +113,11 @@ def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef
     grad_h, grad_W = fs.token_logprobs_backward(h, W, r.ids, r.temp, logp, lse, grad_logp, bias=r.bias, kept=kept)
     grad_weight = grad_bias = None
     if norm is not None:
-        grad_h, grad_weight, grad_bias = fs.layer_norm_backward(grad_h, r.h, norm.weight, mu, rstd,
+        # (rows that take no part may hold anything, NaN included, which their gradient of 0 would not keep out)
+        rest = ~mask
+        x, rstd = r.h.masked_fill(rest[:, None], 0.0), rstd.masked_fill(rest, 0.0)
+        mu = None if mu is None else mu.masked_fill(rest, 0.0)
+        grad_h, grad_weight, grad_bias = fs.layer_norm_backward(grad_h, x, norm.weight, mu, rstd,
                                                                 need_bias=norm.bias is not None, out=grad_h)
     grads = [g for g in (grad_h, grad_W, grad_weight, grad_bias) if g is not None]
     total = None if max_norm is None else fs.clip_grad_norm(grads, max_norm)

@@ -33,7 +33,7 @@ from . import binding as fs
 @dataclass
 class FinalNorm:
     """The model's last norm, between its hidden states and the head."""
-    weight: object          # [d] bf16 or fp32
+    weight: object          # [d] bf16 or fp32, or None: a norm without one
     bias: object = None     # [d] of weight's type
     eps: float = 1e-5
     rms: bool = False       # without the mean
@@ -78,7 +78,7 @@ class StepResult:
     grad_h: object          # bf16 [N, d]
     grad_W: object          # bf16 [V, d]
     logp: object            # fp32 [N]
-    grad_norm_weight: object = None   # [d], the final norm's, where there is one
+    grad_norm_weight: object = None   # [d], the final norm's, where there is one and it has a weight
     grad_norm_bias: object = None     # [d], where it has a bias
 
 
@@ -117,8 +117,8 @@ def policy_step(rollout, W, ref_logp=None, clip_low=0.2, clip_high=0.28, kl_coef
         rest = ~mask
         x, rstd = r.h.masked_fill(rest[:, None], 0.0), rstd.masked_fill(rest, 0.0)
         mu = None if mu is None else mu.masked_fill(rest, 0.0)
-        grad_h, grad_weight, grad_bias = fs.layer_norm_backward(grad_h, x, norm.weight, mu, rstd,
-                                                                need_bias=norm.bias is not None, out=grad_h)
+        need = dict(need_bias=norm.bias is not None, **({} if norm.weight is not None else {"need_weight": False}))
+        grad_h, grad_weight, grad_bias = fs.layer_norm_backward(grad_h, x, norm.weight, mu, rstd, out=grad_h, **need)
     grads = [g for g in (grad_h, grad_W, grad_weight, grad_bias) if g is not None]
     total = None if max_norm is None else fs.clip_grad_norm(grads, max_norm)
     return StepResult(stats, total, grad_h, grad_W, logp, grad_weight, grad_bias)

@@ -66,3 +66,13 @@ def test_rows_without_a_token_reach_no_gradient_of_the_norm(monkeypatch, fill, r
         if a is not None:
             assert bool(b.isfinite().all()) and torch.equal(a, b)
     assert bool((got.grad_h[[2, 5, 9, 11]] == 0).all())
+
+
+def test_a_norm_without_weight_has_no_gradient_of_one(monkeypatch):
+    h = torch.randn(12, 16, generator=torch.Generator().manual_seed(0))
+    got, plain = _step(monkeypatch, h, ps.FinalNorm(None), max_norm=1e-3)
+    assert got.grad_norm_weight is None and got.grad_norm_bias is None
+    assert ("layer_norm_backward", False) in plain.calls
+    assert len(plain.calls[-1][1]) == 2                        # what is clipped: grad_h and grad_W
+    total = torch.cat((got.grad_h.flatten(), got.grad_W.flatten()))
+    assert abs(float(total.norm()) - 1e-3) < 1e-5

@@ -485,6 +485,9 @@ FS_API fs_status fs_clip_grad_norm(const void* const* grads, void* const* outs, 
  * a row i is one row of q (block_rows 1) or 128 (block_rows 128).  q times its
  * scale is the value.  Rows of scales side by side (scale_row_stride 1) are
  * read fastest where block_rows is 1.  Widths need not be multiples of anything.
+ * What a call writes shares no memory with what it reads or writes besides
+ * (FS_ERR_INVALID_ARG), but where it says so.  Matrices whose rows lie equally
+ * far apart may lie side by side, a row behind a row.
  * fs_sample_fp8 uses the sampling workspace of (device, stream);
  * fs_layer_norm_backward's comes from the caller as the training calls' does;
  * the others need none.  fs_workspace_reserve() makes all of them capturable.
@@ -522,8 +525,7 @@ FS_API fs_status fs_quantize_fp8(const void* x, int x_type, int64_t rows, int64_
  * registers, in an order that the sizes fix; a_scale b_scale is formed first, in
  * fp32 (its overflow is an infinity).  out: fp32, bf16 or fp16, rows
  * out_row_stride >= n elements apart, rounded once.  Types of a and b may differ.
- * m, n <= 2^31 - 1024, k <= 2^24; k == 0 gives zeros.  out overlaps neither a nor
- * b, nor their scales (those are not checked).
+ * m, n <= 2^31 - 1024, k <= 2^24; k == 0 gives zeros.
  * For a linear layer in training: y = x8 W8^T, grad_x = g8 (W^T)8^T with
  * W^T from a transposing fs_quantize_fp8 (of 128 x 128 blocks: the same
  * values as W's), grad_W = (g^T)8 (x^T)8^T, both quantised along the tokens.
@@ -572,7 +574,7 @@ FS_API fs_status fs_layer_norm(const void* x, int x_type, int64_t n, int64_t d, 
  * xh = (x - mean) rstd and a = g weight,
  *   grad_x = rstd (a - mean(a) - xh mean(a xh))     (rms: without mean(a))
  *   grad_weight = sum over rows of g xh,  grad_bias = sum over rows of g
- * each nullable; grad_x [n, d] of x_type (it may be g itself), grad_weight and
+ * each nullable; grad_x [n, d] of x_type (it may be g or x itself), grad_weight and
  * grad_bias [d] of w_type.  mean and rstd are the forward call's (mean NULL
  * with rms).  Sums are held in fp32 and do not depend on the run.
  *   workspace: fs_layer_norm_backward_workspace_bytes(n, d) bytes, or NULL

@@ -937,7 +937,7 @@ def layer_norm_backward(grad, x, weight, mean, rstd, need_x=True, need_weight=Tr
     one that is not needed is None.  ``mean`` and ``rstd`` are the forward
     call's; a ``mean`` of None says that it was called with ``rms``.
     ``weight_dtype``: the type of the two sums where weight is None (fp32).
-    ``out``: the tensor for grad_x, ``grad`` itself included."""
+    ``out``: the tensor for grad_x, ``grad`` or x itself included."""
     torch = _torch()
     x_ptr, kind, n, d, x_stride, w, _, w_kind = _norm_args(x, weight, None)
     g_ptr, _, _, _, g_stride = _rows(grad, "grad", (kind,), (n, d))

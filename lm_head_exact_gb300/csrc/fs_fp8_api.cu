@@ -2,6 +2,7 @@
 // and launches.  Contracts: include/flashsample.h.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 
 #include "flashsample.h"
 #include "fs_api_util.h"
@@ -26,8 +27,9 @@ fs_status check_rows(int64_t rows, int64_t cols, int64_t stride, const char* nam
   return FS_OK;
 }
 
-fs_status check_fp8(const void* q, int type, int64_t rows, int64_t cols, int64_t stride, const float* scale,
-                    int64_t s_row, int64_t s_col, int block_rows, const char* name) {
+// An 8-bit matrix but for its addresses, and those.
+fs_status check_fp8_form(int type, int64_t rows, int64_t cols, int64_t stride, int64_t s_row, int64_t s_col, int block_rows,
+                         const char* name) {
   if (!is_fp8(type)) return api_fail(FS_ERR_INVALID_ARG, "%s: type %d is not an 8-bit one", name, type);
   if (block_rows != 1 && block_rows != kQuantBlock)
     return api_fail(FS_ERR_INVALID_ARG, "%s: blocks of %d rows; 1 or 128", name, block_rows);
@@ -36,19 +38,74 @@ fs_status check_fp8(const void* q, int type, int64_t rows, int64_t cols, int64_t
   if (stride % 16 != 0) return api_fail(FS_ERR_UNSUPPORTED, "%s: a row stride of %lld bytes, not a multiple of 16", name, (long long)stride);
   if (s_row < 0 || s_col < 0 || s_row >= kMaxStride || s_col >= kMaxStride)
     return api_fail(FS_ERR_INVALID_ARG, "%s: strides of the scales must be >= 0", name);
+  return FS_OK;
+}
+
+fs_status check_fp8_arrays(const void* q, const float* scale, int64_t rows, int64_t cols, const char* name) {
+  if (rows == 0 || cols == 0) return FS_OK;
   FS_API_TRY(api_check_array(q, 16, name));
   return api_check_array(scale, 4, name);
 }
 
-// Bytes from the first element of [rows, cols] to behind the last.
-size_t span_of(int64_t rows, int64_t cols, int64_t stride, size_t width) {
-  return rows == 0 || cols == 0 ? 0 : (static_cast<size_t>(rows - 1) * stride + cols) * width;
+fs_status check_fp8(const void* q, int type, int64_t rows, int64_t cols, int64_t stride, const float* scale,
+                    int64_t s_row, int64_t s_col, int block_rows, const char* name) {
+  FS_API_TRY(check_fp8_form(type, rows, cols, stride, s_row, s_col, block_rows, name));
+  return check_fp8_arrays(q, scale, rows, cols, name);
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const char* x = static_cast<const char*>(a);
-  const char* y = static_cast<const char*>(b);
-  return x != nullptr && y != nullptr && na > 0 && nb > 0 && x < y + nb && y < x + na;
+// Memory of a matrix: rows of `width` bytes, `pitch` bytes apart (at NULL: none).
+// Sums of strides pass 64 bits before they are known to be memory.
+using Wide = __int128;
+struct Region {
+  const void* at;
+  int64_t rows;
+  Wide width, pitch;
+  const char* name;
+  bool in_place = false;      // of an output and an input: they may be the same memory
+};
+
+Region matrix(const void* at, int64_t rows, int64_t cols, int64_t stride, size_t width, const char* name, bool in_place = false) {
+  return Region{at, rows, Wide(cols) * width, Wide(stride) * width, name, in_place};
+}
+Region vector(const void* at, int64_t n, size_t width, const char* name) { return matrix(at, 1, n, n, width, name); }
+// The scales of an 8-bit [rows, cols], by rows or by columns, whichever lie further apart.
+Region scales(const float* at, int64_t rows, int64_t cols, int64_t s_row, int64_t s_col, int block_rows, const char* name) {
+  const int64_t r = (rows + block_rows - 1) / block_rows, c = quant_blocks(cols);
+  if (r == 0 || c == 0) return Region{nullptr, 0, 0, 0, name};
+  return s_row >= s_col ? Region{at, r, (Wide(c - 1) * s_col + 1) * 4, Wide(s_row) * 4, name}
+                        : Region{at, c, (Wide(r - 1) * s_row + 1) * 4, Wide(s_col) * 4, name};
+}
+
+Wide floor_div(Wide a, Wide b) { return a / b - (a % b < 0 ? 1 : 0); }      // b > 0
+
+// Whether two matrices share a byte.  Rows of one pitch may lie side by side;
+// where pitches differ, matrices between each other's ends count as sharing.
+bool overlap(const Region& a, const Region& b) {
+  if (a.at == nullptr || b.at == nullptr || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const Wide apart = Wide(reinterpret_cast<uintptr_t>(b.at)) - Wide(reinterpret_cast<uintptr_t>(a.at));
+  if (apart >= (a.rows - 1) * a.pitch + a.width || -apart >= (b.rows - 1) * b.pitch + b.width) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  const Wide pitch = a.rows == 1 ? b.pitch : a.pitch;
+  if (pitch <= 0 || (b.rows > 1 && b.pitch != pitch)) return true;
+  // row i of a and row j of b meet where (i - j) pitch lies in (apart - a.width, apart + b.width)
+  const Wide least = std::max<Wide>(floor_div(apart - a.width, pitch) + 1, 1 - b.rows);
+  const Wide most = std::min<Wide>(floor_div(apart + b.width - 1, pitch), a.rows - 1);
+  return least <= most;
+}
+
+// Outputs share no memory with one another, and none with inputs but where both
+// may be the same matrix and are.
+fs_status check_apart(std::initializer_list<Region> outputs, std::initializer_list<Region> inputs) {
+  for (const Region* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Region* other = outputs.begin(); other != o; ++other)
+      if (overlap(*o, *other)) return api_fail(FS_ERR_INVALID_ARG, "%s overlaps %s", o->name, other->name);
+    for (const Region& i : inputs) {
+      const bool same = o->in_place && i.in_place && o->at == i.at && (o->rows == 1 || o->pitch == i.pitch);
+      if (!same && overlap(*o, i))
+        return api_fail(FS_ERR_INVALID_ARG, "%s overlaps %s%s", o->name, i.name, o->in_place && i.in_place ? " without being it" : "");
+    }
+  }
+  return FS_OK;
 }
 
 // No C++ exception leaves a C entry (the library's maps can run out of memory).
@@ -80,11 +137,13 @@ fs_status fs_quantize_fp8(const void* x, int x_type, int64_t rows, int64_t cols,
   if (transpose != 0 && transpose != 1) return api_fail(FS_ERR_INVALID_ARG, "transpose must be 0 or 1");
   FS_API_TRY(check_rows(rows, cols, x_row_stride, "x"));
   const int64_t R = transpose ? cols : rows, C = transpose ? rows : cols;
-  FS_API_TRY(check_fp8(q, q_type, R, C, q_row_stride, scale, scale_row_stride, scale_col_stride, block_rows, "q"));
+  FS_API_TRY(check_fp8_form(q_type, R, C, q_row_stride, scale_row_stride, scale_col_stride, block_rows, "q"));
   if (rows == 0 || cols == 0) return FS_OK;
+  FS_API_TRY(check_apart({matrix(q, R, C, q_row_stride, 1, "q"),
+                          scales(scale, R, C, scale_row_stride, scale_col_stride, block_rows, "scale")},
+                         {matrix(x, rows, cols, x_row_stride, width_of(x_type), "x")}));
+  FS_API_TRY(check_fp8_arrays(q, scale, R, C, "q"));
   FS_API_TRY(api_check_array(x, width_of(x_type), "x"));
-  if (overlap(q, span_of(R, C, q_row_stride, 1), x, span_of(rows, cols, x_row_stride, width_of(x_type))))
-    return api_fail(FS_ERR_INVALID_ARG, "q overlaps x");
   FS_API_TRY(api_check_launch());
   const QuantProblem p{x, x_type, rows, cols, x_row_stride, transpose == 1, block_rows, q_type, q, q_row_stride, scale,
                        scale_row_stride, scale_col_stride};
@@ -103,18 +162,21 @@ fs_status fs_fp8_matmul(const void* a, int a_type, int64_t a_row_stride, const f
     return api_fail(FS_ERR_UNSUPPORTED, "m and n must be <= %lld, k <= %lld", (long long)kMaxSize, (long long)kMaxDepth);
   if (!is_wide(out_type)) return api_fail(FS_ERR_INVALID_ARG, "out: unknown type %d", out_type);
   FS_API_TRY(check_rows(m, n, out_row_stride, "out"));
-  FS_API_TRY(check_fp8(a, a_type, m, k, a_row_stride, a_scale, a_scale_row_stride, a_scale_col_stride, 1, "a"));
-  FS_API_TRY(check_fp8(b, b_type, n, k, b_row_stride, b_scale, b_scale_row_stride, b_scale_col_stride, b_block_rows, "b"));
-  if (m == 0 || n == 0) return FS_OK;
+  FS_API_TRY(check_fp8_form(a_type, m, k, a_row_stride, a_scale_row_stride, a_scale_col_stride, 1, "a"));
+  FS_API_TRY(check_fp8_form(b_type, n, k, b_row_stride, b_scale_row_stride, b_scale_col_stride, b_block_rows, "b"));
   const size_t width = width_of(out_type);
+  FS_API_TRY(check_apart({matrix(out, m, n, out_row_stride, width, "out")},
+                         {matrix(a, m, k, a_row_stride, 1, "a"), matrix(b, n, k, b_row_stride, 1, "b"),
+                          scales(a_scale, m, k, a_scale_row_stride, a_scale_col_stride, 1, "a_scale"),
+                          scales(b_scale, n, k, b_scale_row_stride, b_scale_col_stride, b_block_rows, "b_scale")}));
+  FS_API_TRY(check_fp8_arrays(a, a_scale, m, k, "a"));
+  FS_API_TRY(check_fp8_arrays(b, b_scale, n, k, "b"));
+  if (m == 0 || n == 0) return FS_OK;
   FS_API_TRY(api_check_array(out, width, "out"));
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   if (k == 0)
     return api_launched(m == 1 ? cudaMemsetAsync(out, 0, n * width, stream)
                                : cudaMemset2DAsync(out, out_row_stride * width, 0, n * width, m, stream), "zeroing out");
-  const size_t so = span_of(m, n, out_row_stride, width);
-  if (overlap(out, so, a, span_of(m, k, a_row_stride, 1)) || overlap(out, so, b, span_of(n, k, b_row_stride, 1)))
-    return api_fail(FS_ERR_INVALID_ARG, "out overlaps a or b");
   int* err = nullptr;
   FS_API_TRY(api_error_word(&err, stream));
   FS_API_TRY(api_check_launch());
@@ -193,24 +255,28 @@ fs_status fs_layer_norm(const void* x, int x_type, int64_t n, int64_t d, int64_t
   FS_API_TRY(check_rows(n, d, x_row_stride, "x"));
   if (n == 0) return FS_OK;
   if ((y == nullptr) == (q == nullptr)) return api_fail(FS_ERR_INVALID_ARG, "one of y and q");
+  if (y != nullptr)
+    FS_API_TRY(check_rows(n, d, y_row_stride, "y"));
+  else
+    FS_API_TRY(check_fp8_form(q_type, n, d, q_row_stride, scale_row_stride, scale_col_stride, 1, "q"));
+  const size_t width = width_of(x_type), w_width = width_of(w_type);
+  if (rms == 1) mean = nullptr;             // not written
+  FS_API_TRY(check_apart({y != nullptr ? matrix(y, n, d, y_row_stride, width, "y", true) : matrix(q, n, d, q_row_stride, 1, "q"),
+                          y != nullptr ? Region{} : scales(scale, n, d, scale_row_stride, scale_col_stride, 1, "scale"),
+                          vector(mean, n, 4, "mean"), vector(rstd, n, 4, "rstd")},
+                         {matrix(x, n, d, x_row_stride, width, "x", true), vector(weight, d, w_width, "weight"),
+                          vector(bias, d, w_width, "bias")}));
   FS_API_TRY(check_norm(n, d, x_type, weight, bias, w_type, rms));
-  const size_t width = width_of(x_type);
   FS_API_TRY(api_check_array(x, width, "x"));
   if (mean != nullptr) FS_API_TRY(api_check_array(mean, 4, "mean"));
   if (rstd != nullptr) FS_API_TRY(api_check_array(rstd, 4, "rstd"));
-  const size_t sx = span_of(n, d, x_row_stride, width);
-  if (y != nullptr) {
-    FS_API_TRY(check_rows(n, d, y_row_stride, "y"));
+  if (y != nullptr)
     FS_API_TRY(api_check_array(y, width, "y"));
-    if (!(y == x && y_row_stride == x_row_stride) && overlap(y, span_of(n, d, y_row_stride, width), x, sx))
-      return api_fail(FS_ERR_INVALID_ARG, "y overlaps x without being it");
-  } else {
-    FS_API_TRY(check_fp8(q, q_type, n, d, q_row_stride, scale, scale_row_stride, scale_col_stride, 1, "q"));
-    if (overlap(q, span_of(n, d, q_row_stride, 1), x, sx)) return api_fail(FS_ERR_INVALID_ARG, "q overlaps x");
-  }
+  else
+    FS_API_TRY(check_fp8_arrays(q, scale, n, d, "q"));
   FS_API_TRY(api_check_launch());
   const NormProblem p{x, x_type, n, d, x_row_stride, weight, bias, w_type, rms == 1, static_cast<float>(eps), y, y_row_stride,
-                      rms == 1 ? nullptr : mean, rstd, q, q_type, q_row_stride, scale, scale_row_stride, scale_col_stride};
+                      mean, rstd, q, q_type, q_row_stride, scale, scale_row_stride, scale_col_stride};
   return api_launched(launch_norm(p, static_cast<cudaStream_t>(stream)), "layer norm launch");
   });
 }
@@ -230,10 +296,20 @@ fs_status fs_layer_norm_backward(const void* g, int64_t g_row_stride, const void
   FS_API_TRY(check_rows(n, d, x_row_stride, "x"));
   const size_t width = width_of(x_type), w_width = width_of(w_type);
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (grad_x != nullptr && n > 0) FS_API_TRY(check_rows(n, d, grad_x_row_stride, "grad_x"));
+  const bool sums = grad_weight != nullptr || grad_bias != nullptr;
+  const size_t need = sums ? fs_layer_norm_backward_workspace_bytes(n, d) : 0;
+  const bool own_block = workspace == nullptr && need <= FS_SMALL_WORKSPACE;
+  if (sums && !own_block && workspace_bytes < need)
+    return api_fail(FS_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  FS_API_TRY(check_apart({matrix(n > 0 ? grad_x : nullptr, n, d, grad_x_row_stride, width, "grad_x", true),
+                          vector(grad_weight, d, w_width, "grad_weight"), vector(grad_bias, d, w_width, "grad_bias"),
+                          vector(sums ? workspace : nullptr, static_cast<int64_t>(need), 1, "workspace")},
+                         {matrix(g, n, d, g_row_stride, width, "g", true), matrix(x, n, d, x_row_stride, width, "x", true),
+                          vector(n > 0 ? weight : nullptr, d, w_width, "weight"),
+                          vector(rms == 0 ? mean : nullptr, n, 4, "mean"), vector(rstd, n, 4, "rstd")}));
   if (grad_weight != nullptr) FS_API_TRY(api_check_array(grad_weight, w_width, "grad_weight"));
   if (grad_bias != nullptr) FS_API_TRY(api_check_array(grad_bias, w_width, "grad_bias"));
-  if (overlap(grad_weight, d * w_width, grad_bias, d * w_width))
-    return api_fail(FS_ERR_INVALID_ARG, "grad_weight and grad_bias overlap");
   if (n == 0) {                             // sums over no rows
     if (grad_weight != nullptr)
       FS_API_TRY(api_launched(cudaMemsetAsync(grad_weight, 0, d * w_width, stream), "zeroing grad_weight"));
@@ -246,34 +322,15 @@ fs_status fs_layer_norm_backward(const void* g, int64_t g_row_stride, const void
   FS_API_TRY(api_check_array(x, width, "x"));
   FS_API_TRY(api_check_array(rstd, 4, "rstd"));
   if (rms == 0) FS_API_TRY(api_check_array(mean, 4, "mean"));
-  const size_t sg = span_of(n, d, g_row_stride, width), sx = span_of(n, d, x_row_stride, width);
-  if (grad_x != nullptr) {
-    FS_API_TRY(check_rows(n, d, grad_x_row_stride, "grad_x"));
-    FS_API_TRY(api_check_array(grad_x, width, "grad_x"));
-    const size_t so = span_of(n, d, grad_x_row_stride, width);
-    const bool is_g = grad_x == g && grad_x_row_stride == g_row_stride, is_x = grad_x == x && grad_x_row_stride == x_row_stride;
-    if ((!is_g && overlap(grad_x, so, g, sg)) || (!is_x && overlap(grad_x, so, x, sx)) ||
-        overlap(grad_x, so, weight, d * w_width) || overlap(grad_x, so, grad_weight, d * w_width) ||
-        overlap(grad_x, so, grad_bias, d * w_width))
-      return api_fail(FS_ERR_INVALID_ARG, "grad_x overlaps another tensor without being g or x");
-  }
-  for (void* sum : {grad_weight, grad_bias})
-    if (overlap(sum, d * w_width, g, sg) || overlap(sum, d * w_width, x, sx) || overlap(sum, d * w_width, weight, d * w_width))
-      return api_fail(FS_ERR_INVALID_ARG, "grad_weight and grad_bias must not overlap g, x or weight");
-  const bool sums = grad_weight != nullptr || grad_bias != nullptr;
+  if (grad_x != nullptr) FS_API_TRY(api_check_array(grad_x, width, "grad_x"));
   if (!sums && grad_x == nullptr) return FS_OK;
   const CallLock lock(stream);
-  if (sums) {
-    const size_t need = fs_layer_norm_backward_workspace_bytes(n, d);
-    if (workspace == nullptr && need <= FS_SMALL_WORKSPACE) {
-      TrainScratch* scratch = nullptr;
-      FS_API_TRY(api_train_scratch(stream, &scratch));
-      workspace = scratch->small;
-    } else {
-      if (workspace_bytes < need)
-        return api_fail(FS_ERR_INVALID_ARG, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
-      FS_API_TRY(api_check_array(workspace, 16, "workspace"));
-    }
+  if (own_block && sums) {
+    TrainScratch* scratch = nullptr;
+    FS_API_TRY(api_train_scratch(stream, &scratch));
+    workspace = scratch->small;
+  } else if (sums) {
+    FS_API_TRY(api_check_array(workspace, 16, "workspace"));
   }
   int* err = nullptr;
   FS_API_TRY(api_error_word(&err, stream));

@@ -539,6 +539,7 @@ __global__ void __launch_bounds__(512) norm_grad_ring_kernel(const NormGradProbl
   }
   int turn = 0, slot = 0;
   uint32_t phase = 0;
+  bool live = true;
   float next_mean = p.rms ? 0.0f : p.mean[blockIdx.x], next_rstd = p.rstd[blockIdx.x];
 #pragma unroll 1
   for (int64_t row = blockIdx.x; row < p.n; row += step) {
@@ -547,9 +548,17 @@ __global__ void __launch_bounds__(512) norm_grad_ring_kernel(const NormGradProbl
       next_mean = p.rms ? 0.0f : p.mean[row + step];
       next_rstd = p.rstd[row + step];
     }
-    // (a wait that gives up leaves the error word set; the block goes on with
-    // whatever lies there, so that its barriers stay whole)
-    sm100::mbar_wait(&full[slot], phase, p.err, &abort_flag);
+    // (a wait that gives up leaves the error word set; the thread goes on without
+    // further waits, on whatever lies there, so that the block's barriers stay
+    // whole, and thread 0 asks for no more rows, once those on their way have landed)
+    if (live && !sm100::mbar_wait(&full[slot], phase, p.err, &abort_flag)) {
+      live = false;
+      volatile int no_abort = 0;
+      for (int i = 0, at = slot, of = phase; t == 0 && i < ring && row + i * step < p.n; ++i) {
+        sm100::mbar_wait(&full[at], of, p.err, &no_abort);
+        if (++at == ring) { at = 0; of ^= 1; }
+      }
+    }
     const T* x = reinterpret_cast<const T*>(rows + static_cast<size_t>(slot) * 2 * bytes);
     const T* g = x + d;
     float xh[kN][kV], a[kN][kV];
@@ -585,7 +594,7 @@ __global__ void __launch_bounds__(512) norm_grad_ring_kernel(const NormGradProbl
       parts[turn][1][t >> 5] = sum_ax;
     }
     __syncthreads();
-    if (t == 0) fill(row + ring * step, slot);
+    if (t == 0 && live) fill(row + ring * step, slot);
     if (++slot == ring) { slot = 0; phase ^= 1; }
     if (p.gx == nullptr) continue;
     const bool mine = (t & 31) < (threads >> 5);

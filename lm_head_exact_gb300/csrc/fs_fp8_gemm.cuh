@@ -40,6 +40,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "fs_epilogue.cuh"
@@ -903,10 +904,15 @@ cudaError_t launch(Args a, const Fp8Matrix& ma, const Fp8Matrix& mb, int64_t m, 
   if (e == cudaSuccess) e = raise_smem_limit<fn>(dev, S::kSmem);
   if (e == cudaSuccess) {
     // a warpgroup's rise would wait for ever in a kernel compiled with fewer
-    static const int regs = [] {
+    // (only an answer is kept: a query that failed is made again by the next call)
+    static std::atomic<int> known{0};
+    int regs = known.load(std::memory_order_relaxed);
+    if (regs == 0) {
       cudaFuncAttributes attr = {};
-      return cudaFuncGetAttributes(&attr, fn) == cudaSuccess ? attr.numRegs : 0;
-    }();
+      e = cudaFuncGetAttributes(&attr, fn);
+      if (e != cudaSuccess) return e;
+      known.store(regs = attr.numRegs, std::memory_order_relaxed);
+    }
     if (regs != S::kLaunchRegs) return cudaErrorInvalidDeviceFunction;
   }
   if (e != cudaSuccess) return e;

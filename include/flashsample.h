@@ -540,10 +540,11 @@ FS_API fs_status fs_fp8_matmul(const void* a, int a_type, int64_t a_row_stride, 
  * fs_sample_ex with h [B, d] and the head W [V, d] in 8 bits, both
  * FS_TYPE_E4M3: h quantised by rows (block_rows 1; fs_quantize_fp8 or
  * fs_layer_norm), W by rows or in blocks of 128 x 128 (W_block_rows).  The
- * same noise, temperatures, bias, ties and outputs as fs_sample_ex, over the
- * logits that fs_fp8_matmul forms; reads half the bytes of a bf16 head.
- * d <= 2^24, B and V <= 2^31 - 1024.  A row's samples do not depend on the
- * batch beyond the order in which sizes have its products summed.
+ * same noise, temperatures, bias, ties and outputs as fs_sample_ex, over
+ * logits that are fs_fp8_matmul's in fp32 but for the order in which blocks of
+ * 128 are added (small products take a kernel of their own); reads half the
+ * bytes of a bf16 head.  d <= 2^24, B and V <= 2^31 - 1024.  A row's samples do not
+ * depend on the batch beyond the order in which sizes have its products summed.
  */
 FS_API fs_status fs_sample_fp8(const void* h, int64_t h_row_stride, const float* h_scale, int64_t h_scale_row_stride,
                                int64_t h_scale_col_stride, const void* W, int64_t W_row_stride, const float* W_scale,
@@ -562,6 +563,8 @@ FS_API fs_status fs_sample_fp8(const void* h, int64_t h_row_stride, const float*
  *   mean, rstd (nullable) [n] fp32, for the backward pass; mean is not written
  *     with rms.
  *   1 <= d <= 32768, n < 2^31, eps >= 0.
+ * Statistics are taken in fp32: rows whose squares (about the mean) sum beyond
+ * its range have rstd 0.
  */
 FS_API fs_status fs_layer_norm(const void* x, int x_type, int64_t n, int64_t d, int64_t x_row_stride,
                                const void* weight, const void* bias, int w_type, int rms, double eps, void* y,
@@ -576,7 +579,8 @@ FS_API fs_status fs_layer_norm(const void* x, int x_type, int64_t n, int64_t d, 
  *   grad_weight = sum over rows of g xh,  grad_bias = sum over rows of g
  * each nullable; grad_x [n, d] of x_type (it may be g or x itself), grad_weight and
  * grad_bias [d] of w_type.  mean and rstd are the forward call's (mean NULL
- * with rms).  Sums are held in fp32 and do not depend on the run.
+ * with rms).  Sums are held in fp32 and do not depend on the run; the two over the
+ * rows are off by up to (n / 304 + 43) 2^-24 of the sum of their terms' magnitudes.
  *   workspace: fs_layer_norm_backward_workspace_bytes(n, d) bytes, or NULL
  *     where FS_SMALL_WORKSPACE suffices or no sums are wanted.
  */

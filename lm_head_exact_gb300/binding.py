@@ -825,7 +825,9 @@ def quantize_fp8(x, block_rows=1, dtype=None, transpose=False, out=None, stream=
 def fp8_matmul(a, a_scale, b, b_scale, out_dtype=None, out=None, stream=None):
     """a bᵀ of two 8-bit matrices: a [m, k] quantised by rows, b [n, k] by rows
     or in blocks of 128 x 128 (told by the shape of its scales).  Returns
-    [m, n] of ``out_dtype`` (bf16 by default; fp32 or fp16), or writes ``out``."""
+    [m, n] of ``out_dtype`` (bf16 by default; fp32 or fp16), or writes ``out``.
+    (A result that becomes the W of ``sample``: some other work goes between
+    the two calls, for ``sample`` reads W ahead, see fs_set_launch_overlap.)"""
     a_ptr, a_kind, m, k, a_stride = _fp8_rows(a, "a", _FP8)
     b_ptr, b_kind, n, k2, b_stride = _fp8_rows(b, "b", _FP8)
     if k != k2:
@@ -896,7 +898,8 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, out=None, stream=
     ``weight`` and ``bias`` [d]: fp32 or x's type, or None.  Returns (y, mean,
     rstd): y in x's type, the statistics fp32 [n] for ``layer_norm_backward``
     (mean is None with ``rms``).  ``out``: the tensor to write, x itself
-    included.  d <= 32768."""
+    included.  d <= 32768.  (A result that becomes the W of ``sample``: as with
+    ``fp8_matmul``.)"""
     torch = _torch()
     ptr, kind, n, d, stride, w, b, w_kind = _norm_args(x, weight, bias)
     device = x.device

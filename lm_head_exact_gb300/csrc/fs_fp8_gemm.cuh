@@ -22,9 +22,10 @@
 // in registers, to nearest.)
 //
 // What bounds it beyond few rows is the way of the sums through the epilogue, not
-// the MMAs: of a lane quarter's port and of its scheduler, loading a column's sums
-// from TMEM takes 2 clocks and adding them up 2 more, and what hands a buffer over
-// (barriers take 100 clocks to look at) some 300 a block.  kWide and kPair
+// the MMAs (a third of the cycles): by the times of the forms below, loading a
+// column's sums of a lane quarter from TMEM takes 2 clocks and adding them up 2 more, and
+// what hands a buffer over (barriers take 100 clocks to look at) some 300 a block, one
+// after another; that one of these units is full is not shown.  kWide and kPair
 // therefore take 192 columns, by twelve warps of a lane quarter and 64 columns (1000
 // clocks a block; 256 columns by eight warps 1400, 128 by eight 800); kThin eight warps,
 // with registers for two blocks' sums, so that one is loaded while the other is

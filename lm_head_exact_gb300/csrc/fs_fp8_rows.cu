@@ -66,7 +66,8 @@ __device__ __forceinline__ void mma_rows(float (&d)[4], uint32_t w0, uint32_t w1
 #undef FS_MMA_ROWS
 }
 
-__device__ __forceinline__ uint4 load_once(const uint8_t* p) {       // b, which no other block of threads reads
+// b: what further groups of tokens read again comes from L2.
+__device__ __forceinline__ uint4 load_once(const uint8_t* p) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)

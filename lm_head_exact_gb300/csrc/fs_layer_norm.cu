@@ -3,11 +3,19 @@
 //   y = xh w + b,  xh = (x - mean) rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
 //   a = g w,  gx = rstd (a - mean(a) - xh mean(a xh)),  gw = sum g xh,  gb = sum g
 //
-// rms: without the mean (and without mean(a)).  Both passes are bound by
-// memory: a row is read once and stays in registers, where its statistics are
-// taken in two passes (the mean, then the squares about it, which cancel
+// rms: without the mean (and without mean(a)).  Both passes are to be bound by
+// memory: a row is read once and held by its threads, which take its statistics
+// in two passes (the mean, then the squares about it, which cancel
 // nothing), in fp32.  The forward pass can write the result in 8 bits with a
 // scale for each 128 columns instead, from the fp32 values.
+//
+// Rows on 16-byte boundaries stay in registers (but for up to 72 bytes a thread),
+// in the backward pass up to 8192 columns.  Other forms spill, bytes a thread: shifted
+// rows of more than some 500 columns 270 to 430, single elements over a block 460 to
+// 710, the backward pass of more than 8192 columns 1600 to 2450.  us, and what the
+// bytes take:
+//   16384 x 4097 forward 112, 40; into 8 bits 335, 30; backward 169, 59
+//   4096 x 12288 backward 339, 45; 4096 x 16384 520, 59
 #include <algorithm>
 
 #include "fs_fp8.cuh"
@@ -632,7 +640,7 @@ __global__ void __launch_bounds__(512) norm_grad_ring_kernel(const NormGradProbl
   }
 }
 
-// Sums over the blocks' partials: 32 columns a block of threads, 8 slices of the
+// Sums over the blocks' partials: 32 columns a block of threads, 16 slices of the
 // partials, joined in the order of the slices.
 constexpr int kSumSlices = 16;
 
@@ -661,8 +669,8 @@ __global__ void __launch_bounds__(32 * kSumSlices) norm_sum_kernel(const float* 
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
-// Rows of up to 1024 columns are one warp's, of which a thread takes 8, 16 or
-// 32 elements; wider ones a block's.
+// Rows of up to 1024 columns (256 where there are up to 512 of them) are one
+// warp's, wider ones a block's; a thread takes 8 or 32 elements.
 template <typename T, typename W, int kV, int kE, bool kOneWarp>
 cudaError_t launch_norm_as(const NormProblem& p, int threads, cudaStream_t stream) {
   const int64_t grid = kOneWarp ? (p.n + kRowsPerBlock - 1) / kRowsPerBlock : p.n;
